@@ -496,6 +496,133 @@ qlin_status qlin_quaff_backward(const uint16_t* dy, int64_t M, int64_t N, int64_
 qlin_status qlin_outlier_comp(const uint16_t* xO, const float* sa, int32_t nO, const void* WO,
                               int64_t M, int64_t N, uint16_t* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Key/value cache of a decoding model (OffQ, core contributions: the W4A4KV4
+ * scheme, whose linear half is above): appending rows, attention of one new
+ * token, eviction by accumulated attention weight
+ * --------------------------------------------------------------------- */
+
+/*
+ * A pool of pages in device memory, described by a host struct that the caller
+ * keeps; the library reads it during a call only.  Page p holds `page` slots of
+ * every kv head, and every array is indexed [p][head][line]:
+ *   k, v          bits == 16: fp16 [pages x kv_heads x page x head_dim];
+ *                 else uint8 codes [.. x head_dim * bits / 8] (int4: two codes
+ *                 per byte, low nibble = even channel)
+ *   kmeta, vmeta  fp16 [pages x kv_heads x page x 2]: (step, lo) of each row,
+ *                 which stands for lo + step * code (step >= 0); NULL when
+ *                 bits == 16
+ *   signs         int8 [128] or NULL: with it (head_dim 128, bits < 16) stored K
+ *                 rows are (k * d) H_128 as in qlin_hadamard_offset, so that an
+ *                 outlier channel becomes an offset that lo absorbs; queries
+ *                 are turned the same way inside qlin_attn_decode.  V is not
+ *                 turned: its rotation folds into the weights around it.
+ * A block table int32 [B x max_pages] gives each sequence its pages: slot i of
+ * row b is line i % page of page table[b, i / page].  Slots whose table entry
+ * is outside [0, pages) do not exist: they are not written, have no weight in
+ * the attention, and do not move.  mass (fp32) and pos (int32), both
+ * [B x kv_heads x ld], hold each slot's accumulated attention weight and the
+ * position of its token; a caller who never evicts needs neither.
+ */
+typedef struct qlin_kv_cache {
+  void* k;
+  void* v;
+  uint16_t* kmeta;
+  uint16_t* vmeta;
+  const int8_t* signs;
+  int64_t pages;
+  int32_t page;     /* slots per page: a power of two from 16 to 1024 */
+  int32_t kv_heads; /* 1 .. 65535 */
+  int32_t head_dim; /* 64, 128 or 256 */
+  int32_t bits;     /* 16, 8 or 4 */
+} qlin_kv_cache;
+
+/*
+ * qlin_kv_append -- store the K and V rows of T tokens (OffQ, methodology:
+ * standard uniform asymmetric quantization per row, after the Hadamard when
+ * `signs` is given).  bits == 16 copies.  Otherwise, per row, in fp32 with one
+ * rounding per operation, t the row (turned by a butterfly of spans
+ * 1, 2, .., 64 for K with signs), qmax = 2^bits - 1:
+ *   lo = fp16(min t), step = fp16((max t - lo) * fp32(1 / qmax)),
+ *   code = clamp(rint((t - lo) * (1 / step)), 0, qmax)   (0 if step == 0)
+ * A row that is not finite reads back as not finite.
+ *   k, v      fp16 [T x kv_heads x head_dim], ld_k and ld_v elements between
+ *             tokens (a multiple of 8, so a slice of a fused projection's
+ *             output will do)
+ *   row       int32 [T]: the token's row of the table, or NULL (token t is row
+ *             t, T <= B)
+ *   slot      int32 [T]: its slot; a row or slot outside the table stores
+ *             nothing (padding).  No two tokens may name the same slot.
+ *   position  int32 [T] with mass and pos, or all three NULL: mass = 0 and
+ *             pos = position at the new slots (those below ld)
+ */
+qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t* k, int64_t ld_k, const uint16_t* v,
+                           int64_t ld_v, int64_t T, const int32_t* row, const int32_t* slot, const int32_t* table,
+                           int64_t B, int64_t max_pages, const int32_t* position, float* mass, int32_t* pos,
+                           int64_t ld, void* stream);
+
+/*
+ * qlin_attn_decode -- attention of one new token per sequence (its own K and V
+ * rows appended before).  n = min(max(lens[b], 0), max_len, table's slots);
+ * over the slots max(0, n - window) <= i < n (window == 0: all):
+ *   s_i = scale * q . k_i,  p = softmax(s),  out = fp16(sum_i p_i v_i)
+ * An empty range, or one whose logits are all -inf, gives zeros.  Logits,
+ * maxima, sums and outputs are held in fp32; p is rounded to fp16 for the
+ * product with V.  The same call gives the same bits.
+ *   q         fp16 [B x heads x head_dim], ld_q elements between sequences (a
+ *             multiple of 8); heads a multiple of kv_heads, query head j reads
+ *             kv head j / (heads / kv_heads)
+ *   lens      int32 [B] (device); max_len: a host bound of them, which sizes
+ *             the launch and the workspace
+ *   window    a slot window: only for caches that nothing was evicted from
+ *             (eviction reorders slots)
+ *   out       fp16 [B x heads x head_dim], contiguous
+ *   mass_in   fp32 [B x kv_heads x ld] or NULL (zeros); mass_out the same shape
+ *             or NULL: mass_out = mass_in + sum of the group's p at slots < n,
+ *             other slots untouched; may be the same array
+ *   work      device workspace of qlin_attn_decode_work_bytes(..) bytes, 16-byte
+ *             aligned (NULL if that is 0); its contents on entry do not matter.
+ *             Calls that overlap must not share it.
+ * One launch when a sequence is one chunk and mass_out is NULL, else two.
+ */
+qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16_t* q, int64_t ld_q, int32_t heads,
+                             const int32_t* table, const int32_t* lens, int64_t B, int64_t max_pages,
+                             int64_t max_len, float scale, int32_t window, uint16_t* out, const float* mass_in,
+                             float* mass_out, int64_t ld, void* work, void* stream);
+
+/* Bytes of the qlin_attn_decode workspace; mass != 0 when mass_out is given.
+ * 0 for invalid arguments.  Host only. */
+size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, int64_t B, int64_t max_len,
+                                   int32_t window, int32_t mass);
+
+/*
+ * qlin_kv_evict -- bring every sequence back to at most `budget` slots per kv
+ * head.  Per row b and kv head, n as in qlin_attn_decode, left = min(n, budget):
+ * the slots of the `recent` newest positions (pos > max pos - recent) stay
+ * first, then those of largest mass, ties to the lowest slot (a NaN mass
+ * counts least).  Slots that stay and lie past `left` move, in ascending order,
+ * into the freed slots below it, in ascending order: K and V rows in place in
+ * the pool, mass and pos to mass_out and pos_out.  Attention is the same for
+ * any order of slots.  Pages past ceil(left / page) are free afterwards.
+ * A page must belong to one sequence only.
+ *   budget    at least 1;  recent in [0, budget]
+ *   mass, pos [B x kv_heads x ld], ld >= max_len;  mass_out, pos_out the same
+ *             shape, written at slots < left; each may be its input
+ *   lens_out  int32 [B]: left (not the array `lens`)
+ *   kept      int32 [B x kv_heads x budget]: the old slot of each new one, -1
+ *             from `left` on
+ *   work      device workspace of qlin_kv_evict_work_bytes(..) bytes, 16-byte
+ *             aligned; its contents on entry do not matter.  Calls that
+ *             overlap must not share it.
+ */
+qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const int32_t* table, const int32_t* lens, int64_t B,
+                          int64_t max_pages, int64_t max_len, int32_t budget, int32_t recent, const float* mass,
+                          const int32_t* pos, int64_t ld, float* mass_out, int32_t* pos_out, int32_t* lens_out,
+                          int32_t* kept, void* work, void* stream);
+
+/* Bytes of the qlin_kv_evict workspace (0 for invalid arguments). Host only. */
+size_t qlin_kv_evict_work_bytes(const qlin_kv_cache* cache, int64_t B, int64_t max_len, int32_t budget);
+
 #ifdef __cplusplus
 }
 #endif

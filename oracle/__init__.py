@@ -25,9 +25,10 @@ Modules:
   layer     -- whole-layer forward passes composed from the above
   pca       -- OffQ's Top-1 PCA concentration (extreme tokens, covariance,
                leading eigenvector, Householder rotation of acts and weights)
+  kv      -- paged key/value cache: row codes, attention of one token, eviction
 
 Parity pins: every public function is pinned in ``tests/test_oracle_*.py``
 against closed forms, brute force in exact Python integers / fractions,
 library routines, or hand-worked examples in ``tests/golden/``.
 """
-from . import hadamard, quant, gemm, quaff, layer, pca  # noqa: F401
+from . import hadamard, quant, gemm, quaff, layer, pca, kv  # noqa: F401

@@ -47,8 +47,20 @@ SIGNATURES = {
     "qlin_pca_leading_eigvec": (i32, [p, i64, i64, i32, C.c_double, p, p, p, p, p]),
     "qlin_pca_fold_weight": (i32, [p, i64, i64, p, p, p, p]),
     "qlin_pca_rotate": (i32, [p, i64, i64, p, p, p]),
+    "qlin_kv_append": (i32, [p, p, i64, p, i64, i64, p, p, p, i64, i64, p, p, p, i64, p]),
+    "qlin_attn_decode": (i32, [p, p, i64, i32, p, p, i64, i64, i64, f32, i32, p, p, p, i64, p, p]),
+    "qlin_attn_decode_work_bytes": (C.c_size_t, [p, i32, i64, i64, i32, i32]),
+    "qlin_kv_evict": (i32, [p, p, p, i64, i64, i64, i32, i32, p, p, i64, p, p, p, p, p, p]),
+    "qlin_kv_evict_work_bytes": (C.c_size_t, [p, i64, i64, i32]),
     "qlin_quaff_backward": (i32, [p, i64, i64, i64, p, p, p, p, p, i32, p, p, p, p, p, p, p]),
 }
+
+
+class KVCacheStruct(C.Structure):
+    """qlin_kv_cache of include/qlin.h."""
+    _fields_ = [("k", p), ("v", p), ("kmeta", p), ("vmeta", p), ("signs", p), ("pages", i64), ("page", i32),
+                ("kv_heads", i32), ("head_dim", i32), ("bits", i32)]
+
 
 QLIN_OK = 0
 QLIN_ERR_INVALID_ARG = 1

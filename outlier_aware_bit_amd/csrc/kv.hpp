@@ -1,0 +1,150 @@
+// The paged key/value cache shared by qlin_kv_append, qlin_attn_decode and
+// qlin_kv_evict: host-side checks and the device helpers more than one of them
+// uses.
+#pragma once
+
+#include "common.hpp"
+
+namespace qlin {
+
+// A slot's rows of one kv head lie at row index (page id * kv_heads + head) *
+// page + line in every array of the pool (k, v, kmeta, vmeta), so one index
+// serves all four.
+struct KvPool {
+  uint8_t* k;
+  uint8_t* v;
+  uint32_t* kmeta;  // (step, lo) fp16 pairs; null for fp16 rows
+  uint32_t* vmeta;
+  const int8_t* signs;
+  int64_t pages;
+  int32_t heads;
+  int32_t page_shift;
+};
+
+inline int kv_page_shift(int32_t page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+inline KvPool kv_pool(const qlin_kv_cache& c) {
+  return KvPool{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), reinterpret_cast<uint32_t*>(c.kmeta),
+                reinterpret_cast<uint32_t*>(c.vmeta), c.signs, c.pages, c.kv_heads, kv_page_shift(c.page)};
+}
+
+// The parts of a cache's description that need no pointers (enough for the
+// workspace sizes), then the whole of it with the block table's size.
+inline bool kv_shape_ok(const qlin_kv_cache* c) {
+  return c != nullptr && (c->bits == 4 || c->bits == 8 || c->bits == 16) &&
+         (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) && c->page >= 16 && c->page <= 1024 &&
+         (c->page & (c->page - 1)) == 0 && c->kv_heads >= 1 && c->kv_heads <= 65535;
+}
+
+#define QLIN_KV_CACHE(c)                                                                                     \
+  do {                                                                                                       \
+    QLIN_REQUIRE((c) != nullptr, QLIN_ERR_INVALID_ARG, "cache: null pointer");                               \
+    QLIN_REQUIRE((c)->bits == 4 || (c)->bits == 8 || (c)->bits == 16, QLIN_ERR_UNSUPPORTED,                  \
+                 "bits=%d: 4, 8 and 16 are provided", (c)->bits);                                            \
+    QLIN_REQUIRE((c)->head_dim == 64 || (c)->head_dim == 128 || (c)->head_dim == 256, QLIN_ERR_UNSUPPORTED,  \
+                 "head_dim=%d: 64, 128 and 256 are provided", (c)->head_dim);                                \
+    QLIN_REQUIRE((c)->page >= 16 && (c)->page <= 1024 && ((c)->page & ((c)->page - 1)) == 0,                 \
+                 QLIN_ERR_UNSUPPORTED, "page=%d: a power of two from 16 to 1024", (c)->page);                \
+    QLIN_REQUIRE((c)->kv_heads >= 1 && (c)->kv_heads <= 65535, QLIN_ERR_SHAPE,                               \
+                 "kv_heads=%d must be in [1, 65535]", (c)->kv_heads);                                        \
+    QLIN_REQUIRE((c)->pages >= 1 && (c)->pages < ::qlin::kMaxDim &&                                          \
+                     (c)->pages * (c)->page <= ::qlin::kMaxElems / (c)->head_dim / (c)->kv_heads,            \
+                 QLIN_ERR_SHAPE, "pages=%lld: at least 1, the pool at most 2^40 elements",                   \
+                 (long long)(c)->pages);                                                                     \
+    QLIN_PTR((c)->k);                                                                                        \
+    QLIN_PTR((c)->v);                                                                                        \
+    if ((c)->bits == 16) {                                                                                   \
+      QLIN_REQUIRE((c)->kmeta == nullptr && (c)->vmeta == nullptr && (c)->signs == nullptr,                  \
+                   QLIN_ERR_INVALID_ARG, "kmeta, vmeta and signs must be NULL when bits == 16");             \
+    } else {                                                                                                 \
+      QLIN_PTR((c)->kmeta);                                                                                  \
+      QLIN_PTR((c)->vmeta);                                                                                  \
+      QLIN_OPT_PTR((c)->signs);                                                                              \
+      QLIN_REQUIRE((c)->signs == nullptr || (c)->head_dim == 128, QLIN_ERR_UNSUPPORTED,                      \
+                   "signs: only head_dim 128 has the block-128 Hadamard");                                   \
+    }                                                                                                        \
+  } while (0)
+
+// B rows of max_pages page ids; the slots of a row stay below 2^31.
+#define QLIN_KV_TABLE(c, B, max_pages)                                                                        \
+  do {                                                                                                        \
+    QLIN_REQUIRE((B) >= 0, QLIN_ERR_INVALID_ARG, "B=%lld is negative", (long long)(B));                       \
+    QLIN_REQUIRE((max_pages) >= 1 && (max_pages) <= (::qlin::kMaxDim - 1) / (c)->page, QLIN_ERR_SHAPE,        \
+                 "max_pages=%lld: at least 1, and fewer than 2^31 slots", (long long)(max_pages));            \
+    QLIN_DIMS(B, max_pages);                                                                                  \
+  } while (0)
+
+// mass / pos [B x kv_heads x ld]
+#define QLIN_KV_TRACK(c, B, ld)                                                                                \
+  QLIN_REQUIRE((ld) >= 1 && (ld) < ::qlin::kMaxDim && (B) < ::qlin::kMaxDim &&                                 \
+                   (B) * (ld) <= ::qlin::kMaxElems / (c)->kv_heads,                                            \
+               QLIN_ERR_SHAPE, "ld=%lld: at least 1, B * kv_heads * ld at most 2^40", (long long)(ld))
+
+// ---------------------------------------------------------------- device side
+// Minimum and maximum that pass a NaN on (fminf and fmaxf drop it).
+__device__ __forceinline__ float min_nan(float a, float b) { return (a < b || a != a) ? a : b; }
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+// The value of the lane whose number differs in bit MASK (1, 2, 4 or 8: within
+// a row of 16 lanes).  quad_perm swaps bits 0 and 1; a reversal of each 8 lanes
+// (xor 7) after a reversal of each quad (xor 3) is xor 4; a rotation by 8 in a
+// row of 16 is xor 8.
+template <int MASK>
+__device__ __forceinline__ float lane_xor(float v) {
+  static_assert(MASK == 1 || MASK == 2 || MASK == 4 || MASK == 8, "");
+  if constexpr (MASK == 1) return dpp_f32<0xB1>(v);
+  if constexpr (MASK == 2) return dpp_f32<0x4E>(v);
+  if constexpr (MASK == 4) return dpp_f32<0x141>(dpp_f32<0x1B>(v));
+  return dpp_f32<0x128>(v);
+}
+
+// t = (x * d) H_128 for 128 values held by 16 neighbouring lanes, 8 each
+// (lane c of the 16 holds 8c .. 8c + 7): a butterfly of spans 1, 2, .., 64 in
+// fp32, every sum and difference rounded once.  Across lanes the lower one
+// keeps u + other and the upper one other - u, both fma(u, +-1, other): the
+// product is exact.
+__device__ __forceinline__ void hadamard128(float (&u)[8], int c) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if ((e & h) == 0) {
+        const float a = u[e], b = u[e + h];
+        u[e] = add_rn(a, b);
+        u[e + h] = sub_rn(a, b);
+      }
+    }
+  }
+  auto across = [&](auto mask) {
+    constexpr int MASK = decltype(mask)::value;
+    const float sg = (c & MASK) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = __builtin_fmaf(u[e], sg, lane_xor<MASK>(u[e]));
+  };
+  across(std::integral_constant<int, 1>{});
+  across(std::integral_constant<int, 2>{});
+  across(std::integral_constant<int, 4>{});
+  across(std::integral_constant<int, 8>{});
+}
+
+// Eight fp16 values of x with the signs' sign bits flipped in, as fp32.
+__device__ __forceinline__ void signed8(const v4i raw, const int8_t* signs, float (&f)[8]) {
+  const uint2 s = *reinterpret_cast<const uint2*>(signs);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t word = static_cast<uint32_t>(raw[i >> 1]);
+    const uint16_t h = static_cast<uint16_t>((i & 1) ? word >> 16 : word);
+    const uint32_t sw = (i < 4) ? s.x : s.y;
+    f[i] = h2f(static_cast<uint16_t>(h ^ (((sw >> (8 * (i & 3) + 7)) & 1u) << 15)));
+  }
+}
+
+}  // namespace qlin

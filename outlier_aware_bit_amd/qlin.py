@@ -7,6 +7,8 @@ kernels; nothing here computes.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -455,3 +457,203 @@ def qlin_pca_rotate(x, v):
     out = _empty((M, K), torch.float16, x)
     _lib.check("qlin_pca_rotate", lib.qlin_pca_rotate(x.data_ptr(), M, K, v.data_ptr(), out.data_ptr(), _stream()))
     return out
+
+
+# ---------------------------------------------------------------- paged key/value cache
+class KVCache:
+    """A pool of pages for qlin_kv_append, qlin_attn_decode and qlin_kv_evict.
+
+    k, v: fp16 [pages, kv_heads, page, head_dim] (bits 16), or uint8
+    [pages, kv_heads, page, head_dim * bits / 8] (bits 8 or 4; int4 low nibble
+    = even channel) with kmeta, vmeta fp16 [pages, kv_heads, page, 2]: (step,
+    lo) of each row, which stands for lo + step * code.  signs: int8 [128] for
+    stored K rows (k * signs) H_128 (head_dim 128, bits below 16), or None.
+    The tensors are checked here, once, and kept.
+    """
+
+    def __init__(self, k, v, head_dim, bits, kmeta=None, vmeta=None, signs=None):
+        if bits not in (4, 8, 16):
+            raise ValueError(f"bits={bits}: 4, 8 and 16 are provided")
+        dt = torch.float16 if bits == 16 else torch.uint8
+        _req(k, "k", dt)
+        if k.dim() != 4:
+            raise ValueError(f"k: expected [pages, kv_heads, page, row], got {tuple(k.shape)}")
+        pages, kv_heads, page, _ = k.shape
+        width = head_dim if bits == 16 else head_dim * bits // 8
+        _req(k, "k", dt, (pages, kv_heads, page, width))
+        _req(v, "v", dt, (pages, kv_heads, page, width))
+        if bits == 16:
+            if kmeta is not None or vmeta is not None or signs is not None:
+                raise ValueError("kmeta, vmeta and signs are for bits 4 and 8")
+        else:
+            _req(kmeta, "kmeta", torch.float16, (pages, kv_heads, page, 2))
+            _req(vmeta, "vmeta", torch.float16, (pages, kv_heads, page, 2))
+            _opt(signs, "signs", torch.int8, (128,))
+        for t in (v, kmeta, vmeta, signs):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"the cache's tensors are on {k.device} and {t.device}")
+        self.k, self.v, self.kmeta, self.vmeta, self.signs = k, v, kmeta, vmeta, signs
+        self.pages, self.kv_heads, self.page, self.head_dim, self.bits = pages, kv_heads, page, head_dim, bits
+        self.device = k.device
+        self._struct = _lib.KVCacheStruct(k.data_ptr(), v.data_ptr(), _ptr(kmeta), _ptr(vmeta), _ptr(signs), pages,
+                                          page, kv_heads, head_dim, bits)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, head_dim, page=64, bits=4, signs=None, device="cuda"):
+        """A pool of its own, zeroed."""
+        if bits not in (4, 8, 16):
+            raise ValueError(f"bits={bits}: 4, 8 and 16 are provided")
+        dt = torch.float16 if bits == 16 else torch.uint8
+        shape = (pages, kv_heads, page)
+        width = head_dim if bits == 16 else head_dim * bits // 8
+        k, v = (torch.zeros(shape + (width,), dtype=dt, device=device) for _ in range(2))
+        meta = [None if bits == 16 else torch.zeros(shape + (2,), dtype=torch.float16, device=device)
+                for _ in range(2)]
+        return cls(k, v, head_dim, bits, *meta, signs)
+
+
+def _rows3(t, name, heads, head_dim):
+    """fp16 [n, heads, head_dim] whose tokens lie any multiple of 8 elements
+    apart (a slice of a fused projection's output): (n, elements apart)."""
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name}: expected shape (n, {heads}, {head_dim}), got {tuple(t.shape)}")
+    n = t.shape[0]
+    st = t.stride()
+    if n and (st[2] != 1 or (heads > 1 and st[1] != head_dim)):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    if n <= 1:
+        return n, heads * head_dim
+    return n, st[0]
+
+
+def _table(table):
+    _req(table, "table", torch.int32)
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [B, max_pages], got {tuple(table.shape)}")
+    return table.shape
+
+
+def _tracked(t, name, dtype, B, heads):
+    _req(t, name, dtype)
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != heads:
+        raise ValueError(f"{name}: expected shape ({B}, {heads}, ld), got {tuple(t.shape)}")
+    return t.shape[2]
+
+
+def _work(work, need, like):
+    if not need:
+        return None
+    if work is None:
+        return _empty((need,), torch.uint8, like)
+    _req(work, "work", torch.uint8)
+    if work.numel() < need:
+        raise ValueError(f"work: {work.numel()} bytes, needs {need}")
+    return work
+
+
+def qlin_kv_append(cache, k, v, table, slot, row=None, position=None, mass=None, pos=None):
+    """Stores the rows k, v fp16 [T, kv_heads, head_dim] (tokens may lie any
+    multiple of 8 elements apart) at slot int32 [T] of table row row int32 [T]
+    (None: token t is row t), quantized as the cache holds them.  With mass
+    (float32) and pos (int32) [B, kv_heads, ld] and position int32 [T]: mass = 0
+    and pos = position at the new slots."""
+    lib = _lib.load()
+    B, max_pages = _table(table)
+    T, ld_k = _rows3(k, "k", cache.kv_heads, cache.head_dim)
+    Tv, ld_v = _rows3(v, "v", cache.kv_heads, cache.head_dim)
+    if Tv != T:
+        raise ValueError(f"k holds {T} tokens, v {Tv}")
+    _req(slot, "slot", torch.int32, (T,))
+    _opt(row, "row", torch.int32, (T,))
+    ld = 0
+    if mass is not None or pos is not None or position is not None:
+        ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads)
+        _req(pos, "pos", torch.int32, mass.shape)
+        _req(position, "position", torch.int32, (T,))
+    if T == 0:
+        return
+    _lib.check("qlin_kv_append", lib.qlin_kv_append(
+        cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, _ptr(row), slot.data_ptr(), table.data_ptr(), B,
+        max_pages, _ptr(position), _ptr(mass), _ptr(pos), ld, _stream()))
+
+
+def qlin_attn_decode_work_bytes(cache, heads, B, max_len, window=0, mass=False) -> int:
+    return int(_lib.load().qlin_attn_decode_work_bytes(cache._ref, heads, B, max_len, window, int(mass)))
+
+
+def qlin_attn_decode(cache, q, table, lens, max_len, scale=None, window=0, mass=None, mass_out=None, out=None,
+                     work=None):
+    """Attention of one new token per sequence: q fp16 [B, heads, head_dim]
+    (sequences may lie any multiple of 8 elements apart), lens int32 [B] slots
+    each, at most max_len; scale defaults to head_dim ** -0.5, window (slots) to
+    all of them.  With mass_out float32 [B, kv_heads, ld]: mass_out = mass (None:
+    zeros) + this step's weights, summed over each kv head's query heads; it may
+    be mass itself.  work: a uint8 workspace of at least
+    qlin_attn_decode_work_bytes(cache, heads, B, max_len, window, mass_out is
+    not None) bytes, or None to allocate one.  Returns (out, mass_out)."""
+    lib = _lib.load()
+    B, max_pages = _table(table)
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [B, heads, {cache.head_dim}], got {tuple(q.shape)}")
+    heads = q.shape[1]
+    Bq, ld_q = _rows3(q, "q", heads, cache.head_dim)
+    if Bq != B:
+        raise ValueError(f"q holds {Bq} sequences, table {B}")
+    _req(lens, "lens", torch.int32, (B,))
+    out = _req(out, "out", torch.float16, q.shape) if out is not None else _empty(q.shape, torch.float16, q)
+    ld = 0
+    if mass_out is not None:
+        ld = _tracked(mass_out, "mass_out", torch.float32, B, cache.kv_heads)
+        _opt(mass, "mass", torch.float32, mass_out.shape)
+    elif mass is not None:
+        raise ValueError("mass needs mass_out")
+    if B == 0:
+        return out, mass_out
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    need = lib.qlin_attn_decode_work_bytes(cache._ref, heads, B, max_len, window, mass_out is not None)
+    work = _work(work, need, q)
+    _lib.check("qlin_attn_decode", lib.qlin_attn_decode(
+        cache._ref, q.data_ptr(), ld_q, heads, table.data_ptr(), lens.data_ptr(), B, max_pages, max_len, float(scale),
+        window, out.data_ptr(), _ptr(mass), _ptr(mass_out), ld, _ptr(work), _stream()))
+    return out, mass_out
+
+
+def qlin_kv_evict_work_bytes(cache, B, max_len, budget) -> int:
+    return int(_lib.load().qlin_kv_evict_work_bytes(cache._ref, B, max_len, budget))
+
+
+def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_out=None, pos_out=None, lens_out=None,
+                  kept=None, work=None):
+    """Keeps at most budget slots of every sequence and kv head: the newest
+    `recent` positions, then the largest mass (float32 [B, kv_heads, ld]; pos
+    int32, the same shape).  The pool is changed in place; mass_out and pos_out
+    may be their inputs (the default).  work: a uint8 workspace of at least
+    qlin_kv_evict_work_bytes(cache, B, max_len, budget) bytes, or None to
+    allocate one.  Returns (lens_out [B], kept [B, kv_heads, budget], mass_out,
+    pos_out); kept holds the old slot of each new one, -1 past lens_out."""
+    lib = _lib.load()
+    B, max_pages = _table(table)
+    _req(lens, "lens", torch.int32, (B,))
+    ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads)
+    _req(pos, "pos", torch.int32, mass.shape)
+    mass_out = mass if mass_out is None else _req(mass_out, "mass_out", torch.float32, mass.shape)
+    pos_out = pos if pos_out is None else _req(pos_out, "pos_out", torch.int32, mass.shape)
+    lens_out = _req(lens_out, "lens_out", torch.int32, (B,)) if lens_out is not None else torch.empty_like(lens)
+    if B and lens_out.data_ptr() == lens.data_ptr():
+        raise ValueError("lens_out must not be lens")
+    shape = (B, cache.kv_heads, budget)
+    kept = _req(kept, "kept", torch.int32, shape) if kept is not None else _empty(shape, torch.int32, lens)
+    if B == 0:
+        return lens_out, kept, mass_out, pos_out
+    work = _work(work, lib.qlin_kv_evict_work_bytes(cache._ref, B, max_len, budget), lens)
+    _lib.check("qlin_kv_evict", lib.qlin_kv_evict(
+        cache._ref, table.data_ptr(), lens.data_ptr(), B, max_pages, max_len, budget, recent, mass.data_ptr(),
+        pos.data_ptr(), ld, mass_out.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), kept.data_ptr(), _ptr(work),
+        _stream()))
+    return lens_out, kept, mass_out, pos_out
