@@ -572,8 +572,9 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t* k, int64_
  *   q         fp16 [B x heads x head_dim], ld_q elements between sequences (a
  *             multiple of 8); heads a multiple of kv_heads, query head j reads
  *             kv head j / (heads / kv_heads)
- *   lens      int32 [B] (device); max_len: a host bound of them, which sizes
- *             the launch and the workspace
+ *   B         at most 65535
+ *   lens      int32 [B] (device); max_len: a host bound of them (at most 2^30),
+ *             which sizes the launch and the workspace
  *   window    a slot window: only for caches that nothing was evicted from
  *             (eviction reorders slots)
  *   out       fp16 [B x heads x head_dim], contiguous

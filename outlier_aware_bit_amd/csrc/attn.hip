@@ -13,9 +13,12 @@
 // eight slots by D / 16 channels per lane and transposed in registers by byte
 // permutes.  Nothing of K, V, S or P goes through LDS.
 //
-// The cache is split over its length: a workgroup takes `chunk` slots of one
-// kv head, its four waves 32 * U slots at a time; a second launch joins the
-// chunks of a head by their maxima and sums (none when one chunk is enough).
+// The work is a sequence of tiles of 32 slots, row after row (a row: a sequence,
+// a kv head, and up to 32 of its query heads).  As many workgroups as the GPU
+// holds at a time take equal runs of it, wherever rows begin and end, so ragged
+// batches and single long rows fill it alike; a row that lies in several
+// workgroups leaves a maximum, a sum and a vector in each, which a second launch
+// joins.  Rows that are one short run each need no second launch.
 #include <type_traits>
 
 #include "kv.hpp"
@@ -29,6 +32,7 @@ struct AttnArgs {
   int64_t ld_q;
   int32_t heads;  // query heads
   int32_t group;  // query heads per kv head
+  int32_t parts;  // rows per kv head: its query heads, 32 at a time
   const int32_t* table;
   const int32_t* lens;
   int64_t B, max_pages;
@@ -39,24 +43,31 @@ struct AttnArgs {
   const float* mass_in;
   float* mass_out;
   int64_t ld_mass;
-  int32_t chunk, splits, head_tiles;
-  float* part_o;    // [B * heads x splits x D] (splits > 1)
-  float2* part_ml;  // [B * heads x splits]: reference exponent and sum
+  int32_t groups;   // workgroups that share the tiles; 0: one row each, whole
+  int2* runs;       // [rows]: slot of a row's first part, and its last workgroup
+  float* part_o;    // [2 * groups x row_heads x D]: a workgroup's first and last row, if cut
+  float2* part_ml;  // [2 * groups x row_heads]: reference exponent and sum
+  int32_t row_heads;
+  float2* head_ml;  // [B * heads] of rows that are not cut (with mass)
   float* logits;    // [B * heads x ld_logits], log2 domain (with mass)
   int64_t ld_logits;
 };
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
-constexpr int kMaxChunk = 2048;
-constexpr int kTileHeads = 8;  // query heads of a workgroup
+constexpr int kCus = 256;
+constexpr int kTile = 32;       // slots
+constexpr int kTileHeads = 8;   // query heads of a wave
+constexpr int kRowHeads = kTileHeads * kAttnWaves;
 
-// A wave's exponent reference m starts below any finite logit.
+// A head's weights are exp2(s - m), for codes times the row's step, with m such
+// that the largest is 2^kTop when m is set; m moves when one would pass 2^kCeil,
+// so fp16 holds them (below 2^16), and slots down to 2^-(24 + kTop) of the
+// largest still count.  The sum's own terms may grow to 2^kSumTop where steps
+// are small (or zero: those weights are all 0).
+constexpr float kTop = 7.0f, kCeil = 0x1p15f, kSumTop = 30.0f, kSumCeil = 0x1p40f;
+// The reference of nothing: below any finite logit.
 constexpr float kNoRef = -3.0e38f;
-// exp2(s - m) reaches 2^kTop at the maximum that m was set from and may grow to
-// 2^kCeil before m is moved, so fp16 holds it (below 2^16) and slots down to
-// 2^-(24 + kTop) of that maximum still count.
-constexpr float kTop = 7.0f, kCeil = 15.0f;
 
 __device__ __forceinline__ v8h as_v8h(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const v4i w = {static_cast<int>(a), static_cast<int>(b), static_cast<int>(c), static_cast<int>(d)};
@@ -65,6 +76,14 @@ __device__ __forceinline__ v8h as_v8h(uint32_t a, uint32_t b, uint32_t c, uint32
 
 __device__ __forceinline__ float lo_half(uint32_t w) { return h2f(static_cast<uint16_t>(w)); }
 __device__ __forceinline__ float hi_half(uint32_t w) { return h2f(static_cast<uint16_t>(w >> 16)); }
+
+// Four channels of the output, fp16; zero where nothing has weight.
+__device__ __forceinline__ uint2 out4(float4 acc, float sum) {
+  const bool none = sum == 0.0f;
+  const uint32_t x = f2h(none ? 0.0f : div_rn(acc.x, sum)), y = f2h(none ? 0.0f : div_rn(acc.y, sum));
+  const uint32_t z = f2h(none ? 0.0f : div_rn(acc.z, sum)), w = f2h(none ? 0.0f : div_rn(acc.w, sum));
+  return make_uint2(x | y << 16, z | w << 16);
+}
 
 __device__ __forceinline__ float max_groups(float v) {  // over the four lane groups of a head
   v = fmaxf(v, __shfl_xor(v, 16, 64));
@@ -75,33 +94,77 @@ __device__ __forceinline__ float sum_groups(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// First slot that row b attends to, and one past the last.
-__device__ __forceinline__ void attn_range(const AttnArgs& a, int64_t b, int& low, int& n) {
-  const int64_t cap = a.max_pages << a.c.page_shift;
-  n = a.lens[b];
-  n = n < 0 ? 0 : n;
-  n = n > a.max_len ? a.max_len : n;
-  n = n > cap ? static_cast<int>(cap) : n;
+// A value that no kernel here writes, at an address that is the same for the
+// whole wave: a scalar load, apart from the vector loads' counter.
+__device__ __forceinline__ int32_t scalar_i32(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(p);
+}
+// Some values are the same in every lane without the compiler seeing it (a
+// division's result, a sum after a branch of one lane); it would keep them, and
+// all that follows from them, in vector registers.
+__device__ __forceinline__ int uniform_i32(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform_i64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// First slot that a sequence of `len` attends to, and one past the last.
+__device__ __forceinline__ void attn_range(const AttnArgs& a, int len, int& low, int& n) {
+  n = len < 0 ? 0 : len;
+  n = n > a.max_len ? a.max_len : n;  // at most the table's slots
   low = (a.window > 0 && n > a.window) ? n - a.window : 0;
 }
-// The chunks of a row start at the 32-slot block of its first slot.
-__device__ __forceinline__ int attn_base(int low) { return low & ~31; }
+// A row's tiles: those of its sequence that hold a slot in the range.
+__device__ __forceinline__ void attn_tiles(int low, int n, int& t0, int& t1) {
+  t0 = low / kTile;
+  t1 = (n + kTile - 1) / kTile;
+}
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // one lane up, in rows of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  return v;
+}
+// x / y of numbers that are the same in every lane, y > 0: 32 bits where they do.
+__device__ __forceinline__ int64_t attn_div(int64_t x, int64_t y) {
+  if (x <= 0x7fffffff && y <= 0x7fffffff) return uniform_i32(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+  return uniform_i64(x / y);
+}
+// A workgroup's share of `total` tiles.
+__device__ __forceinline__ int64_t attn_share(const AttnArgs& a, int64_t total) {
+  const int64_t share = attn_div(total + a.groups - 1, a.groups);
+  return share < kAttnWaves ? kAttnWaves : share;
+}
+// Where a workgroup leaves its part of a row: apart if it is a row that begins
+// inside the workgroup's run (its last), not at its start or before.
+__device__ __forceinline__ int64_t part_slot(int64_t group, int64_t row_begin, int64_t share) {
+  return 2 * group + (row_begin > group * share ? 1 : 0);
+}
 
-// Codes enter the matrix products as fp16 denormals, code * 2^-24, which the
-// matrix instructions keep exactly: an AND or a byte permute then makes an
-// operand, and 2^24 goes into the row's step.  The second and fourth nibble of
-// a 16-bit half stay where they are, 16 times larger; the first product
-// divides q by 16 there, the second one its result.
+// Codes enter the matrix products as the low 11 bits of an fp16, which are
+// linear (denormals, then the first binade): bits * 2^-24.  An AND or a byte
+// permute then makes an operand, and the power of two goes into the row's step.
+// Of the four nibbles of a 16-bit half, two sit four bits higher, 16 times
+// larger; the first product divides q by 16 there, the second one its result.
+// The matrix instructions align such operands as if they were normal numbers
+// and drop what falls off the end, always downwards: measured, -1.4e-7 of the
+// sum for nibbles in bits 0 .. 3, which shows where V's codes cancel against
+// the rows' lo over a long cache.  V's nibbles go to bits 3 .. 6 and 7 .. 10
+// instead, one shift more (2^-3 of that, and nothing).
 template <int BITS>
 struct Codes {
-  static constexpr float unit = 16777216.0f;  // 2^24
-  static constexpr float mid = (BITS == 4) ? 7.5f : 127.5f;
+  static constexpr float k_unit = 16777216.0f;                              // 2^24
+  static constexpr float v_unit = (BITS == 4) ? 2097152.0f : 16777216.0f;  // 2^21
 };
 
-template <int BITS, int D, bool ROT, bool LOGITS>
+template <int BITS, int D>
 struct Attn {
   static constexpr int RB = D * BITS / 8;                  // bytes of a stored row
-  static constexpr int U = (BITS == 4 && D <= 128) ? 2 : 1;  // 32-slot blocks of a wave at a time
   static constexpr int KS = D / 32;                        // k steps of the first product
   static constexpr int NT = D / 16;                        // channel tiles of the second
   static constexpr int KW = RB / 16;                       // dwords of K of a lane and row
@@ -151,8 +214,8 @@ struct Attn {
       return __builtin_amdgcn_perm(wb[t >> 2], wa[t >> 2], 0x0c000c00u | ((4 + d) << 16) | d);
     } else {
       const uint32_t w = __builtin_amdgcn_perm(wb[t >> 3], wa[t >> 3], (t & 4) ? 0x07060302u : 0x05040100u);
-      const uint32_t y = (t & 2) ? w >> 8 : w;
-      return y & ((t & 1) ? 0x00f000f0u : 0x000f000fu);
+      const uint32_t y = (t & 2) ? w >> 5 : w << 3;
+      return y & ((t & 1) ? 0x07800780u : 0x00780078u);
     }
   }
 
@@ -194,353 +257,482 @@ struct Attn {
   }
 };
 
-// Bytes of the split kernel's dynamic LDS: the row indices of the chunk's
-// pages, and either the rotated q or the waves' results, whichever is larger.
-constexpr int kIdBytes = (kMaxChunk / 16 + 1) * 8 + 8;
+// Bytes of the kernel's dynamic LDS: the waves' sums, then their vectors or the
+// rotated q, whichever is larger.
+constexpr int kRotLd = 132;  // of a rotated q: eight heads in different banks
 constexpr int kMlBytes = kAttnWaves * kTileHeads * 8;
-inline size_t attn_lds(int D, int group, bool rot) {
-  const int hs = group < kTileHeads ? group : kTileHeads;
+inline size_t attn_lds(int D, int row_heads, bool rot) {
+  const int tiles = (row_heads + kTileHeads - 1) / kTileHeads;
+  const int hs = row_heads < kTileHeads ? row_heads : kTileHeads;
   const size_t o = static_cast<size_t>(kAttnWaves) * hs * (D + 4) * sizeof(float);
-  const size_t qr = rot ? kTileHeads * 128 * sizeof(float) : 0;
-  return kIdBytes + kMlBytes + (o > qr ? o : qr);
+  const size_t q = rot ? static_cast<size_t>(tiles) * kTileHeads * kRotLd * sizeof(float) : 0;
+  return kMlBytes + (o > q ? o : q);
 }
 
+// Workgroups that a CU holds: as many as fit with two tiles in registers, so
+// that the next one is on its way while one is computed on.
+constexpr int attn_resident(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
+
 template <int BITS, int D, bool ROT, bool LOGITS>
-__global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
-  using A = Attn<BITS, D, ROT, LOGITS>;
-  constexpr int RB = A::RB, U = A::U, KS = A::KS, NT = A::NT, KW = A::KW, VW = A::VW;
+__global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(AttnArgs a) {
+  using A = Attn<BITS, D>;
+  constexpr int RB = A::RB, KS = A::KS, NT = A::NT, KW = A::KW, VW = A::VW;
   constexpr bool QUANT = A::QUANT;
   extern __shared__ uint8_t lds[];
-  int64_t* ids = reinterpret_cast<int64_t*>(lds);                      // row index of each page, or -1
-  float2* lds_ml = reinterpret_cast<float2*>(lds + kIdBytes);          // [wave][kTileHeads]
-  float* lds_o = reinterpret_cast<float*>(lds + kIdBytes + kMlBytes);  // [wave][head][D + 4]
+  float2* lds_ml = reinterpret_cast<float2*>(lds);         // [wave][kTileHeads]
+  float* lds_o = reinterpret_cast<float*>(lds + kMlBytes);  // [wave][head][D + 4]
 
-  // Head tiles of one chunk are eight workgroups apart: the same XCD's cache.
-  const int64_t idx = blockIdx.x;
-  const int64_t rest = idx / (8 * a.head_tiles) * 8 + (idx & 7);
-  const int ht = static_cast<int>((idx >> 3) % a.head_tiles);
-  if (rest >= a.B * a.c.heads * a.splits) return;
-  const int split = static_cast<int>(rest % a.splits);
-  const int64_t bh = rest / a.splits;
-  const int h = static_cast<int>(bh % a.c.heads);
-  const int64_t b = bh / a.c.heads;
-  int low, n;
-  attn_range(a, b, low, n);
-  const int c0 = attn_base(low) + split * a.chunk;
-  const int hs = min(kTileHeads, a.group - kTileHeads * ht);  // query heads here
-  const int hfirst = h * a.group + kTileHeads * ht;           // the first of them
-  const int64_t head0 = b * a.heads + hfirst;
-  if (c0 >= n) {  // uniform
-    if (a.splits == 1)
-      for (int i = threadIdx.x; i < hs * D; i += kAttnThreads) a.out[head0 * D + i] = 0;
-    return;
-  }
-  const int end = min(n, c0 + a.chunk);
-
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = lane >> 4, col = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ps = a.c.page_shift, line_mask = (1 << ps) - 1;
-  const int page0 = c0 >> ps, page_count = ((end - 1) >> ps) - page0 + 1;
-  for (int i = threadIdx.x; i < page_count; i += kAttnThreads) {
-    const int32_t id = a.table[b * a.max_pages + page0 + i];
-    ids[i] = (id >= 0 && id < a.c.pages) ? (static_cast<int64_t>(id) * a.c.heads + h) << ps : -1;
-  }
+  const int rows_b = a.c.heads * a.parts;  // rows of a sequence
 
-  // q in the operand order of the first product, and sum_d q_d for the rows'
-  // lo.  Columns 8 .. 15: the same q, or what fp16 leaves of a rotated one.
-  const int hcol = col & 7, rem = col >> 3;
-  const float frem = static_cast<float>(rem);
-  v8h qf[KS];
-  float qsum = 0.0f;
-  constexpr int SPP = A::EPP / 8;  // k steps of a piece
-  if constexpr (ROT) {
-    float* q_lds = lds_o;  // [head][128]
-    const int hd = threadIdx.x >> 4, c = threadIdx.x & 15;
-    if (hd < kTileHeads) {  // uniform per wave
-      float u[8];
-      const int hq = hd < hs ? hd : 0;
-      const v4i raw = *reinterpret_cast<const v4i*>(a.q + b * a.ld_q + (hfirst + hq) * D + 8 * c);
-      signed8(raw, a.c.signs + 8 * c, u);
-      hadamard128(u, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q_lds[hd * 128 + 8 * c + i] = hd < hs ? u[i] * 0.0078125f : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d0 = A::k_channel(s / SPP, g) + 8 * (s % SPP);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x = q_lds[hcol * 128 + d0 + A::k_order(i)];
-        qsum += x;
-        if (BITS == 4 && (i & 2)) x *= 0.0625f;
-        const _Float16 hi = static_cast<_Float16>(x);
-        qf[s][i] = rem ? static_cast<_Float16>(x - static_cast<float>(hi)) : hi;
-      }
-    }
+  // The run of this workgroup: rows (b, r) from tile `at` of the flat sequence
+  // of tiles up to `stop`; row_at: where the row begins in it.
+  int64_t at = 0, stop = 0, row_at = 0, share = 0;
+  int b, r;
+  if (a.groups == 0) {
+    b = uniform_i32(static_cast<int>(blockIdx.x) / rows_b);
+    r = static_cast<int>(blockIdx.x) - b * rows_b;
   } else {
-    const bool here = hcol < hs;
-    const uint16_t* qp = a.q + b * a.ld_q + (hfirst + (here ? hcol : 0)) * D;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const v8h raw = *reinterpret_cast<const v8h*>(qp + A::k_channel(s / SPP, g) + 8 * (s % SPP));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const _Float16 x = here ? raw[A::k_order(i)] : static_cast<_Float16>(0.0f);
-        if constexpr (QUANT) qsum += static_cast<float>(x);
-        qf[s][i] = (BITS == 4 && (i & 2)) ? x * static_cast<_Float16>(0.0625f) : x;
+    // Every wave for itself: the tiles of all sequences, then the one where the
+    // run begins.
+    auto tiles_of = [&](int i) {
+      if (i >= a.B) return 0;
+      int low, n, t0, t1;
+      attn_range(a, a.lens[i], low, n);
+      attn_tiles(low, n, t0, t1);
+      return t1 - t0;
+    };
+    const int tiles0 = tiles_of(lane);
+    const uint32_t sum0 = wave_scan(tiles0);  // 64 times 2^25 at most
+    int64_t total = static_cast<uint32_t>(__builtin_amdgcn_readlane(sum0, 63));
+    for (int b0 = 64; b0 < a.B; b0 += 64)
+      total += static_cast<uint32_t>(__builtin_amdgcn_readlane(wave_scan(tiles_of(b0 + lane)), 63));
+    total *= rows_b;
+    share = attn_share(a, total);
+    at = blockIdx.x * share;
+    stop = min(at + share, total);
+    if (at >= stop) return;
+    int64_t before = 0;  // tiles of the sequences before b0
+    for (int b0 = 0;; b0 += 64) {
+      const int tiles = b0 == 0 ? tiles0 : tiles_of(b0 + lane);
+      const uint32_t sum = b0 == 0 ? sum0 : wave_scan(tiles);
+      const uint64_t past = __ballot((before + sum) * rows_b > at);
+      if (past != 0) {
+        const int i = __builtin_ctzll(past);
+        const int own = __builtin_amdgcn_readlane(tiles, i);
+        b = b0 + i;
+        row_at = (before + static_cast<uint32_t>(__builtin_amdgcn_readlane(sum, i)) - own) * rows_b;
+        r = static_cast<int>(attn_div(at - row_at, own));
+        row_at += static_cast<int64_t>(r) * own;
+        break;
       }
+      before += static_cast<uint32_t>(__builtin_amdgcn_readlane(sum, 63));
     }
   }
-  if constexpr (QUANT) qsum = sum_groups(qsum) * a.scale_log2;
-  const float qscale = QUANT ? a.scale_log2 * Codes<BITS>::unit : a.scale_log2;
-  __syncthreads();  // ids
 
-  v4f o[NT];
+  // A row, or the part of it in this run: tiles [t0, t1) of sequence b.
+  struct Row {
+    int low, n, t0, t1, tiles;  // slots attended to, tiles here and in all
+    int h, hrow, hq0;           // kv head; query heads, and the first of them
+    int per, ht, hs, end;       // waves of a head tile; this wave's head tile, its heads (none: it idles)
+    const int32_t* table;
+    int last_page;
+  };
+  auto row_of = [&]() {
+    Row w;
+    attn_range(a, scalar_i32(a.lens + b), w.low, w.n);
+    attn_tiles(w.low, w.n, w.t0, w.t1);
+    w.tiles = w.t1 - w.t0;
+    if (a.groups != 0) {
+      const int64_t first = at > row_at ? at - row_at : 0;
+      const int64_t last = stop - row_at < w.tiles ? stop - row_at : w.tiles;
+      w.t1 = w.t0 + static_cast<int>(last);
+      w.t0 += static_cast<int>(first);
+    }
+    w.h = a.parts == 1 ? r : uniform_i32(r / a.parts);
+    const int part = r - w.h * a.parts;
+    w.hrow = min(kRowHeads, a.group - part * kRowHeads);
+    w.hq0 = w.h * a.group + part * kRowHeads;
+    // The waves share out the head tiles, then the slots.
+    const int head_tiles = (w.hrow + kTileHeads - 1) / kTileHeads;
+    const int shift = head_tiles == 1 ? 2 : head_tiles == 2 ? 1 : 0;
+    w.per = 1 << shift;
+    w.ht = wave >> shift;
+    w.hs = min(kTileHeads, w.hrow - w.ht * kTileHeads);
+    w.end = min(w.n, w.t1 * kTile);
+    w.table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    w.last_page = max(w.n - 1, 0) >> ps;
+    return w;
+  };
+  struct Tile {
+    uint32_t k[2][KW], v[8][VW], km[8], vm[8];
+    bool ok0, ok1;  // its halves are on pages of the pool
+  };
+  auto load = [&](Tile& x, const Row& w, int tile, int g, int col) {
+    // The rows where the halves of the tile begin: pages hold 16 slots or
+    // more.  A half beyond the last page, or on a page outside the pool,
+    // reads another row instead, and its values are dropped below.
+    const int slot = tile * kTile;
+    const int32_t id0 = scalar_i32(w.table + (slot >> ps));
+    const int32_t id1 = scalar_i32(w.table + min((slot + 16) >> ps, w.last_page));
+    const uint32_t pages = static_cast<uint32_t>(a.c.pages), heads = static_cast<uint32_t>(a.c.heads);
+    x.ok0 = static_cast<uint32_t>(id0) < pages;
+    x.ok1 = static_cast<uint32_t>(id1) < pages;
+    const uint32_t p0 = x.ok0 ? id0 : 0, p1 = x.ok1 ? id1 : 0;
+    const int64_t row0 = ((static_cast<uint64_t>(p0) * heads + w.h) << ps) + (slot & line_mask);
+    const int64_t row1 = ((static_cast<uint64_t>(p1) * heads + w.h) << ps) + ((slot + 16) & line_mask);
+    // Row 8 * (run & 1) + line of the lane's run of eight slots, from the row
+    // where its half of the tile begins.
+    const int krun = col >> 2;
+    const int64_t krow = krun < 2 ? row0 : row1, vrow = g < 2 ? row0 : row1;
+    const int v_row = 8 * (g & 1);
+    const uint8_t* kp = a.c.k + krow * RB + (8 * (krun & 1) + (col & 3)) * RB + (RB == 32 ? 8 : 16) * g;
+    const uint8_t* vp = a.c.v + vrow * RB + v_row * RB + col * (RB / 16 / A::VC);
+    A::load_k(kp, x.k[0]);
+    A::load_k(kp + 4 * RB, x.k[1]);
+    if constexpr (QUANT) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) o[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  v4f psum = {0.0f, 0.0f, 0.0f, 0.0f};  // sum of the rounded P, for the codes' midpoint
-  float m = kNoRef, l = 0.0f, omid = 0.0f, inv_ref = 0.0f, ref = 0.0f;
+      for (int i = 0; i < 8; i += 4) {
+        const uint4 m = *reinterpret_cast<const uint4*>(a.c.kmeta + vrow + v_row + i);
+        x.km[i] = m.x, x.km[i + 1] = m.y, x.km[i + 2] = m.z, x.km[i + 3] = m.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) A::load_v(vp + i * RB, x.v[i]);
+    if constexpr (QUANT) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const uint4 m = *reinterpret_cast<const uint4*>(a.c.vmeta + vrow + v_row + i);
+        x.vm[i] = m.x, x.vm[i + 1] = m.y, x.vm[i + 2] = m.z, x.vm[i + 3] = m.w;
+      }
+    }
+  };
+  while (true) {
+    const Row w = row_of();
+    const int low = w.low, end = w.end, hrow = w.hrow, hs = w.hs, ht = w.ht, per = w.per;
+    const int64_t head0 = static_cast<int64_t>(b) * a.heads + w.hq0;
+    // What depends on the lane alone is worked out anew for each row: kept
+    // across rows, it would take the registers of a tile.
+    int lane_again = lane;
+    asm volatile("" : "+v"(lane_again));
+    const int g = lane_again >> 4, col = lane_again & 15;
 
-  const int krun = col >> 2, kline = col & 3;
-  for (int base = c0 + wave * 32 * U; base < end; base += kAttnWaves * 32 * U) {  // uniform per wave
-    // Slots beyond the last page read another row of the same page, whose
-    // values are dropped below.
-    uint32_t kw[U][2][KW], vw[U][8][VW], km[QUANT ? U : 1][8], vm[QUANT ? U : 1][8];
-    bool run_ok[U];
+    // Two tiles, in turn: one is loaded while the other is computed on.  (A
+    // wave without a tile loads one as well: of the row, or of page 0 for a row
+    // without slots.)  The first is on its way while q is prepared, where the
+    // registers for both are there.
+    constexpr bool EARLY = D <= 128;
+    Tile x, y;
+    int tile = w.t0 + (wave & (per - 1));  // uniform per wave
+    if constexpr (EARLY) load(x, w, max(min(tile, w.t1 - 1), 0), g, col);
+
+    // q in the operand order of the first product, and sum_d q_d for the rows'
+    // lo.  Columns 8 .. 15: the same q, or what fp16 leaves of a rotated one.
+    const int hcol = col & 7, rem = col >> 3;
+    const float frem = static_cast<float>(rem);
+    v8h qf[KS];
+    float qsum = 0.0f;
+    constexpr int SPP = A::EPP / 8;  // k steps of a piece
+    if constexpr (ROT) {
+      float* q_lds = lds_o;  // [head][kRotLd]
+      const int c = tid & 15;
+      for (int hd = tid >> 4; hd < (hrow + kTileHeads - 1) / kTileHeads * kTileHeads; hd += kAttnThreads / 16) {
+        float u[8];  // uniform per wave: 16 lanes a head
+        const int hq = hd < hrow ? hd : 0;
+        const v4i raw = *reinterpret_cast<const v4i*>(a.q + b * a.ld_q + (w.hq0 + hq) * D + 8 * c);
+        signed8(raw, a.c.signs + 8 * c, u);
+        hadamard128(u, c);
+        const float f = hd < hrow ? 0.0078125f : 0.0f;
+        float4* dst = reinterpret_cast<float4*>(q_lds + hd * kRotLd + 8 * c);
+        dst[0] = make_float4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
+        dst[1] = make_float4(u[4] * f, u[5] * f, u[6] * f, u[7] * f);
+      }
+      lds_barrier();
+      const float* q_row = q_lds + ((hs > 0 ? ht : 0) * kTileHeads + hcol) * kRotLd;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int ks = base + 32 * u + 8 * krun, vs = base + 32 * u + 8 * g;
-      const int64_t ki = ids[min((ks >> ps) - page0, page_count - 1)];
-      const int64_t vi = ids[min((vs >> ps) - page0, page_count - 1)];
-      run_ok[u] = vi >= 0;
-      const int64_t krow = (ki < 0 ? 0 : ki) + (ks & line_mask) + kline;
-      const int64_t vrow = (vi < 0 ? 0 : vi) + (vs & line_mask);
-      const uint8_t* kp = a.c.k + krow * RB + (RB == 32 ? 8 : 16) * g;
-      const uint8_t* vp = a.c.v + vrow * RB + col * (RB / 16 / A::VC);
-      A::load_k(kp, kw[u][0]);
-      A::load_k(kp + 4 * RB, kw[u][1]);
-      if constexpr (QUANT) {
+      for (int s = 0; s < KS; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(q_row + A::k_channel(s / SPP, g) + 8 * (s % SPP));
+        const float4 lo4 = src[0], hi4 = src[1];
+        const float u[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(a.c.kmeta + vrow + i);
-          km[u][i] = x.x, km[u][i + 1] = x.y, km[u][i + 2] = x.z, km[u][i + 3] = x.w;
+        for (int i = 0; i < 8; ++i) {
+          float v = u[A::k_order(i)];
+          qsum += v;
+          if (BITS == 4 && (i & 2)) v *= 0.0625f;
+          const _Float16 hi = static_cast<_Float16>(v);
+          qf[s][i] = rem ? static_cast<_Float16>(v - static_cast<float>(hi)) : hi;
         }
       }
+      lds_barrier();  // lds_o takes the vectors next
+    } else {
+      const bool here = hcol < hs;
+      const uint16_t* qp = a.q + b * a.ld_q + (w.hq0 + (here ? ht * kTileHeads + hcol : 0)) * D;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) A::load_v(vp + i * RB, vw[u][i]);
-      if constexpr (QUANT) {
+      for (int s = 0; s < KS; ++s) {
+        const v8h raw = *reinterpret_cast<const v8h*>(qp + A::k_channel(s / SPP, g) + 8 * (s % SPP));
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(a.c.vmeta + vrow + i);
-          vm[u][i] = x.x, vm[u][i + 1] = x.y, vm[u][i + 2] = x.z, vm[u][i + 3] = x.w;
+        for (int i = 0; i < 8; ++i) {
+          const _Float16 v = here ? raw[A::k_order(i)] : static_cast<_Float16>(0.0f);
+          if constexpr (QUANT) qsum += static_cast<float>(v);
+          qf[s][i] = (BITS == 4 && (i & 2)) ? v * static_cast<_Float16>(0.0625f) : v;
         }
       }
     }
+    if constexpr (QUANT) qsum = sum_groups(qsum) * a.scale_log2;
+    const float qscale = QUANT ? a.scale_log2 * Codes<BITS>::k_unit : a.scale_log2;
 
-    float s[U][8];
-    float smax = -INFINITY;
-    bool whole = base >= low && base + 32 * U <= end;
+    v4f o[NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) whole = whole && run_ok[u];
-    const bool all_whole = __all(whole);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int t = 0; t < NT; ++t) o[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = 0.0f, l = 0.0f, olo = 0.0f;  // olo: the weights times the rows' lo
+
+    auto compute = [&](Tile& x, int tile) {
+      const int base = tile * kTile;
+      float s[8];  // logits less m
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const v8h kf = A::k_operand(kw[u][t], k);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[k], acc, 0, 0, 0);
-        }
+        for (int k = 0; k < KS; ++k)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(A::k_operand(x.k[t], k), qf[k], acc, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (ROT) acc[r] += lane_xor<8>(acc[r]);
-          const int i = 4 * t + r;
+        for (int i = 4 * t; i < 4 * t + 4; ++i) {
+          if constexpr (ROT) acc[i & 3] += lane_xor<8>(acc[i & 3]);
           if constexpr (QUANT)
-            s[u][i] = __builtin_fmaf(acc[r], lo_half(km[u][i]) * qscale, hi_half(km[u][i]) * qsum);
+            s[i] = __builtin_fmaf(acc[i & 3] * qscale, lo_half(x.km[i]), __builtin_fmaf(hi_half(x.km[i]), qsum, -m));
           else
-            s[u][i] = acc[r] * qscale;
+            s[i] = __builtin_fmaf(acc[i & 3], qscale, -m);
         }
       }
-    }
-    if (!all_whole) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (!(x.ok0 && x.ok1 && base >= low && base + kTile <= end)) {  // uniform
+        const bool on_page = g < 2 ? x.ok0 : x.ok1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int slot = base + 32 * u + 8 * g + i;
-          const bool ok = run_ok[u] && slot >= low && slot < end;
-          s[u][i] = ok ? s[u][i] : -INFINITY;
+          const int slot = base + 8 * g + i;
+          const bool ok = on_page && slot >= low && slot < end;
+          s[i] = ok ? s[i] : -INFINITY;
 #pragma unroll
-          for (int w = 0; w < VW; ++w) vw[u][i][w] = ok ? vw[u][i][w] : 0u;
-          if constexpr (QUANT) vm[u][i] = ok ? vm[u][i] : 0u;
+          for (int w = 0; w < VW; ++w) x.v[i][w] = ok ? x.v[i][w] : 0u;
+          if constexpr (QUANT) x.vm[i] = ok ? x.vm[i] : 0u;
         }
       }
-    }
-    if constexpr (LOGITS) {
-      if (col < hs) {
-        float* lp = a.logits + (head0 + col) * a.ld_logits + base + 8 * g;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (base + 32 * u + 8 * g < a.ld_logits) {
-            *reinterpret_cast<float4*>(lp + 32 * u) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
-            *reinterpret_cast<float4*>(lp + 32 * u + 4) = make_float4(s[u][4], s[u][5], s[u][6], s[u][7]);
-          }
+      if constexpr (LOGITS) {
+        if (col < hs) {
+          float* lp = a.logits + (head0 + ht * kTileHeads + col) * a.ld_logits + base + 8 * g;
+          *reinterpret_cast<float4*>(lp) = make_float4(s[0] + m, s[1] + m, s[2] + m, s[3] + m);
+          *reinterpret_cast<float4*>(lp + 4) = make_float4(s[4] + m, s[5] + m, s[6] + m, s[7] + m);
         }
       }
-    }
-    float vmax = 0.0f;
+      float e[8], w[8], sum, wmax;
+      auto weights = [&]() {
+        sum = 0.0f;
+        wmax = 0.0f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        smax = fmaxf(smax, s[u][i]);
-        if constexpr (QUANT) vmax = fmaxf(vmax, lo_half(vm[u][i]));
-      }
-    }
-    // The references move only when a weight would leave fp16's range.
-    bool move = smax > m + kCeil;
-    if constexpr (QUANT) move = move || vmax * inv_ref > 1.0f || ref == 0.0f;
-    if (__any(move)) {
-      const float top = max_groups(smax);
-      const float mn = top > m + kCeil ? top - kTop : m;
-      float alpha = __builtin_amdgcn_exp2f(m - mn), beta = alpha;
-      if constexpr (QUANT) {
-        // A power of two at least four times the largest step so far.
-        float big = max_groups(vmax);
-        big = __shfl(big, 0, 64);
-        if (!(big * inv_ref <= 1.0f) || ref == 0.0f) {
-          const int e = big > 0.0f ? static_cast<int>((__builtin_bit_cast(uint32_t, big) >> 23) & 255u) - 127 + 3 : -24;
-          const float nr = __builtin_bit_cast(float, static_cast<uint32_t>(e + 127) << 23);
-          const float ni = __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
-          beta *= ref * ni;
-          ref = nr;
-          inv_ref = ni;
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(s[i]);
+          sum += e[i];
+          w[i] = QUANT ? __builtin_fmaf(e[i], lo_half(x.vm[i]), 0.0f) : e[i];
+          wmax = fmaxf(wmax, w[i]);
         }
+      };
+      weights();
+      // Out of range, or nothing yet to be in range of.
+      if (__any(wmax > kCeil || sum > kSumCeil || !(l + sum > 0.0f))) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, s[i] - kSumTop);
+          const float step = QUANT ? lo_half(x.vm[i]) : 1.0f;
+          if (step > 0.0f) top = fmaxf(top, s[i] + __builtin_amdgcn_logf(step) - kTop);
+        }
+        top = max_groups(top);
+        const bool none = sum_groups(l) == 0.0f;
+        const float up = top == -INFINITY ? 0.0f : (none ? top : fmaxf(top, 0.0f));
+        const float alpha = none ? 1.0f : __builtin_amdgcn_exp2f(-up);
+        m += up;
+        l *= alpha;
+        olo *= alpha;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] -= up;
+        weights();
       }
-      l *= alpha;
-      omid *= alpha;
-      m = mn;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) o[t] *= beta;
-      psum *= beta;
-    }
-
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float w[8];
+      l += sum;
       v8h p;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float e = __builtin_amdgcn_exp2f(s[u][i] - m);
-        l += e;
-        if constexpr (QUANT) {
-          // The step goes into the weight, the codes' midpoint apart.
-          const float step = lo_half(vm[u][i]);
-          omid = __builtin_fmaf(e, __builtin_fmaf(step, Codes<BITS>::mid, hi_half(vm[u][i])), omid);
-          w[i] = e * (step * inv_ref);
-        } else {
-          w[i] = e;
-        }
+        if constexpr (QUANT) olo = __builtin_fmaf(e[i], hi_half(x.vm[i]), olo);
+        p[i] = static_cast<_Float16>(w[i]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = static_cast<_Float16>(w[i]);
       // Columns 8 .. 15 take the remainders.
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = static_cast<_Float16>(__builtin_fmaf(-frem, static_cast<float>(p[i]), w[i]));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const v8h vf = as_v8h(A::v_pair(vw[u][0], vw[u][1], t), A::v_pair(vw[u][2], vw[u][3], t),
-                              A::v_pair(vw[u][4], vw[u][5], t), A::v_pair(vw[u][6], vw[u][7], t));
+        if (t % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+        const v8h vf = as_v8h(A::v_pair(x.v[0], x.v[1], t), A::v_pair(x.v[2], x.v[3], t),
+                              A::v_pair(x.v[4], x.v[5], t), A::v_pair(x.v[6], x.v[7], t));
         o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p, o[t], 0, 0, 0);
       }
-      if constexpr (QUANT) {
-        const v8h ones = as_v8h(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u);
-        psum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p, psum, 0, 0, 0);
+    };
+    if (hs > 0 && tile < w.t1) {
+      if constexpr (!EARLY) load(x, w, tile, g, col);
+      // The last load of a row reads its last tile again: without a branch
+      // around it, what is in flight is known, and only what is used is waited
+      // for.
+      while (true) {
+        load(y, w, min(tile + per, w.t1 - 1), g, col);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(x, tile);
+        tile += per;
+        if (tile >= w.t1) break;
+        load(x, w, min(tile + per, w.t1 - 1), g, col);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(y, tile);
+        tile += per;
+        if (tile >= w.t1) break;
       }
     }
-  }
-
-  // The wave's sums in the values' own units.
-  l = sum_groups(l);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[t][r] += lane_xor<8>(o[t][r]);
-  }
-  if constexpr (QUANT) {
-    omid = sum_groups(omid) - (psum[0] + lane_xor<8>(psum[0])) * (ref * Codes<BITS>::mid);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float unit = ref * ((BITS == 4 && (t & 1)) ? Codes<BITS>::unit / 16.0f : Codes<BITS>::unit);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[t][r] = __builtin_fmaf(o[t][r], unit, omid);
-    }
-  }
-  if (lane < kTileHeads) lds_ml[wave * kTileHeads + lane] = make_float2(m, l);
-  if (col < hs) {
-    float* dst = lds_o + (wave * hs + col) * (D + 4);
+    // The wave's sums in the values' own units, then the waves of each head tile.
+    l = sum_groups(l);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dst[A::v_channel(t, 4 * g + r)] = o[t][r];
+      for (int i = 0; i < 4; ++i) {
+        // An infinite value of V times a remainder of 0 is a NaN that is not the sum's.
+        const float both = o[t][i] + lane_xor<8>(o[t][i]);
+        o[t][i] = both == both ? both : o[t][i];
+      }
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < hs * D; i += kAttnThreads) {
-    const int hd = i / D, d = i % D;
-    float mx = kNoRef;
+    if constexpr (QUANT) {
+      olo = sum_groups(olo);
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mx = fmaxf(mx, lds_ml[w * kTileHeads + hd].x);
-    float sum = 0.0f, acc = 0.0f;
+      for (int t = 0; t < NT; ++t) {
+        constexpr float unit = Codes<BITS>::v_unit;
+        const float f = (BITS == 4 && (t & 1)) ? unit / 16.0f : unit;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float2 ml = lds_ml[w * kTileHeads + hd];
-      const float f = __builtin_amdgcn_exp2f(ml.x - mx);
-      sum = __builtin_fmaf(ml.y, f, sum);
-      acc = __builtin_fmaf(lds_o[(w * hs + hd) * (D + 4) + d], f, acc);
+        for (int i = 0; i < 4; ++i) o[t][i] = __builtin_fmaf(o[t][i], f, olo);
+      }
     }
-    if (a.splits == 1) a.out[(head0 + hd) * D + d] = f2h(sum == 0.0f ? 0.0f : div_rn(acc, sum));
-    if (a.splits > 1) a.part_o[((head0 + hd) * a.splits + split) * D + d] = acc;
-    if (d == 0 && a.part_ml != nullptr) a.part_ml[(head0 + hd) * a.splits + split] = make_float2(mx, sum);
+    const int lds_heads = min(hrow, kTileHeads);
+    if (lane < kTileHeads) lds_ml[wave * kTileHeads + lane] = make_float2(l == 0.0f ? kNoRef : m, l);
+    if (col < hs) {
+      float* dst = lds_o + (wave * lds_heads + col) * (D + 4);
+#pragma unroll
+      for (int t = 0; t < NT; t += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(dst + A::v_channel(t, 4 * g + i)) =
+              make_float4(o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]);
+      }
+    }
+    const bool whole = w.t1 - w.t0 == w.tiles;
+    lds_barrier();
+    const int64_t slot = whole ? 0 : part_slot(blockIdx.x, row_at, share) * a.row_heads;
+    for (int i = tid; i < hrow * (D / 4); i += kAttnThreads) {
+      const int hd = i / (D / 4), d = i % (D / 4) * 4, w0 = hd / kTileHeads * per, hl = hd % kTileHeads;
+      float mx = kNoRef;
+      for (int v = w0; v < w0 + per; ++v) mx = fmaxf(mx, lds_ml[v * kTileHeads + hl].x);
+      float sum = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int v = w0; v < w0 + per; ++v) {
+        const float2 ml = lds_ml[v * kTileHeads + hl];
+        const float4 u = *reinterpret_cast<const float4*>(lds_o + (v * lds_heads + hl) * (D + 4) + d);
+        const float f = __builtin_amdgcn_exp2f(ml.x - mx);
+        sum = __builtin_fmaf(ml.y, f, sum);
+        acc.x = __builtin_fmaf(u.x, f, acc.x);
+        acc.y = __builtin_fmaf(u.y, f, acc.y);
+        acc.z = __builtin_fmaf(u.z, f, acc.z);
+        acc.w = __builtin_fmaf(u.w, f, acc.w);
+      }
+      if (whole) {
+        *reinterpret_cast<uint2*>(a.out + (head0 + hd) * D + d) = out4(acc, sum);
+        if (LOGITS && d == 0) a.head_ml[head0 + hd] = make_float2(mx, sum);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot + hd) * D + d) = acc;
+        if (d == 0) a.part_ml[slot + hd] = make_float2(mx, sum);
+      }
+    }
+    if (a.groups == 0) return;
+    // A row that begins here says where its first part is, and its last workgroup.
+    const int last_group = whole ? blockIdx.x : static_cast<int>(attn_div(row_at + w.tiles - 1, share));
+    if (tid == 0 && at <= row_at)
+      a.runs[static_cast<int64_t>(b) * rows_b + r] =
+          make_int2(static_cast<int>(part_slot(blockIdx.x, row_at, share)), last_group);
+    row_at = uniform_i64(row_at + w.tiles);
+    if (row_at >= stop) return;
+    at = row_at;
+    if (++r == rows_b) {
+      r = 0;
+      int next_low, next_n;
+      do {  // the next sequence with a tile; there is one, as row_at < stop
+        ++b;
+        attn_range(a, scalar_i32(a.lens + b), next_low, next_n);
+      } while (next_n == 0);
+    }
+    lds_barrier();  // lds_o and lds_ml are read
   }
 }
 
-// Joins the chunks of a head (blocks below B * heads, when there are several),
-// then adds the heads' weights of each slot to mass (the other blocks).
+// Per (row, kv head): the first join_blocks workgroups (one for each query head
+// of the group, or none) join the parts of a row that several workgroups took;
+// each of the others adds the group's weights of kMassSlots slots to mass.
 constexpr int kJoinThreads = 256;
-constexpr int kMassSlots = 1024;
+constexpr int kMassSlots = 4 * kJoinThreads;
+
+// The parts of one query head of a row: index of part i in part_ml.
+struct Parts {
+  int64_t first, rest;
+  int count, step;
+  __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? first : rest + static_cast<int64_t>(i) * step; }
+};
+__device__ __forceinline__ Parts attn_parts(const AttnArgs& a, int64_t row, int hd) {
+  if (a.groups == 0) return Parts{0, 0, 1, 0};
+  const int2 run = a.runs[row];
+  const int w0 = run.x >> 1;
+  return Parts{static_cast<int64_t>(run.x) * a.row_heads + hd, static_cast<int64_t>(2 * w0) * a.row_heads + hd,
+               run.y - w0 + 1, 2 * a.row_heads};
+}
 
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int64_t join_blocks, int mass_blocks) {
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int join_blocks) {
+  constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
   __shared__ float4 acc_lds[kJoinThreads];
   __shared__ float red[kJoinThreads / 64];
-  __shared__ float sums[16];  // ROWS of them: 16, 8 or 4
-  __shared__ float2 head_ml[16];
+  __shared__ float sums[ROWS];
+  __shared__ float2 head_ml[kRowHeads];
   const int tid = threadIdx.x;
-  if (blockIdx.x < join_blocks) {
-    const int64_t head = blockIdx.x;  // b * heads + query head
-    int low, n;
-    attn_range(a, head / a.heads, low, n);
-    const int used = n <= 0 ? 0 : (n - attn_base(low) + a.chunk - 1) / a.chunk;
-    const float2* ml = a.part_ml + head * a.splits;
+  const int h = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  int low, n;
+  attn_range(a, scalar_i32(a.lens + b), low, n);
+  if (static_cast<int>(blockIdx.x) < join_blocks) {
+    const int hd = blockIdx.x;
+    uint2* out = reinterpret_cast<uint2*>(a.out + (b * a.heads + h * a.group + hd) * D);
+    if (n == 0) {
+      if (tid < LANES) out[tid] = make_uint2(0, 0);
+      return;
+    }
+    const Parts p = attn_parts(a, (b * a.c.heads + h) * a.parts + hd / kRowHeads, hd % kRowHeads);
+    if (p.count == 1) return;
     float mx = kNoRef;
-    for (int i = tid; i < used; i += kJoinThreads) mx = fmaxf(mx, ml[i].x);
+    for (int i = tid; i < p.count; i += kJoinThreads) mx = fmaxf(mx, a.part_ml[p.at(i)].x);
     mx = wave_max(mx);
     if ((tid & 63) == 0) red[tid >> 6] = mx;
     __syncthreads();
     mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
     const int d4 = tid % LANES, r0 = tid / LANES;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + head * a.splits * D) + d4;
     float sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = r0; i < used; i += ROWS) {
-      const float2 x = ml[i];
+#pragma unroll 4
+    for (int i = r0; i < p.count; i += ROWS) {
+      const int64_t at = p.at(i);
+      const float2 x = a.part_ml[at];
+      const float4 v = reinterpret_cast<const float4*>(a.part_o + at * D)[d4];
       const float f = __builtin_amdgcn_exp2f(x.x - mx);
-      const float4 v = po[static_cast<int64_t>(i) * LANES];
       sum = __builtin_fmaf(x.y, f, sum);
       acc.x = __builtin_fmaf(v.x, f, acc.x);
       acc.y = __builtin_fmaf(v.y, f, acc.y);
@@ -559,119 +751,128 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
         total += sums[i];
         t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
       }
-      const bool none = total == 0.0f;
-      uint2 w;
-      w.x = f2h(none ? 0.0f : div_rn(t.x, total)) | static_cast<uint32_t>(f2h(none ? 0.0f : div_rn(t.y, total))) << 16;
-      w.y = f2h(none ? 0.0f : div_rn(t.z, total)) | static_cast<uint32_t>(f2h(none ? 0.0f : div_rn(t.w, total))) << 16;
-      reinterpret_cast<uint2*>(a.out + head * D)[tid] = w;
+      out[tid] = out4(t, total);
     }
     return;
   }
   // mass of slots [s0, s0 + kMassSlots) of one (row, kv head)
-  const int64_t idx = blockIdx.x - join_blocks;
-  const int64_t bh = idx / mass_blocks;
-  const int s0 = static_cast<int>(idx % mass_blocks) * kMassSlots;
-  const int64_t b = bh / a.c.heads;
-  const int h = static_cast<int>(bh % a.c.heads);
-  int low, n;
-  attn_range(a, b, low, n);
+  const int64_t bh = b * a.c.heads + h;
+  const int s0 = (static_cast<int>(blockIdx.x) - join_blocks) * kMassSlots;
   if (s0 >= n) return;  // uniform
-  const int base = attn_base(low);
-  const int used = (n - base + a.chunk - 1) / a.chunk;
   const int64_t head0 = b * a.heads + h * a.group;
-  float w[kMassSlots / kJoinThreads];
-#pragma unroll
-  for (int i = 0; i < kMassSlots / kJoinThreads; ++i) w[i] = 0.0f;
-  for (int h0 = 0; h0 < a.group; h0 += 16) {
-    const int hs = min(16, a.group - h0);
+  const int slot0 = s0 + 4 * tid;  // four slots of each thread
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int h0 = 0; h0 < a.group; h0 += kRowHeads) {
+    const int hs = min(kRowHeads, a.group - h0);
     __syncthreads();
-    // Each wave takes heads in turn: maximum, then sum, over the chunks.
+    // Each wave takes heads in turn: maximum, then sum, over the parts.
     for (int hd = tid >> 6; hd < hs; hd += kJoinThreads / 64) {
-      const float2* ml = a.part_ml + (head0 + h0 + hd) * a.splits;
-      float mx = kNoRef;
-      for (int i = tid & 63; i < used; i += 64) mx = fmaxf(mx, ml[i].x);
-      mx = wave_max(mx);
-      float sum = 0.0f;
-      for (int i = tid & 63; i < used; i += 64) sum = __builtin_fmaf(ml[i].y, __builtin_amdgcn_exp2f(ml[i].x - mx), sum);
+      const Parts p = attn_parts(a, bh * a.parts + h0 / kRowHeads, hd);
+      float mx, sum;
+      if (p.count == 1) {
+        const float2 ml = a.head_ml[head0 + h0 + hd];
+        mx = ml.x;
+        sum = ml.y;
+      } else {
+        mx = kNoRef;
+        for (int i = tid & 63; i < p.count; i += 64) mx = fmaxf(mx, a.part_ml[p.at(i)].x);
+        mx = wave_max(mx);
+        sum = 0.0f;
+        for (int i = tid & 63; i < p.count; i += 64) {
+          const float2 ml = a.part_ml[p.at(i)];
+          sum = __builtin_fmaf(ml.y, __builtin_amdgcn_exp2f(ml.x - mx), sum);
+        }
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      }
       if ((tid & 63) == 0) head_ml[hd] = make_float2(mx, sum == 0.0f ? 0.0f : div_rn(1.0f, sum));
     }
-    __syncthreads();
-    for (int hd = 0; hd < hs; ++hd) {
-      const float2 ml = head_ml[hd];
-      const float* lp = a.logits + (head0 + h0 + hd) * a.ld_logits;
+    // Four heads' logits at a time; a group's last ones again past its end.
+    const float* lp = a.logits + (head0 + h0) * a.ld_logits + slot0;
+    for (int hd = 0; hd < hs; hd += 4) {
+      float4 s[4];
 #pragma unroll
-      for (int i = 0; i < kMassSlots / kJoinThreads; ++i) {
-        const int slot = s0 + i * kJoinThreads + tid;
-        if (slot >= low && slot < n) w[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(lp[slot] - ml.x), ml.y, w[i]);
+      for (int i = 0; i < 4; ++i)
+        s[i] = slot0 < a.ld_logits ? *reinterpret_cast<const float4*>(lp + min(hd + i, hs - 1) * a.ld_logits)
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (hd == 0) __syncthreads();  // head_ml
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (hd + i < hs) {
+          const float2 ml = head_ml[hd + i];
+          w[0] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].x - ml.x), ml.y, w[0]);
+          w[1] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].y - ml.x), ml.y, w[1]);
+          w[2] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].z - ml.x), ml.y, w[2]);
+          w[3] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].w - ml.x), ml.y, w[3]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kMassSlots / kJoinThreads; ++i) {
-    const int slot = s0 + i * kJoinThreads + tid;
+  for (int i = 0; i < 4; ++i) {
+    const int slot = slot0 + i;
     if (slot < n && slot < a.ld_mass) {
       const int64_t at = bh * a.ld_mass + slot;
-      a.mass_out[at] = (a.mass_in != nullptr ? a.mass_in[at] : 0.0f) + w[i];
+      // Logits outside the range were never written.
+      a.mass_out[at] = (a.mass_in != nullptr ? a.mass_in[at] : 0.0f) + (slot >= low ? w[i] : 0.0f);
     }
   }
 }
 
 struct AttnPlan {
-  int chunk, splits, head_tiles;
+  int parts, row_heads, groups;
   int64_t ld_logits;
-  size_t o_bytes, ml_bytes, logit_bytes;
+  size_t run_bytes, ml_bytes, head_bytes, o_bytes, logit_bytes;
+  size_t total() const { return run_bytes + ml_bytes + head_bytes + o_bytes + logit_bytes; }
 };
 
-// Slots a wave takes at a time, times the waves: the unit of a chunk.
-inline int attn_unit(const qlin_kv_cache& c) { return kAttnWaves * 32 * ((c.bits == 4 && c.head_dim <= 128) ? 2 : 1); }
+inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Rows of at most this many tiles are one workgroup each: no second launch.
+constexpr int64_t kWholeTiles = 8;
 
 AttnPlan attn_plan(const qlin_kv_cache& c, int32_t heads, int64_t B, int64_t max_len, int32_t window, bool mass) {
   AttnPlan p;
   const int group = heads / c.kv_heads;
-  p.head_tiles = (group + kTileHeads - 1) / kTileHeads;
-  // A window may begin 31 slots into its first 32-slot block.
-  int64_t span = max_len;
-  if (window > 0 && window + 31 < span) span = window + 31;
-  if (span < 1) span = 1;
-  const int unit = attn_unit(c);
-  // Workgroups for every CU several times over, so that ragged rows even out;
-  // but no chunk below two units, where the fixed work would show, and none
-  // above kMaxChunk.
-  const int64_t rows = B * c.kv_heads * p.head_tiles;
-  int64_t chunk = (span * rows + 2047) / 2048;
-  chunk = (chunk + unit - 1) / unit * unit;
-  if (chunk < 2 * unit) chunk = 2 * unit;
-  if (chunk > kMaxChunk) chunk = kMaxChunk;
-  p.chunk = static_cast<int>(chunk);
-  p.splits = static_cast<int>((span + chunk - 1) / chunk);
+  p.parts = (group + kRowHeads - 1) / kRowHeads;
+  p.row_heads = group < kRowHeads ? group : kRowHeads;
+  int64_t tiles = (max_len + kTile - 1) / kTile;
+  if (window > 0) {  // a window may begin inside a tile
+    const int64_t w = (static_cast<int64_t>(window) + kTile - 2) / kTile + 1;
+    tiles = w < tiles ? w : tiles;
+  }
+  const int64_t rows = B * c.kv_heads * p.parts;
+  const int64_t most = int64_t(kCus) * attn_resident(c.head_dim);
+  const int64_t runs = (rows * tiles + kAttnWaves - 1) / kAttnWaves;
+  p.groups = tiles <= kWholeTiles ? 0 : static_cast<int>(runs < most ? runs : most);
+  const size_t parts = static_cast<size_t>(2) * p.groups * p.row_heads;
   const size_t n = static_cast<size_t>(B) * heads;
-  p.o_bytes = p.splits > 1 ? n * p.splits * c.head_dim * sizeof(float) : 0;
-  p.ml_bytes = (p.splits > 1 || mass) ? (n * p.splits * sizeof(float2) + 255) / 256 * 256 : 0;
-  p.ld_logits = (max_len + 31) / 32 * 32;
+  p.run_bytes = p.groups ? up256(static_cast<size_t>(rows) * sizeof(int2)) : 0;
+  p.ml_bytes = up256(parts * sizeof(float2));
+  p.o_bytes = up256(parts * c.head_dim * sizeof(float));
+  p.head_bytes = mass ? up256(n * sizeof(float2)) : 0;
+  p.ld_logits = (max_len + kTile - 1) / kTile * kTile;
   p.logit_bytes = mass ? n * static_cast<size_t>(p.ld_logits) * sizeof(float) : 0;
   return p;
 }
 
 template <int BITS, int D, bool ROT>
-void launch_split(const AttnArgs& a, int64_t blocks, hipStream_t st) {
-  const size_t lds = attn_lds(D, a.group, ROT);
-  const dim3 grid(static_cast<unsigned>(blocks));
+void launch_attn(const AttnArgs& a, const dim3 grid, hipStream_t st) {
+  const size_t lds = attn_lds(D, a.row_heads, ROT);
   if (a.logits != nullptr)
-    attn_split_kernel<BITS, D, ROT, true><<<grid, kAttnThreads, lds, st>>>(a);
+    attn_kernel<BITS, D, ROT, true><<<grid, kAttnThreads, lds, st>>>(a);
   else
-    attn_split_kernel<BITS, D, ROT, false><<<grid, kAttnThreads, lds, st>>>(a);
+    attn_kernel<BITS, D, ROT, false><<<grid, kAttnThreads, lds, st>>>(a);
 }
 
 template <int BITS>
-void launch_bits(const AttnArgs& a, int D, int64_t blocks, hipStream_t st) {
-  if (D == 64) return launch_split<BITS, 64, false>(a, blocks, st);
-  if (D == 256) return launch_split<BITS, 256, false>(a, blocks, st);
+void launch_bits(const AttnArgs& a, int D, const dim3 grid, hipStream_t st) {
+  if (D == 64) return launch_attn<BITS, 64, false>(a, grid, st);
+  if (D == 256) return launch_attn<BITS, 256, false>(a, grid, st);
   if constexpr (BITS < 16) {
-    if (a.c.signs != nullptr) return launch_split<BITS, 128, true>(a, blocks, st);
+    if (a.c.signs != nullptr) return launch_attn<BITS, 128, true>(a, grid, st);
   }
-  launch_split<BITS, 128, false>(a, blocks, st);
+  launch_attn<BITS, 128, false>(a, grid, st);
 }
 
 }  // namespace
@@ -681,11 +882,11 @@ using namespace qlin;
 
 extern "C" size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, int64_t B, int64_t max_len,
                                               int32_t window, int32_t mass) {
-  if (!kv_shape_ok(cache) || heads < 1 || heads % cache->kv_heads != 0 || B < 1 || max_len < 0 || window < 0 ||
+  if (!kv_shape_ok(cache) || heads < 1 || heads % cache->kv_heads != 0 || B < 1 || max_len < 0 || max_len > kMaxDim / 2 || window < 0 ||
       !dims_ok(B, max_len) || !dims_ok(B * heads, max_len + 1) || !dims_ok(B * heads, cache->head_dim))
     return 0;
   const AttnPlan p = attn_plan(*cache, heads, B, max_len, window, mass != 0);
-  return p.o_bytes + p.ml_bytes + p.logit_bytes;
+  return p.total();
 }
 
 extern "C" qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16_t* q, int64_t ld_q, int32_t heads,
@@ -703,8 +904,10 @@ extern "C" qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16
   QLIN_REQUIRE(max_len >= 0, QLIN_ERR_INVALID_ARG, "max_len=%lld is negative", (long long)max_len);
   QLIN_REQUIRE(max_len <= max_pages * cache->page, QLIN_ERR_SHAPE, "max_len=%lld: the table holds %lld slots",
                (long long)max_len, (long long)(max_pages * cache->page));
+  QLIN_REQUIRE(max_len <= kMaxDim / 2, QLIN_ERR_SHAPE, "max_len=%lld: at most 2^30", (long long)max_len);
   QLIN_REQUIRE(window >= 0, QLIN_ERR_INVALID_ARG, "window=%d is negative", window);
   QLIN_REQUIRE(scale == scale, QLIN_ERR_INVALID_ARG, "scale is NaN");
+  QLIN_REQUIRE(B <= 65535, QLIN_ERR_SHAPE, "B=%lld: at most 65535", (long long)B);
   QLIN_REQUIRE(B * heads < kMaxDim, QLIN_ERR_SHAPE, "B * heads: at most 2^31 - 1");
   QLIN_DIMS(B * heads, max_len + 1);
   const bool mass = mass_out != nullptr;
@@ -721,13 +924,12 @@ extern "C" qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16
   QLIN_OPT_PTR(mass_in);
   QLIN_OPT_PTR(mass_out);
   const AttnPlan p = attn_plan(*cache, heads, B, max_len, window, mass);
-  const int64_t rest = B * cache->kv_heads * p.splits;
-  const int64_t blocks = p.head_tiles == 1 ? rest : (rest + 7) / 8 * 8 * p.head_tiles;
-  const int mass_blocks = static_cast<int>((max_len + kMassSlots - 1) / kMassSlots);
-  const int64_t join = p.splits > 1 ? B * heads : 0;
-  const int64_t join_blocks = join + (mass ? B * cache->kv_heads * mass_blocks : 0);
-  QLIN_REQUIRE(blocks < kMaxDim && join_blocks < kMaxDim, QLIN_ERR_SHAPE, "B * heads * max_len too large");
-  if (p.o_bytes + p.ml_bytes + p.logit_bytes > 0) QLIN_PTR(work);
+  const int64_t rows = B * cache->kv_heads * p.parts;
+  QLIN_REQUIRE(rows < kMaxDim, QLIN_ERR_SHAPE, "B * kv_heads: fewer than 2^31");
+  const dim3 grid(static_cast<unsigned>(p.groups ? p.groups : rows));
+  const int join_blocks = p.groups ? heads / cache->kv_heads : 0;
+  const int mass_blocks = mass ? static_cast<int>((max_len + kMassSlots - 1) / kMassSlots) : 0;
+  if (p.total() > 0) QLIN_PTR(work);
 
   uint8_t* w = static_cast<uint8_t*>(work);
   AttnArgs a{};
@@ -747,29 +949,37 @@ extern "C" qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.ld_mass = ld;
-  a.chunk = p.chunk;
-  a.splits = p.splits;
-  a.head_tiles = p.head_tiles;
-  a.part_o = p.o_bytes ? reinterpret_cast<float*>(w) : nullptr;
-  a.part_ml = p.ml_bytes ? reinterpret_cast<float2*>(w + p.o_bytes) : nullptr;
-  a.logits = p.logit_bytes ? reinterpret_cast<float*>(w + p.o_bytes + p.ml_bytes) : nullptr;
+  a.parts = p.parts;
+  a.groups = p.groups;
+  a.row_heads = p.row_heads;
   a.ld_logits = p.ld_logits;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = bytes ? w : nullptr;
+    w += bytes;
+    return at;
+  };
+  a.runs = reinterpret_cast<int2*>(take(p.run_bytes));
+  a.part_ml = reinterpret_cast<float2*>(take(p.ml_bytes));
+  a.part_o = reinterpret_cast<float*>(take(p.o_bytes));
+  a.head_ml = reinterpret_cast<float2*>(take(p.head_bytes));
+  a.logits = reinterpret_cast<float*>(take(p.logit_bytes));
   hipStream_t st = as_stream(stream);
   if (cache->bits == 16)
-    launch_bits<16>(a, cache->head_dim, blocks, st);
+    launch_bits<16>(a, cache->head_dim, grid, st);
   else if (cache->bits == 8)
-    launch_bits<8>(a, cache->head_dim, blocks, st);
+    launch_bits<8>(a, cache->head_dim, grid, st);
   else
-    launch_bits<4>(a, cache->head_dim, blocks, st);
-  QLIN_LAUNCH_CHECK("attn_split_kernel");
-  if (join_blocks > 0) {
-    const dim3 grid(static_cast<unsigned>(join_blocks));
+    launch_bits<4>(a, cache->head_dim, grid, st);
+  QLIN_LAUNCH_CHECK("attn_kernel");
+  if (join_blocks + mass_blocks > 0) {
+    const dim3 jgrid(static_cast<unsigned>(join_blocks + mass_blocks), static_cast<unsigned>(cache->kv_heads),
+                     static_cast<unsigned>(B));
     if (cache->head_dim == 64)
-      attn_join_kernel<64><<<grid, kJoinThreads, 0, st>>>(a, join, mass_blocks);
+      attn_join_kernel<64><<<jgrid, kJoinThreads, 0, st>>>(a, join_blocks);
     else if (cache->head_dim == 128)
-      attn_join_kernel<128><<<grid, kJoinThreads, 0, st>>>(a, join, mass_blocks);
+      attn_join_kernel<128><<<jgrid, kJoinThreads, 0, st>>>(a, join_blocks);
     else
-      attn_join_kernel<256><<<grid, kJoinThreads, 0, st>>>(a, join, mass_blocks);
+      attn_join_kernel<256><<<jgrid, kJoinThreads, 0, st>>>(a, join_blocks);
     QLIN_LAUNCH_CHECK("attn_join_kernel");
   }
   return QLIN_OK;

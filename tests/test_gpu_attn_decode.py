@@ -134,6 +134,33 @@ def test_groups(q, group):
         _check(q, c, group, seed=group)
 
 
+def test_more_query_heads_than_a_workgroup_takes(q):
+    for group in (33, 40, 64):
+        rng = np.random.default_rng(group)
+        log(f"attend group={group}")
+        c = HostCache(rng, [5, 700, 0, 300], 700, 2, 64, 16, 8)
+        _check(q, c, group, seed=group)
+        c = HostCache(rng, [5, 100], 100, 1, 64, 16, 8)  # one workgroup a row
+        _check(q, c, group, seed=group)
+
+
+@pytest.mark.parametrize("B", [63, 65, 200])
+def test_many_ragged_sequences(q, B):
+    # Runs of tiles that begin and end anywhere, idle rows at both ends and
+    # between, and more sequences than a wave has lanes.
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 900, B)
+    lens[rng.random(B) < 0.3] = 0
+    lens[:2], lens[-2:] = 0, 0
+    log(f"attend B={B}")
+    _check(q, HostCache(rng, lens, 900, 1, 64, 32, 4), 2, seed=B)
+    lens[:] = 0
+    lens[B // 2] = 600
+    _check(q, HostCache(rng, lens, 900, 3, 64, 16, 16), 1, seed=B)
+    lens[:] = 0
+    _check(q, HostCache(rng, lens, 900, 1, 64, 16, 16), 1, seed=B)
+
+
 @pytest.mark.parametrize("window", [1, 31, 32, 100, 511, 5000])
 def test_windows(q, window):
     for bits in (16, 8, 4):
