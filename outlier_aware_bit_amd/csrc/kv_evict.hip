@@ -32,9 +32,11 @@ struct EvictArgs {
   int32_t move_cap;
 };
 
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kCopies = 32;                 // of the digit counts, one per lane pair
-constexpr int kKeysMax = 24576;             // keys held in LDS (96 KiB)
+// Digit counts are kept in copies, one for every eighth lane: the masses of a
+// row share their leading digits, and lanes that count into one word wait for
+// each other.  A copy holds the counts from digit 255 down; copies begin eight
+// banks apart.
+constexpr int kCopies = 8, kCopyLd = 264;
 
 __device__ __forceinline__ int evict_len(const EvictArgs& a, int64_t b) {
   const int64_t cap = a.max_pages << a.c.page_shift;
@@ -53,32 +55,103 @@ __device__ __forceinline__ uint32_t evict_key(float mass, int32_t pos, int64_t n
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sums over the waves of per-wave counts; every thread gets its
-// wave's.  lds holds kSelWaves words; total is the whole sum.
-__device__ __forceinline__ int wave_base(int count, int* lds, int& total) {
-  const int w = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[w] = count;
-  __syncthreads();
-  int base = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSelWaves; ++i) {
-    const int x = lds[i];
-    base += i < w ? x : 0;
-    total += x;
-  }
-  return base;
+__device__ __forceinline__ int lanes_below(uint64_t mask) {  // set bits below the lane's
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+}
+// Maximum over the lanes, in every lane.
+__device__ __forceinline__ int max_wave(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xF, 0xF, false));  // one lane up, in rows of 16
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x112, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x114, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x118, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xA, 0xF, false));  // lane 15 to rows 1 and 3
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));  // lane 31 to rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // one lane up, in rows of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  return v;
 }
 
-template <bool KEYS_IN_LDS>
-__global__ __launch_bounds__(kSelThreads) void kv_select_kernel(EvictArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[256 * kCopies];
-  __shared__ uint32_t bins[256];
-  __shared__ int small[kSelWaves];
-  __shared__ uint32_t found[2];
-  __shared__ int newest_lds[kSelWaves];
+// Rows of which no more bytes than this can move are moved by the workgroup
+// that selected them.
+constexpr int64_t kOwnMoveBytes = 16384;
+constexpr int kMoveThreads = 256;
+constexpr int kMovesAtOnce = 4;
+
+// A row's moves, by `groups` workgroups of THREADS of which this is number
+// `group`: each takes neighbouring moves, whose slots lie close together.  LANES
+// lanes copy a slot's K and V rows, 16 bytes each, several slots at a time so
+// that their loads wait together; two lanes take its mass and position as well.
+template <int RB, int THREADS>
+__device__ __forceinline__ void move_slots(const EvictArgs& a, int64_t row, const int32_t* from, const int32_t* to,
+                                           int count, int group, int groups) {
+  constexpr int HALF = RB / 16, LANES = 2 * HALF, step = THREADS / LANES;
+  const int first = group * kMovesAtOnce * step + threadIdx.x / LANES;
+  const int64_t b = row / a.c.heads;
+  const int h = static_cast<int>(row - b * a.c.heads);
+  const int ps = a.c.page_shift, mask = (1 << ps) - 1;
+  const int l = threadIdx.x % LANES, piece = l < HALF ? l : l - HALF;
+  const int32_t* table = a.table + b * a.max_pages;
+  uint8_t* pool = l < HALF ? a.c.k : a.c.v;
+  uint32_t* metas = l < HALF ? a.c.kmeta : a.c.vmeta;
+  const uint32_t* tracked = reinterpret_cast<const uint32_t*>(l == 0 ? static_cast<const void*>(a.mass) : a.pos) + row * a.ld;
+  uint32_t* tracked_out = reinterpret_cast<uint32_t*>(l == 0 ? static_cast<void*>(a.mass_out) : a.pos_out) + row * a.ld;
+  for (int i0 = first; i0 < count; i0 += groups * kMovesAtOnce * step) {
+    int src[kMovesAtOnce], dst[kMovesAtOnce];
+    int64_t s[kMovesAtOnce], d[kMovesAtOnce];
+    bool ok[kMovesAtOnce];
+    v4i w[kMovesAtOnce];
+    uint32_t m[kMovesAtOnce], t[kMovesAtOnce];
+#pragma unroll
+    for (int u = 0; u < kMovesAtOnce; ++u) {
+      const int i = min(i0 + u * step, count - 1);
+      src[u] = from[i];
+      dst[u] = to[i];
+    }
+#pragma unroll
+    for (int u = 0; u < kMovesAtOnce; ++u) {
+      const int64_t sp = table[src[u] >> ps], dp = table[dst[u] >> ps];
+      ok[u] = i0 + u * step < count && sp >= 0 && sp < a.c.pages && dp >= 0 && dp < a.c.pages;
+      s[u] = (((ok[u] ? sp : 0) * a.c.heads + h) << ps) + (src[u] & mask);
+      d[u] = (((ok[u] ? dp : 0) * a.c.heads + h) << ps) + (dst[u] & mask);
+    }
+#pragma unroll
+    for (int u = 0; u < kMovesAtOnce; ++u) {
+      w[u] = reinterpret_cast<const v4i*>(pool + s[u] * RB)[piece];
+      m[u] = (metas != nullptr && piece == 0) ? metas[s[u]] : 0;
+      t[u] = l < 2 ? tracked[src[u]] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kMovesAtOnce; ++u) {
+      if (ok[u]) {
+        reinterpret_cast<v4i*>(pool + d[u] * RB)[piece] = w[u];
+        if (metas != nullptr && piece == 0) metas[d[u]] = m[u];
+      }
+      if (i0 + u * step < count) {
+        if (l < 2) tracked_out[dst[u]] = t[u];
+        if (l == 2) a.kept[row * a.budget + dst[u]] = src[u];
+      }
+    }
+  }
+}
+
+// Selects the slots of one row.  Each wave holds a contiguous part of it, up to
+// STEPS times 64 slots in registers (STEPS == 0: any number, read from memory
+// each time).  RB > 0: the workgroup moves the rows as well.
+template <int THREADS, int STEPS, int RB>
+__global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ uint4 hist4[2][kCopyLd * kCopies / 4];
+  __shared__ int newest_lds[WAVES], ties_lds[WAVES];
+  __shared__ int2 counts_lds[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
   const int64_t b = row / a.c.heads;
@@ -89,183 +162,205 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_kernel(EvictArgs a) {
   float* mass_out = a.mass_out + row * a.ld;
   int32_t* pos_out = a.pos_out + row * a.ld;
   int32_t* kept = a.kept + row * a.budget;
-  if (tid == 0 && row % a.c.heads == 0) a.lens_out[b] = left;
-  for (int i = left + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
-  if (n <= left) {  // uniform: nothing goes
-    for (int i = tid; i < n; i += kSelThreads) {
-      kept[i] = i;
-      mass_out[i] = mass[i];
-      pos_out[i] = pos[i];
+  if (tid == 0 && row == b * a.c.heads) a.lens_out[b] = left;
+  for (int i = left + tid; i < a.budget; i += THREADS) kept[i] = -1;
+
+  const int steps = (n + THREADS - 1) / THREADS;  // STEPS at most where that is not 0
+  const int i0 = wave * steps * 64 + lane;
+  float mv[STEPS > 0 ? STEPS : 1];
+  int32_t pv[STEPS > 0 ? STEPS : 1];
+  auto slot = [&](int s) { return i0 + 64 * s; };
+  // each(f): f(step, slot, whether it is in the row) over the lane's slots.
+  auto each = [&](auto&& f) {
+    if constexpr (STEPS > 0) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+        if (s < steps) f(s, slot(s), slot(s) < n);  // uniform
+    } else {
+      for (int s = 0; s < steps; ++s) f(s, slot(s), slot(s) < n);
     }
-    if (tid == 0) a.count[row] = 0;
+  };
+  if constexpr (STEPS > 0) {
+    each([&](int s, int i, bool in) {
+      mv[s] = in ? mass[i] : 0.0f;
+      pv[s] = in ? pos[i] : INT32_MIN;
+    });
+  }
+  auto mass_at = [&](int s, int i) { return STEPS > 0 ? mv[s] : mass[i]; };
+  auto pos_at = [&](int s, int i) { return STEPS > 0 ? pv[s] : pos[i]; };
+  if (n <= left) {  // uniform: nothing goes
+    each([&](int s, int i, bool in) {
+      if (!in) return;
+      kept[i] = i;
+      mass_out[i] = mass_at(s, i);
+      pos_out[i] = pos_at(s, i);
+    });
+    if (RB == 0 && tid == 0) a.count[row] = 0;
     return;
   }
 
+  uint32_t* hist0 = reinterpret_cast<uint32_t*>(hist4[0]);
+  uint32_t* hist1 = reinterpret_cast<uint32_t*>(hist4[1]);
+  for (int i = tid; i < kCopyLd * kCopies / 4; i += THREADS) hist4[0][i] = make_uint4(0, 0, 0, 0);
   int newest = INT32_MIN;
-  for (int i = tid; i < n; i += kSelThreads) newest = max(newest, pos[i]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) newest = max(newest, __shfl_xor(newest, o, 64));
+  each([&](int s, int i, bool in) {
+    if (in) newest = max(newest, pos_at(s, i));
+  });
+  newest = max_wave(newest);
   if (lane == 0) newest_lds[wave] = newest;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSelWaves; ++i) newest = max(newest, newest_lds[i]);
+  for (int i = 0; i < WAVES; ++i) newest = max(newest, newest_lds[i]);
   const int64_t gone = static_cast<int64_t>(newest) - a.recent;  // positions up to here are not protected
-
-  if constexpr (KEYS_IN_LDS) {
-    for (int i = tid; i < n; i += kSelThreads) keys[i] = evict_key(mass[i], pos[i], gone);
-  }
-  auto key_of = [&](int i) { return KEYS_IN_LDS ? keys[i] : evict_key(mass[i], pos[i], gone); };
+  uint32_t kv[STEPS > 0 ? STEPS : 1];
+  if constexpr (STEPS > 0) each([&](int s, int, bool) { kv[s] = evict_key(mv[s], pv[s], gone); });
+  auto key_at = [&](int s, int i) { return STEPS > 0 ? kv[s] : evict_key(mass[i], pos[i], gone); };
 
   // The left-th largest key, digit by digit: `prefix` holds the digits found,
-  // `need` how many slots with that prefix stay.
-  uint32_t prefix = 0;
-  int need = left;
+  // `need` how many slots with that prefix stay.  Every wave sums the copies
+  // and finds the digit for itself; the next digit's counts are cleared
+  // meanwhile.
+  uint32_t prefix = 0, need = static_cast<uint32_t>(left);
+  bool all_stay = false;
+#pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kCopies; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
+    uint32_t* hist = (shift & 8) ? hist0 : hist1;
+    uint32_t* next = (shift & 8) ? hist1 : hist0;
     const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t k = key_of(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
-    }
+    each([&](int s, int i, bool in) {
+      if (!in) return;
+      const uint32_t k = key_at(s, i);
+      if ((k & mask) == prefix)
+        atomicAdd(&hist[(lane & (kCopies - 1)) * kCopyLd + (~(k >> shift) & 255u)], 1u);
+    });
     __syncthreads();
-    {  // four threads sum a digit's copies, from different banks
-      const int digit = tid >> 2, part = tid & 3;
-      uint32_t s = 0;
+    for (int i = tid; i < kCopyLd * kCopies / 4; i += THREADS) reinterpret_cast<uint4*>(next)[i] = make_uint4(0, 0, 0, 0);
+    // Lane l: digits 255 - 4l .. 252 - 4l, from the top.
+    uint32_t c[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < kCopies / 4; ++i) s += hist[digit * kCopies + ((part * (kCopies / 4) + i + digit) & (kCopies - 1))];
-      s += __shfl_xor(s, 1, 64);
-      s += __shfl_xor(s, 2, 64);
-      if (part == 0) bins[digit] = s;
+    for (int i = 0; i < kCopies; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(hist + i * kCopyLd)[lane];
+      c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w;
     }
-    __syncthreads();
-    if (wave == 0) {  // lane l: digits 255 - 4l .. 252 - 4l, from the top
-      uint32_t c[4], sum = 0;
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+    uint32_t above = scan_wave(sum) - sum;
+    uint32_t digit = 0, rest = 0, whole = 0, here = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = bins[255 - 4 * lane - i];
-        sum += c[i];
+    for (int i = 0; i < 4; ++i) {
+      if (above < need && above + c[i] >= need) {
+        digit = static_cast<uint32_t>(255 - 4 * lane - i);
+        rest = need - above;
+        whole = c[i];
+        here = 1;
       }
-      uint32_t above = sum;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t x = __shfl_up(above, o, 64);
-        above += lane >= o ? x : 0;
-      }
-      above -= sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t want = static_cast<uint32_t>(need);
-        if (above < want && above + c[i] >= want) {
-          found[0] = static_cast<uint32_t>(255 - 4 * lane - i);
-          found[1] = want - above;
-        }
-        above += c[i];
-      }
+      above += c[i];
     }
-    __syncthreads();
-    prefix |= found[0] << shift;
-    need = static_cast<int>(found[1]);
+    const int at = __builtin_ctzll(__ballot(here != 0));
+    prefix |= static_cast<uint32_t>(__builtin_amdgcn_readlane(digit, at)) << shift;
+    need = static_cast<uint32_t>(__builtin_amdgcn_readlane(rest, at));
     // All slots with this prefix stay: the prefix, as the least key that has
     // it, already separates the rest.
-    if (bins[found[0]] == found[1]) break;  // uniform
+    all_stay = static_cast<uint32_t>(__builtin_amdgcn_readlane(whole, at)) == need;
+    if (all_stay) break;  // uniform
+    if (shift > 0) __syncthreads();  // the next counts are clear
   }
 
-  // Wave w numbers the slots of one contiguous part of the row: ties at the
-  // threshold first (the lowest slots stay), then the freed front slots and the
-  // slots that move.
-  const int part = (n + kSelThreads - 1) / kSelThreads * 64;
-  const int i0 = min(n, wave * part), i1 = min(n, i0 + part);
-  int ties = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 64) ties += __popcll(__ballot(i < i1 && key_of(i) == prefix));
-  int total;
-  const uint64_t below = (uint64_t(1) << lane) - 1;
-  const int tie0 = wave_base(ties, small, total);
-  auto walk = [&](auto&& emit) {
-    int tie = tie0;
-    for (int base = i0; base < i1; base += 64) {
-      const int i = base + lane;
-      const uint32_t k = i < i1 ? key_of(i) : 0u;
-      const bool eq = i < i1 && k == prefix;
-      const uint64_t eqs = __ballot(eq);
-      const bool keep = i < i1 && (k > prefix || (eq && tie + __popcll(eqs & below) < need));
-      tie += __popcll(eqs);
-      emit(i, keep, i < i1 && !keep && i < left, keep && i >= left);
-    }
-  };
-  int frees = 0, moves = 0;
-  walk([&](int, bool, bool free_slot, bool move) {
-    frees += __popcll(__ballot(free_slot));
-    moves += __popcll(__ballot(move));
-  });
-  int free_at = wave_base(frees, small, total);
-  int move_at = wave_base(moves, small, total);
-  int32_t* from = a.from + row * a.move_cap;
-  int32_t* to = a.to + row * a.move_cap;
-  if (tid == 0) a.count[row] = total;
-  {
-    int at = move_at;
-    walk([&](int i, bool, bool, bool move) {
-      const uint64_t ms = __ballot(move);
-      if (move) from[at + __popcll(ms & below)] = i;
-      at += __popcll(ms);
-    });
+  // Ties at the threshold in slot order (the lowest stay), then the freed front
+  // slots and the slots that move, numbered over the row.
+  int tie0 = 0;
+  if (!all_stay) {
+    int ties = 0;
+    each([&](int s, int i, bool in) { ties += __popcll(__ballot(in && key_at(s, i) == prefix)); });
+    if (lane == 0) ties_lds[wave] = ties;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) tie0 += i < wave ? ties_lds[i] : 0;
   }
-  __syncthreads();  // the row's list of moving slots is read below
-  walk([&](int i, bool keep, bool free_slot, bool) {
-    const uint64_t fs = __ballot(free_slot);
-    int src = i;
-    if (free_slot) {
-      const int k = free_at + __popcll(fs & below);
-      src = from[k];
-      to[k] = i;
-    }
+  auto walk = [&](auto&& f) {
+    int tie = tie0;
+    each([&](int s, int i, bool in) {
+      const uint32_t k = in ? key_at(s, i) : 0u;
+      bool keep = in && k >= prefix;
+      if (!all_stay) {
+        const uint64_t eqs = __ballot(in && k == prefix);
+        keep = keep && (k > prefix || tie + lanes_below(eqs) < static_cast<int>(need));
+        tie += __popcll(eqs);
+      }
+      f(s, i, keep, in && !keep && i < left, keep && i >= left);
+    });
+  };
+  int2 counts = make_int2(0, 0);
+  walk([&](int, int, bool, bool free_slot, bool move) {
+    counts.x += __popcll(__ballot(free_slot));
+    counts.y += __popcll(__ballot(move));
+  });
+  if (lane == 0) counts_lds[wave] = counts;
+  __syncthreads();
+  int free_at = 0, move_at = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) {
+    const int2 x = counts_lds[i];
+    free_at += i < wave ? x.x : 0;
+    move_at += i < wave ? x.y : 0;
+    total += x.y;
+  }
+  // The lists of the moves: for the second launch, or in LDS.
+  __shared__ int32_t own_lists[RB > 0 ? 2 * kOwnMoveBytes / (2 * RB) : 1];
+  int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
+  int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
+  if (RB == 0 && tid == 0) a.count[row] = total;
+  walk([&](int s, int i, bool keep, bool free_slot, bool move) {
+    const uint64_t fs = __ballot(free_slot), ms = __ballot(move);
+    if (free_slot) to[free_at + lanes_below(fs)] = i;
+    if (move) from[move_at + lanes_below(ms)] = i;
     free_at += __popcll(fs);
-    if (free_slot || (keep && i < left)) {
-      kept[i] = src;
-      mass_out[i] = mass[src];
-      pos_out[i] = pos[src];
+    move_at += __popcll(ms);
+    if (keep && !move) {
+      kept[i] = i;
+      // Read again where the registers do not hold them along with the keys.
+      mass_out[i] = STEPS > 0 && STEPS <= 8 ? mass_at(s, i) : mass[i];
+      pos_out[i] = STEPS > 0 && STEPS <= 8 ? pos_at(s, i) : pos[i];
     }
   });
+  if constexpr (RB > 0) {
+    __syncthreads();  // the lists
+    move_slots<RB, THREADS>(a, row, from, to, total, 0, 1);
+  }
 }
 
-constexpr int kMoveThreads = 256;
-
-// LANES lanes copy a moved slot: the K row's 16-byte pieces, then the V row's.
 template <int RB>
 __global__ __launch_bounds__(kMoveThreads) void kv_move_kernel(EvictArgs a) {
-  constexpr int HALF = RB / 16, LANES = 2 * HALF;
   const int64_t row = blockIdx.x;
-  const int64_t b = row / a.c.heads;
-  const int h = static_cast<int>(row % a.c.heads);
-  const int count = a.count[row];
-  const int ps = a.c.page_shift, mask = (1 << ps) - 1;
-  const int l = threadIdx.x % LANES;
-  const int32_t* table = a.table + b * a.max_pages;
-  const int step = static_cast<int>(gridDim.y) * (kMoveThreads / LANES);
-  for (int i = blockIdx.y * (kMoveThreads / LANES) + threadIdx.x / LANES; i < count; i += step) {
-    const int src = a.from[row * a.move_cap + i], dst = a.to[row * a.move_cap + i];
-    const int64_t sp = table[src >> ps], dp = table[dst >> ps];
-    if (sp < 0 || sp >= a.c.pages || dp < 0 || dp >= a.c.pages) continue;
-    const int64_t s = ((sp * a.c.heads + h) << ps) + (src & mask), d = ((dp * a.c.heads + h) << ps) + (dst & mask);
-    uint8_t* p = l < HALF ? a.c.k : a.c.v;
-    const int piece = l < HALF ? l : l - HALF;
-    reinterpret_cast<uint4*>(p + d * RB)[piece] = reinterpret_cast<const uint4*>(p + s * RB)[piece];
-    if (a.c.kmeta != nullptr && piece == 0) {
-      uint32_t* meta = l < HALF ? a.c.kmeta : a.c.vmeta;
-      meta[d] = meta[s];
-    }
-  }
+  move_slots<RB, kMoveThreads>(a, row, a.from + row * a.move_cap, a.to + row * a.move_cap, a.count[row], blockIdx.y,
+                               static_cast<int>(gridDim.y));
 }
 
 template <int RB>
-void launch_move(const EvictArgs& a, int64_t rows, hipStream_t st) {
-  const int per = kMoveThreads / (RB / 8);
-  // A workgroup goes over several moves of its row when there are many.
+void launch_evict(const EvictArgs& a, int64_t rows, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(rows));
+  const bool own = static_cast<int64_t>(a.move_cap) * 2 * RB <= kOwnMoveBytes;
+  if (a.max_len <= 2048) {
+    if (own)
+      kv_select_kernel<256, 8, RB><<<grid, 256, 0, st>>>(a);
+    else
+      kv_select_kernel<256, 8, 0><<<grid, 256, 0, st>>>(a);
+  } else if (a.max_len <= 1024 * 8) {
+    if (own)
+      kv_select_kernel<1024, 8, RB><<<grid, 1024, 0, st>>>(a);
+    else
+      kv_select_kernel<1024, 8, 0><<<grid, 1024, 0, st>>>(a);
+  } else if (a.max_len <= 1024 * 20) {
+    kv_select_kernel<1024, 20, 0><<<grid, 1024, 0, st>>>(a);
+  } else {
+    kv_select_kernel<1024, 0, 0><<<grid, 1024, 0, st>>>(a);
+  }
+  if (a.move_cap == 0 || (own && a.max_len <= 1024 * 8)) return;
+  constexpr int per = kMoveThreads / (RB / 8) * kMovesAtOnce;
+  // A workgroup goes over several lots of its row's moves when there are many.
   const int64_t most = (a.move_cap + per - 1) / per;
-  const int64_t want = (4096 + rows - 1) / rows;
-  const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(most < want ? most : want));
-  kv_move_kernel<RB><<<grid, kMoveThreads, 0, st>>>(a);
+  const int64_t want = (16384 + rows - 1) / rows;
+  kv_move_kernel<RB><<<dim3(static_cast<unsigned>(rows), static_cast<unsigned>(most < want ? most : want)), kMoveThreads,
+                       0, st>>>(a);
 }
 
 // At most this many slots of a row move: each fills a slot below the budget
@@ -338,20 +433,13 @@ extern "C" qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const int32_t* 
   a.from = reinterpret_cast<int32_t*>(w + evict_count_bytes(rows));
   a.to = a.from + rows * a.move_cap;
   hipStream_t st = as_stream(stream);
-  if (max_len <= kKeysMax)
-    kv_select_kernel<true><<<dim3(static_cast<unsigned>(rows)), kSelThreads, static_cast<size_t>(max_len) * 4, st>>>(a);
-  else
-    kv_select_kernel<false><<<dim3(static_cast<unsigned>(rows)), kSelThreads, 0, st>>>(a);
-  QLIN_LAUNCH_CHECK("kv_select_kernel");
-  if (a.move_cap > 0) {
-    switch (cache->head_dim * cache->bits / 8) {
-      case 32: launch_move<32>(a, rows, st); break;
-      case 64: launch_move<64>(a, rows, st); break;
-      case 128: launch_move<128>(a, rows, st); break;
-      case 256: launch_move<256>(a, rows, st); break;
-      default: launch_move<512>(a, rows, st); break;
-    }
-    QLIN_LAUNCH_CHECK("kv_move_kernel");
+  switch (cache->head_dim * cache->bits / 8) {
+    case 32: launch_evict<32>(a, rows, st); break;
+    case 64: launch_evict<64>(a, rows, st); break;
+    case 128: launch_evict<128>(a, rows, st); break;
+    case 256: launch_evict<256>(a, rows, st); break;
+    default: launch_evict<512>(a, rows, st); break;
   }
+  QLIN_LAUNCH_CHECK("kv_select_kernel, kv_move_kernel");
   return QLIN_OK;
 }

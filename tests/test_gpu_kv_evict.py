@@ -101,13 +101,14 @@ def test_one_slot_over(q):
         _check(q, rng, c, 1024, 0, kind, in_place=True)
 
 
-@pytest.mark.parametrize("n", [24576, 24577, 60000])
+@pytest.mark.parametrize("n", [2048, 2049, 8192, 8193, 20480, 20481, 24576, 24577, 60000])
 def test_long_rows(q, n):
     log(f"evict long n={n}")
     rng = np.random.default_rng(n)
     c = HostCache(rng, [n, 5], n, 1, 64, 128, 4)
     _check(q, rng, c, 2000, 500, max_len=n)
-    _check(q, rng, c, 20000, 0, "ties", max_len=n, in_place=True)
+    _check(q, rng, c, n // 3, 0, "ties", max_len=n, in_place=True)
+    _check(q, rng, c, n - 3, n // 2, "close", max_len=n, in_place=True)
 
 
 def test_lengths_beyond_the_bounds_are_cut(q):
