@@ -86,8 +86,8 @@ inline bool kv_shape_ok(const qlin_kv_cache* c) {
 
 // ---------------------------------------------------------------- device side
 // Minimum and maximum that pass a NaN on (fminf and fmaxf drop it).
-__device__ __forceinline__ float min_nan(float a, float b) { return (a < b || a != a) ? a : b; }
-__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float v) {
@@ -106,11 +106,40 @@ __device__ __forceinline__ float lane_xor(float v) {
   return dpp_f32<0x128>(v);
 }
 
+// u += s * (u, or v, of the lane that CTRL names) for eight values: s is +-1, so
+// the product is exact and the sum rounded once.  (A DPP operand may be read
+// two wait states after it was written.)
+#define QLIN_FMAC_DPP8(u, s, CTRL)                                                                  \
+  asm("s_nop 1\n\t"                                                                                 \
+      "v_fmac_f32_dpp %0, %0, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %1, %1, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %2, %2, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %3, %3, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %4, %4, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %5, %5, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %6, %6, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                           \
+      "v_fmac_f32_dpp %7, %7, %8 " CTRL " row_mask:0xf bank_mask:0xf"                               \
+      : "+v"(u[0]), "+v"(u[1]), "+v"(u[2]), "+v"(u[3]), "+v"(u[4]), "+v"(u[5]), "+v"(u[6]), "+v"(u[7])\
+      : "v"(s))
+#define QLIN_FMAC_DPP8_OF(u, v, s, CTRL)                                                            \
+  asm("s_nop 1\n\t"                                                                                 \
+      "v_fmac_f32_dpp %0, %8, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
+      "v_fmac_f32_dpp %1, %9, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                          \
+      "v_fmac_f32_dpp %2, %10, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                         \
+      "v_fmac_f32_dpp %3, %11, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                         \
+      "v_fmac_f32_dpp %4, %12, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                         \
+      "v_fmac_f32_dpp %5, %13, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                         \
+      "v_fmac_f32_dpp %6, %14, %16 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                         \
+      "v_fmac_f32_dpp %7, %15, %16 " CTRL " row_mask:0xf bank_mask:0xf"                             \
+      : "+&v"(u[0]), "+&v"(u[1]), "+&v"(u[2]), "+&v"(u[3]), "+&v"(u[4]), "+&v"(u[5]), "+&v"(u[6]),  \
+        "+&v"(u[7])                                                                                 \
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(s))
+
 // t = (x * d) H_128 for 128 values held by 16 neighbouring lanes, 8 each
 // (lane c of the 16 holds 8c .. 8c + 7): a butterfly of spans 1, 2, .., 64 in
-// fp32, every sum and difference rounded once.  Across lanes the lower one
-// keeps u + other and the upper one other - u, both fma(u, +-1, other): the
-// product is exact.
+// fp32, every sum and difference rounded once.  Across lanes the lower one of a
+// pair takes u + other and the upper one u - other, the negative of what is
+// due, which goes on through the later spans and is put right at the end.
 __device__ __forceinline__ void hadamard128(float (&u)[8], int c) {
 #pragma unroll
   for (int h = 1; h < 8; h <<= 1) {
@@ -123,27 +152,30 @@ __device__ __forceinline__ void hadamard128(float (&u)[8], int c) {
       }
     }
   }
-  auto across = [&](auto mask) {
-    constexpr int MASK = decltype(mask)::value;
-    const float sg = (c & MASK) ? -1.0f : 1.0f;
+  const float s1 = (c & 1) ? -1.0f : 1.0f, s2 = (c & 2) ? -1.0f : 1.0f;
+  const float s4 = (c & 4) ? -1.0f : 1.0f, s8 = (c & 8) ? -1.0f : 1.0f;
+  QLIN_FMAC_DPP8(u, s1, "quad_perm:[1,0,3,2]");
+  QLIN_FMAC_DPP8(u, s2, "quad_perm:[2,3,0,1]");
+  float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = __builtin_fmaf(u[e], sg, lane_xor<MASK>(u[e]));
-  };
-  across(std::integral_constant<int, 1>{});
-  across(std::integral_constant<int, 2>{});
-  across(std::integral_constant<int, 4>{});
-  across(std::integral_constant<int, 8>{});
+  for (int e = 0; e < 8; ++e) v[e] = dpp_f32<0x1B>(u[e]);  // each quad reversed, then each eight lanes
+  QLIN_FMAC_DPP8_OF(u, v, s4, "row_half_mirror");
+  QLIN_FMAC_DPP8(u, s8, "row_ror:8");
+  const float sign = (s1 * s2) * (s4 * s8);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = __builtin_fmaf(u[e], sign, 0.0f);
 }
 
-// Eight fp16 values of x with the signs' sign bits flipped in, as fp32.
+// Eight fp16 values times the signs (a negative entry: -1), as fp32: the sign
+// bits (bit 7 of each byte) are moved to the fp16 pairs and flipped in.
 __device__ __forceinline__ void signed8(const v4i raw, const int8_t* signs, float (&f)[8]) {
   const uint2 s = *reinterpret_cast<const uint2*>(signs);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t word = static_cast<uint32_t>(raw[i >> 1]);
-    const uint16_t h = static_cast<uint16_t>((i & 1) ? word >> 16 : word);
-    const uint32_t sw = (i < 4) ? s.x : s.y;
-    f[i] = h2f(static_cast<uint16_t>(h ^ (((sw >> (8 * (i & 3) + 7)) & 1u) << 15)));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mask = __builtin_amdgcn_perm(0u, i < 2 ? s.x : s.y, (i & 1) ? 0x030c020cu : 0x010c000cu) & 0x80008000u;
+    const uint32_t w = static_cast<uint32_t>(raw[i]) ^ mask;
+    f[2 * i] = h2f(static_cast<uint16_t>(w));
+    f[2 * i + 1] = h2f(static_cast<uint16_t>(w >> 16));
   }
 }
 

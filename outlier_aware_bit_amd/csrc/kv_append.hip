@@ -24,6 +24,15 @@ struct AppendArgs {
 
 constexpr int kAppendThreads = 256;
 
+// 1 / s of a positive fp16 value, correctly rounded: one Newton step on the
+// approximate reciprocal gives the quotient for each of them (all 31743 were
+// compared).  An infinite s gives a NaN where 1 / s is 0: codes of such a row
+// stand for nothing.
+__device__ __forceinline__ float inverse(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+}
+
 // One row as stored: fp16 as it is; else, in fp32 with one rounding per
 // operation, lo = fp16(min t), step = fp16((max t - lo) * (1 / qmax)),
 // code = clamp(rint((t - lo) * (1 / step)), 0, qmax).  LANES neighbouring lanes
@@ -68,64 +77,68 @@ __device__ __forceinline__ void store_row(const v4i raw, int c, uint8_t* dst, ui
     const float lo = h2f(lo16);
     const uint16_t step16 = f2h_mul(sub_rn(mx, lo), 1.0f / qmax);
     const float step = h2f(step16);
-    const float inv = (step == 0.0f) ? 0.0f : div_rn(1.0f, step);
-    uint32_t code[8];
+    const float inv = (step == 0.0f) ? 0.0f : inverse(step);
+    uint32_t w[2] = {0, 0};  // a code per byte
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      code[i] = static_cast<uint32_t>(fminf(fmaxf(rint_f(mul_rn(sub_rn(t[i], lo), inv)), 0.0f), qmax));
+    for (int i = 0; i < 8; ++i) {
+      const float code = __builtin_amdgcn_fmed3f(rint_f(mul_rn(sub_rn(t[i], lo), inv)), 0.0f, qmax);
+      w[i >> 2] = __builtin_amdgcn_cvt_pk_u8_f32(code, i & 3, w[i >> 2]);
+    }
     if constexpr (BITS == 8) {
-      uint2 w = make_uint2(0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w.x |= code[i] << (8 * i);
-        w.y |= code[4 + i] << (8 * i);
-      }
-      reinterpret_cast<uint2*>(dst)[c] = w;
+      reinterpret_cast<uint2*>(dst)[c] = make_uint2(w[0], w[1]);
     } else {
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code[i] << (4 * i);
-      reinterpret_cast<uint32_t*>(dst)[c] = w;
+      // Bytes 0 and 2 of w | w >> 4 hold two codes each.
+      w[0] |= w[0] >> 4;
+      w[1] |= w[1] >> 4;
+      reinterpret_cast<uint32_t*>(dst)[c] = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u);
     }
     if (c == 0) *meta = static_cast<uint32_t>(step16) | static_cast<uint32_t>(lo16) << 16;
   }
 }
 
 // A workgroup takes 2048 / D consecutive tokens of one kv head, D / 8 lanes per
-// row, and stores each token's K and V row: the rows, their (step, lo) pairs
-// and the mass / pos entries of neighbouring tokens of a prompt lie side by
-// side in a page, so a workgroup's stores fill whole lines.
+// row, and stores each token's K and V row: the rows, their (step, lo)
+// pairs and the mass / pos entries of neighbouring tokens of a prompt lie side
+// by side in a page, so a workgroup's stores fill whole lines.
 template <int BITS, int D, bool ROT>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int LANES = D / 8;
   constexpr int RB = D * BITS / 8;  // bytes of a stored row
   const int c = threadIdx.x % LANES;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / LANES) + threadIdx.x / LANES;
-  const int h = blockIdx.y;
-  const int64_t tt = t < a.T ? t : a.T - 1;  // every lane takes part in the exchanges
-  const int64_t b = a.row != nullptr ? a.row[tt] : tt;
-  const int32_t slot = a.slot[tt];
-  const v4i kr = *reinterpret_cast<const v4i*>(a.k + tt * a.ld_k + h * D + 8 * c);
-  const v4i vr = *reinterpret_cast<const v4i*>(a.v + tt * a.ld_v + h * D + 8 * c);
+  constexpr int TOKENS = kAppendThreads / LANES;
+  const uint32_t h = blockIdx.x, heads = a.c.heads;
   const int ps = a.c.page_shift;
-  bool ok = t < a.T && b >= 0 && b < a.B && slot >= 0 && (slot >> ps) < a.max_pages;
-  const int32_t id = ok ? a.table[b * a.max_pages + (slot >> ps)] : 0;
-  ok = ok && id >= 0 && id < a.c.pages;
-  if (!ok) return;  // uniform over a row's lanes
-  const int64_t at = ((static_cast<int64_t>(id) * a.c.heads + h) << ps) + (slot & ((1 << ps) - 1));
-  store_row<BITS, LANES, ROT>(kr, c, a.c.k + at * RB, a.c.kmeta + at, a.c.signs);
-  store_row<BITS, LANES, false>(vr, c, a.c.v + at * RB, a.c.vmeta + at, nullptr);
-  if (a.mass != nullptr && c == 0 && slot < a.ld) {
-    const int64_t i = (b * a.c.heads + h) * a.ld + slot;
-    a.mass[i] = 0.0f;
-    a.pos[i] = a.position[tt];
+  const int64_t step = static_cast<int64_t>(gridDim.y) * TOKENS;
+  int64_t t = static_cast<int64_t>(blockIdx.y) * TOKENS + threadIdx.x / LANES;
+  for (int64_t lot = static_cast<int64_t>(blockIdx.y) * TOKENS; lot < a.T; lot += step, t += step) {  // uniform
+    const int64_t tt = t < a.T ? t : a.T - 1;  // every lane takes part in the exchanges
+    const v4i k = *reinterpret_cast<const v4i*>(a.k + tt * a.ld_k + h * D + 8 * c);
+    const v4i v = *reinterpret_cast<const v4i*>(a.v + tt * a.ld_v + h * D + 8 * c);
+    const int32_t slot = a.slot[tt];
+    const int64_t b = a.row != nullptr ? a.row[tt] : tt;
+    bool ok = t < a.T && b >= 0 && b < a.B && slot >= 0 && (slot >> ps) < a.max_pages;
+    const uint32_t entry = ok ? slot >> ps : 0;
+    const uint32_t id = a.table[static_cast<uint64_t>(static_cast<uint32_t>(ok ? b : 0)) *
+                                static_cast<uint32_t>(a.max_pages) + entry];
+    ok = ok && id < static_cast<uint32_t>(a.c.pages);
+    if (!ok) continue;  // uniform over a row's lanes
+    const uint64_t at = ((static_cast<uint64_t>(id) * heads + h) << ps) + (slot & ((1 << ps) - 1));
+    store_row<BITS, LANES, ROT>(k, c, a.c.k + at * RB, a.c.kmeta + at, a.c.signs);
+    store_row<BITS, LANES, false>(v, c, a.c.v + at * RB, a.c.vmeta + at, nullptr);
+    if (a.mass != nullptr && c == 0 && slot < a.ld) {
+      const uint64_t i = static_cast<uint64_t>(static_cast<uint32_t>(b) * heads + h) * static_cast<uint32_t>(a.ld) + slot;
+      a.mass[i] = 0.0f;
+      a.pos[i] = a.position[tt];
+    }
   }
 }
 
 template <int BITS, int D, bool ROT>
 void launch(const AppendArgs& a, hipStream_t st) {
   constexpr int tokens = kAppendThreads / (D / 8);
-  const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens), static_cast<unsigned>(a.c.heads));
+  const int64_t lots = (a.T + tokens - 1) / tokens;
+  // Neighbouring workgroups take the heads of the same tokens, which lie side by side.
+  const dim3 grid(static_cast<unsigned>(a.c.heads), static_cast<unsigned>(lots < 65535 ? lots : 65535));
   kv_append_kernel<BITS, D, ROT><<<grid, kAppendThreads, 0, st>>>(a);
 }
 
@@ -167,7 +180,10 @@ extern "C" qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t
   const bool track = mass != nullptr;
   QLIN_REQUIRE((pos != nullptr) == track && (position != nullptr) == track, QLIN_ERR_INVALID_ARG,
                "mass, pos and position come together or not at all");
-  if (track) QLIN_KV_TRACK(cache, B, ld);
+  if (track) {
+    QLIN_KV_TRACK(cache, B, ld);
+    QLIN_REQUIRE(B < kMaxDim / cache->kv_heads, QLIN_ERR_SHAPE, "B * kv_heads: fewer than 2^31");
+  }
   if (T == 0 || B == 0) return QLIN_OK;
   QLIN_PTR(k);
   QLIN_PTR(v);

@@ -513,43 +513,64 @@ class KVCache:
         return cls(k, v, head_dim, bits, *meta, signs)
 
 
+# The calls below are made once a layer and token, so their checks are kept
+# short: one expression per tensor, and the full check, which names what is
+# wrong, where it does not hold.
+def _is(t, name, dtype, shape):
+    if not (t is not None and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _req(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape):
+    return None if t is None else _is(t, name, dtype, shape)
+
+
+def _raw_stream(cache):
+    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+
+
 def _rows3(t, name, heads, head_dim):
     """fp16 [n, heads, head_dim] whose tokens lie any multiple of 8 elements
     apart (a slice of a fused projection's output): (n, elements apart)."""
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name}: expected shape (n, {heads}, {head_dim}), got {tuple(t.shape)}")
-    n = t.shape[0]
-    st = t.stride()
-    if n and (st[2] != 1 or (heads > 1 and st[1] != head_dim)):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError(f"{name}: expected shape (n, {heads}, {head_dim}), got {tuple(shape)}")
+    n = shape[0]
+    if n == 0:
+        return 0, heads * head_dim
+    ld, head, one = t.stride()
+    if one != 1 or (head != head_dim and heads > 1):
         raise ValueError(f"{name}: heads and channels must be contiguous")
-    if n <= 1:
-        return n, heads * head_dim
-    return n, st[0]
+    return n, ld if n > 1 else heads * head_dim
 
 
 def _table(table):
-    _req(table, "table", torch.int32)
+    if not (table is not None and table.dtype is torch.int32 and table.is_cuda and table.is_contiguous()):
+        _req(table, "table", torch.int32)
     if table.dim() != 2:
         raise ValueError(f"table: expected [B, max_pages], got {tuple(table.shape)}")
     return table.shape
 
 
 def _tracked(t, name, dtype, B, heads):
-    _req(t, name, dtype)
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != heads:
-        raise ValueError(f"{name}: expected shape ({B}, {heads}, ld), got {tuple(t.shape)}")
-    return t.shape[2]
+    if not (t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _req(t, name, dtype)
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != heads:
+        raise ValueError(f"{name}: expected shape ({B}, {heads}, ld), got {tuple(shape)}")
+    return shape[2]
 
 
 def _work(work, need, like):
     if not need:
         return None
     if work is None:
-        return _empty((need,), torch.uint8, like)
+        return torch.empty((need,), dtype=torch.uint8, device=like.device)
     _req(work, "work", torch.uint8)
     if work.numel() < need:
         raise ValueError(f"work: {work.numel()} bytes, needs {need}")
@@ -568,18 +589,22 @@ def qlin_kv_append(cache, k, v, table, slot, row=None, position=None, mass=None,
     Tv, ld_v = _rows3(v, "v", cache.kv_heads, cache.head_dim)
     if Tv != T:
         raise ValueError(f"k holds {T} tokens, v {Tv}")
-    _req(slot, "slot", torch.int32, (T,))
-    _opt(row, "row", torch.int32, (T,))
+    tokens = (T,)
+    slot_p = _is(slot, "slot", torch.int32, tokens)
+    row_p = _maybe(row, "row", torch.int32, tokens)
     ld = 0
+    mass_p = pos_p = position_p = None
     if mass is not None or pos is not None or position is not None:
         ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads)
-        _req(pos, "pos", torch.int32, mass.shape)
-        _req(position, "position", torch.int32, (T,))
+        mass_p = mass.data_ptr()
+        pos_p = _is(pos, "pos", torch.int32, mass.shape)
+        position_p = _is(position, "position", torch.int32, tokens)
     if T == 0:
         return
-    _lib.check("qlin_kv_append", lib.qlin_kv_append(
-        cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, _ptr(row), slot.data_ptr(), table.data_ptr(), B,
-        max_pages, _ptr(position), _ptr(mass), _ptr(pos), ld, _stream()))
+    st = lib.qlin_kv_append(cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, row_p, slot_p, table.data_ptr(), B,
+                            max_pages, position_p, mass_p, pos_p, ld, _raw_stream(cache))
+    if st:
+        _lib.check("qlin_kv_append", st)
 
 
 def qlin_attn_decode_work_bytes(cache, heads, B, max_len, window=0, mass=False) -> int:
@@ -598,18 +623,24 @@ def qlin_attn_decode(cache, q, table, lens, max_len, scale=None, window=0, mass=
     not None) bytes, or None to allocate one.  Returns (out, mass_out)."""
     lib = _lib.load()
     B, max_pages = _table(table)
-    if q.dim() != 3:
-        raise ValueError(f"q: expected [B, heads, {cache.head_dim}], got {tuple(q.shape)}")
-    heads = q.shape[1]
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q: expected [B, heads, {cache.head_dim}], got {tuple(shape)}")
+    heads = shape[1]
     Bq, ld_q = _rows3(q, "q", heads, cache.head_dim)
     if Bq != B:
         raise ValueError(f"q holds {Bq} sequences, table {B}")
-    _req(lens, "lens", torch.int32, (B,))
-    out = _req(out, "out", torch.float16, q.shape) if out is not None else _empty(q.shape, torch.float16, q)
+    lens_p = _is(lens, "lens", torch.int32, (B,))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    else:
+        _is(out, "out", torch.float16, shape)
     ld = 0
+    mass_p = mass_out_p = None
     if mass_out is not None:
         ld = _tracked(mass_out, "mass_out", torch.float32, B, cache.kv_heads)
-        _opt(mass, "mass", torch.float32, mass_out.shape)
+        mass_out_p = mass_out.data_ptr()
+        mass_p = _maybe(mass, "mass", torch.float32, mass_out.shape)
     elif mass is not None:
         raise ValueError("mass needs mass_out")
     if B == 0:
@@ -618,9 +649,10 @@ def qlin_attn_decode(cache, q, table, lens, max_len, scale=None, window=0, mass=
         scale = cache.head_dim ** -0.5
     need = lib.qlin_attn_decode_work_bytes(cache._ref, heads, B, max_len, window, mass_out is not None)
     work = _work(work, need, q)
-    _lib.check("qlin_attn_decode", lib.qlin_attn_decode(
-        cache._ref, q.data_ptr(), ld_q, heads, table.data_ptr(), lens.data_ptr(), B, max_pages, max_len, float(scale),
-        window, out.data_ptr(), _ptr(mass), _ptr(mass_out), ld, _ptr(work), _stream()))
+    st = lib.qlin_attn_decode(cache._ref, q.data_ptr(), ld_q, heads, table.data_ptr(), lens_p, B, max_pages, max_len,
+                              scale, window, out.data_ptr(), mass_p, mass_out_p, ld, _ptr(work), _raw_stream(cache))
+    if st:
+        _lib.check("qlin_attn_decode", st)
     return out, mass_out
 
 
@@ -639,21 +671,28 @@ def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_o
     pos_out); kept holds the old slot of each new one, -1 past lens_out."""
     lib = _lib.load()
     B, max_pages = _table(table)
-    _req(lens, "lens", torch.int32, (B,))
-    ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads)
-    _req(pos, "pos", torch.int32, mass.shape)
-    mass_out = mass if mass_out is None else _req(mass_out, "mass_out", torch.float32, mass.shape)
-    pos_out = pos if pos_out is None else _req(pos_out, "pos_out", torch.int32, mass.shape)
-    lens_out = _req(lens_out, "lens_out", torch.int32, (B,)) if lens_out is not None else torch.empty_like(lens)
-    if B and lens_out.data_ptr() == lens.data_ptr():
-        raise ValueError("lens_out must not be lens")
-    shape = (B, cache.kv_heads, budget)
-    kept = _req(kept, "kept", torch.int32, shape) if kept is not None else _empty(shape, torch.int32, lens)
+    heads = cache.kv_heads
+    lens_p = _is(lens, "lens", torch.int32, (B,))
+    ld = _tracked(mass, "mass", torch.float32, B, heads)
+    shape = mass.shape
+    mass_p, pos_p = mass.data_ptr(), _is(pos, "pos", torch.int32, shape)
+    if mass_out is None:
+        mass_out = mass
+    if pos_out is None:
+        pos_out = pos
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if kept is None:
+        kept = torch.empty((B, heads, budget), dtype=torch.int32, device=cache.device)
+    mass_out_p, pos_out_p = _is(mass_out, "mass_out", torch.float32, shape), _is(pos_out, "pos_out", torch.int32, shape)
+    lens_out_p, kept_p = _is(lens_out, "lens_out", torch.int32, (B,)), _is(kept, "kept", torch.int32, (B, heads, budget))
     if B == 0:
         return lens_out, kept, mass_out, pos_out
+    if lens_out_p == lens_p:
+        raise ValueError("lens_out must not be lens")
     work = _work(work, lib.qlin_kv_evict_work_bytes(cache._ref, B, max_len, budget), lens)
-    _lib.check("qlin_kv_evict", lib.qlin_kv_evict(
-        cache._ref, table.data_ptr(), lens.data_ptr(), B, max_pages, max_len, budget, recent, mass.data_ptr(),
-        pos.data_ptr(), ld, mass_out.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), kept.data_ptr(), _ptr(work),
-        _stream()))
+    st = lib.qlin_kv_evict(cache._ref, table.data_ptr(), lens_p, B, max_pages, max_len, budget, recent, mass_p, pos_p, ld,
+                           mass_out_p, pos_out_p, lens_out_p, kept_p, _ptr(work), _raw_stream(cache))
+    if st:
+        _lib.check("qlin_kv_evict", st)
     return lens_out, kept, mass_out, pos_out
