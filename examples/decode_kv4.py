@@ -1,0 +1,160 @@
+"""One attention layer in W4A4KV4, decoding: the projections as Hadamard + int4
+products, and between them the paged int4 key/value cache.
+
+Per token: x -> qkv projection -> qlin_kv_append -> qlin_attn_decode (which also
+accumulates every slot's attention weight) -> output projection -> the next x.
+When a sequence has used up its pages, qlin_kv_evict keeps the newest slots and
+those with the largest weight, and decoding goes on in the same memory.
+
+    python examples/decode_kv4.py [--bits 4] [--batch 8] [--steps 512] ...
+
+Weights and hidden states are random; one line per eviction and a summary are
+printed.  Needs the GPU and a built library.
+"""
+import argparse
+import os
+import sys
+import time
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from outlier_aware_bit_amd import qlin  # noqa: E402
+
+HEAD_DIM = 128
+
+
+def random_signs(n, generator):
+    s = torch.randint(0, 2, (n,), generator=generator, dtype=torch.int8) * 2 - 1
+    s[::128] = 1  # a block's first row stays all ones
+    return s.cuda()
+
+
+class Linear4:
+    """y = x W with x and W [K, N] as asymmetric int4 of their block Hadamard transforms."""
+
+    def __init__(self, w, signs):
+        self.N, self.signs = w.shape[1], signs
+        codes, self.sw, self.zw, self.colsum = qlin.qlin_quant_weight_offq(w, signs)
+        self.w4 = qlin.qlin_pack_weight(qlin.QLIN_LAYOUT_W4U, codes)
+
+    def __call__(self, x):
+        q4, sa, za, rowsum, _ = qlin.qlin_hadamard_offset(x, self.signs)
+        return qlin.qlin_gemm_w4a4(q4, sa, za, rowsum, self.w4, self.sw, self.zw, self.colsum, self.N)[0]
+
+
+class Attention4:
+    """Projections, cache and eviction state of one layer for a fixed batch.
+
+    Every sequence has pages for `capacity` slots.  lens on the GPU counts a
+    sequence's slots, position its tokens; their upper bound on the host is all
+    that the host decides by, so a step waits for nothing."""
+
+    def __init__(self, hidden, heads, kv_heads, batch, capacity, budget, recent, bits=4, page=64, seed=0):
+        g = torch.Generator().manual_seed(seed)
+
+        def weight(k, n):
+            return (torch.randn(k, n, generator=g) * k ** -0.5).half().cuda()
+
+        self.heads, self.kv_heads, self.budget, self.recent = heads, kv_heads, budget, recent
+        self.qkv = Linear4(weight(hidden, (heads + 2 * kv_heads) * HEAD_DIM), random_signs(hidden, g))
+        self.out = Linear4(weight(heads * HEAD_DIM, hidden), random_signs(heads * HEAD_DIM, g))
+        per_row = -(-capacity // page)
+        self.capacity = per_row * page
+        if not 0 < budget < self.capacity:
+            raise ValueError(f"budget={budget}: a sequence has {self.capacity} slots")
+        turn = random_signs(HEAD_DIM, g)  # K's rows meet the cache's few bits after a Hadamard turn
+        self.cache = qlin.KVCache.empty(batch * per_row, kv_heads, HEAD_DIM, page, bits,
+                                        signs=turn if bits < 16 else None)
+        pages = torch.randperm(batch * per_row, generator=g, dtype=torch.int32)
+        self.table = pages.reshape(batch, per_row).cuda()
+        self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.position = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.mass = torch.zeros(batch, kv_heads, self.capacity, device="cuda")
+        self.pos = torch.zeros(batch, kv_heads, self.capacity, dtype=torch.int32, device="cuda")
+        self.longest = 0  # of lens, on the host
+        self.work = torch.empty(qlin.qlin_attn_decode_work_bytes(self.cache, heads, batch, self.capacity, mass=True),
+                                dtype=torch.uint8, device="cuda")
+        self.evictions = 0
+
+    def _rows(self, x):
+        y = self.qkv(x).view(x.shape[0], self.heads + 2 * self.kv_heads, HEAD_DIM)
+        return y.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
+
+    def prefill(self, x, lens):
+        """Stores the prompts' keys and values: x [sum(lens), hidden], one prompt after another."""
+        if max(lens) > self.capacity:
+            raise ValueError(f"a prompt of {max(lens)} tokens: the sequence has {self.capacity} slots")
+        _, k, v = self._rows(x)
+        row = torch.cat([torch.full((n,), b, dtype=torch.int32) for b, n in enumerate(lens)]).cuda()
+        slot = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]).cuda()
+        qlin.qlin_kv_append(self.cache, k, v, self.table, slot, row, slot, self.mass, self.pos)
+        self.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        self.position.copy_(self.lens)
+        self.longest = max(lens)
+
+    def step(self, x):
+        """One token per sequence: x [batch, hidden] -> [batch, hidden]."""
+        if self.longest == self.capacity:
+            self.evict()
+        q, k, v = self._rows(x)
+        qlin.qlin_kv_append(self.cache, k, v, self.table, self.lens, None, self.position, self.mass, self.pos)
+        self.lens += 1
+        self.position += 1
+        self.longest += 1
+        o, _ = qlin.qlin_attn_decode(self.cache, q, self.table, self.lens, self.capacity, mass=self.mass,
+                                     mass_out=self.mass, work=self.work)
+        return self.out(o.view(x.shape[0], -1))
+
+    def evict(self):
+        self.lens = qlin.qlin_kv_evict(self.cache, self.table, self.lens, self.capacity, self.budget, self.recent,
+                                       self.mass, self.pos)[0]
+        self.longest = self.budget
+        self.evictions += 1
+
+
+def decode(layer, lens, steps, hidden, seed=1):
+    """Prompts of lens tokens, then steps tokens each; the last hidden states."""
+    g = torch.Generator().manual_seed(seed)
+    layer.prefill(torch.randn(sum(lens), hidden, generator=g).half().cuda(), lens)
+    x = torch.randn(len(lens), hidden, generator=g).half().cuda()
+    for _ in range(steps):
+        y = layer.step(x)
+        x = y * torch.rsqrt(y.float().pow(2).mean(-1, keepdim=True) + 1e-6).half()
+    return x
+
+
+def main(argv=None):
+    p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    p.add_argument("--hidden", type=int, default=4096)
+    p.add_argument("--heads", type=int, default=32)
+    p.add_argument("--kv-heads", type=int, default=8)
+    p.add_argument("--batch", type=int, default=8)
+    p.add_argument("--prompt", type=int, default=900, help="tokens of the longest prompt")
+    p.add_argument("--steps", type=int, default=512)
+    p.add_argument("--capacity", type=int, default=1024, help="slots that a sequence has pages for")
+    p.add_argument("--budget", type=int, default=512, help="slots that an eviction keeps")
+    p.add_argument("--recent", type=int, default=128, help="newest tokens among them")
+    p.add_argument("--bits", type=int, default=4, choices=(4, 8, 16))
+    a = p.parse_args(argv)
+    lens = [max(1, a.prompt - 37 * b) for b in range(a.batch)]
+    layer = Attention4(a.hidden, a.heads, a.kv_heads, a.batch, a.capacity, a.budget, a.recent, a.bits)
+    decode(layer, lens, 2, a.hidden)  # first launches
+    layer = Attention4(a.hidden, a.heads, a.kv_heads, a.batch, a.capacity, a.budget, a.recent, a.bits)
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    x = decode(layer, lens, a.steps, a.hidden)
+    torch.cuda.synchronize()
+    t = time.perf_counter() - t
+    pool = sum(m.numel() * m.element_size() for m in (layer.cache.k, layer.cache.v, layer.cache.kmeta,
+                                                      layer.cache.vmeta) if m is not None)
+    print(f"{a.batch} sequences, int{a.bits} cache of {pool / 2**20:.1f} MiB" if a.bits < 16 else
+          f"{a.batch} sequences, fp16 cache of {pool / 2**20:.1f} MiB")
+    print(f"{a.steps} steps, {layer.evictions} evictions, {t / a.steps * 1e6:.0f} us a step, "
+          f"{a.batch * a.steps / t:.0f} tokens/s through one layer")
+    print(f"lens {layer.lens.tolist()}, last states finite: {bool(torch.isfinite(x).all())}")
+    return layer, x
+
+
+if __name__ == "__main__":
+    main()
