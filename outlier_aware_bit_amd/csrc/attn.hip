@@ -162,6 +162,11 @@ struct Codes {
   static constexpr float v_unit = (BITS == 4) ? 2097152.0f : 16777216.0f;  // 2^21
 };
 
+// What a workgroup does once per row (q, the join of the waves, the output)
+// takes about as long as reading this many bytes, and counts as so many tiles
+// before the row's own when the work is divided.
+constexpr int kRowBytes = 65536;
+
 template <int BITS, int D>
 struct Attn {
   static constexpr int RB = D * BITS / 8;                  // bytes of a stored row
@@ -173,6 +178,7 @@ struct Attn {
   static constexpr int VC = VW > 4 ? 2 : 1;                // 16-byte pieces of them, D / VC channels apart
   static constexpr int DPC = DPL / VC;
   static constexpr bool QUANT = BITS < 16;
+  static constexpr int PAD = kRowBytes / (kTile * (2 * RB + (QUANT ? 8 : 0)));  // tiles
 
   // K: the bytes of lane group g in a row are 16-byte pieces j at 64 j + 16 g
   // (8 bytes at 8 g for 32-byte rows).  Channel of element e of piece j:
@@ -286,28 +292,30 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
   const int ps = a.c.page_shift, line_mask = (1 << ps) - 1;
   const int rows_b = a.c.heads * a.parts;  // rows of a sequence
 
-  // The run of this workgroup: rows (b, r) from tile `at` of the flat sequence
-  // of tiles up to `stop`; row_at: where the row begins in it.
+  // The run of this workgroup: rows (b, r) from place `at` of the flat sequence
+  // of places up to `stop`; a row takes PAD places and one for each of its tiles,
+  // from row_at on.  len: the sequence's length.
   int64_t at = 0, stop = 0, row_at = 0, share = 0;
-  int b, r;
+  int b, r, len;
   if (a.groups == 0) {
     b = uniform_i32(static_cast<int>(blockIdx.x) / rows_b);
+    len = scalar_i32(a.lens + b);
     r = static_cast<int>(blockIdx.x) - b * rows_b;
   } else {
     // Every wave for itself: the tiles of all sequences, then the one where the
     // run begins.
-    auto tiles_of = [&](int i) {
-      if (i >= a.B) return 0;
+    auto len_of = [&](int i) { return i < a.B ? a.lens[i] : 0; };
+    auto tiles_of = [&](int len) {
       int low, n, t0, t1;
-      attn_range(a, a.lens[i], low, n);
+      attn_range(a, len, low, n);
       attn_tiles(low, n, t0, t1);
-      return t1 - t0;
+      return t1 == t0 ? 0 : t1 - t0 + A::PAD;
     };
-    const int tiles0 = tiles_of(lane);
+    const int len0 = len_of(lane), tiles0 = tiles_of(len0);
     const uint32_t sum0 = wave_scan(tiles0);  // 64 times 2^25 at most
     int64_t total = static_cast<uint32_t>(__builtin_amdgcn_readlane(sum0, 63));
     for (int b0 = 64; b0 < a.B; b0 += 64)
-      total += static_cast<uint32_t>(__builtin_amdgcn_readlane(wave_scan(tiles_of(b0 + lane)), 63));
+      total += static_cast<uint32_t>(__builtin_amdgcn_readlane(wave_scan(tiles_of(len_of(b0 + lane))), 63));
     total *= rows_b;
     share = attn_share(a, total);
     at = blockIdx.x * share;
@@ -315,13 +323,14 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     if (at >= stop) return;
     int64_t before = 0;  // tiles of the sequences before b0
     for (int b0 = 0;; b0 += 64) {
-      const int tiles = b0 == 0 ? tiles0 : tiles_of(b0 + lane);
+      const int row_len = b0 == 0 ? len0 : len_of(b0 + lane), tiles = b0 == 0 ? tiles0 : tiles_of(row_len);
       const uint32_t sum = b0 == 0 ? sum0 : wave_scan(tiles);
       const uint64_t past = __ballot((before + sum) * rows_b > at);
       if (past != 0) {
         const int i = __builtin_ctzll(past);
         const int own = __builtin_amdgcn_readlane(tiles, i);
         b = b0 + i;
+        len = __builtin_amdgcn_readlane(row_len, i);
         row_at = (before + static_cast<uint32_t>(__builtin_amdgcn_readlane(sum, i)) - own) * rows_b;
         r = static_cast<int>(attn_div(at - row_at, own));
         row_at += static_cast<int64_t>(r) * own;
@@ -341,12 +350,12 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
   };
   auto row_of = [&]() {
     Row w;
-    attn_range(a, scalar_i32(a.lens + b), w.low, w.n);
+    attn_range(a, len, w.low, w.n);
     attn_tiles(w.low, w.n, w.t0, w.t1);
     w.tiles = w.t1 - w.t0;
     if (a.groups != 0) {
-      const int64_t first = at > row_at ? at - row_at : 0;
-      const int64_t last = stop - row_at < w.tiles ? stop - row_at : w.tiles;
+      const int64_t first = at > row_at + A::PAD ? at - row_at - A::PAD : 0;
+      const int64_t last = stop - row_at - A::PAD < w.tiles ? stop - row_at - A::PAD : w.tiles;
       w.t1 = w.t0 + static_cast<int>(last);
       w.t0 += static_cast<int>(first);
     }
@@ -408,6 +417,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
       }
     }
   };
+  if (a.groups != 0 && row_at + A::PAD >= stop) return;  // the run ends before the row's first tile
   while (true) {
     const Row w = row_of();
     const int low = w.low, end = w.end, hrow = w.hrow, hs = w.hs, ht = w.ht, per = w.per;
@@ -423,25 +433,39 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     // without slots.)  The first is on its way while q is prepared, where the
     // registers for both are there.
     constexpr bool EARLY = D <= 128;
+    // q's loads go out before the tile's: loads are waited for in order.
+    constexpr int SPP = A::EPP / 8;  // k steps of a piece
+    const int hcol = col & 7, rem = col >> 3;
+    const bool here = hcol < hs;
+    const int c = tid & 15;  // of a rotated q: 16 lanes a head, heads tid >> 4 and on
+    const uint16_t* q_row0 = a.q + b * a.ld_q + static_cast<int64_t>(w.hq0) * D;
+    v4i qr;
+    uint2 qsigns;
+    v8h qf[KS];
+    if constexpr (ROT) {
+      qr = *reinterpret_cast<const v4i*>(q_row0 + min(tid >> 4, hrow - 1) * D + 8 * c);
+      qsigns = *reinterpret_cast<const uint2*>(a.c.signs + 8 * c);
+    } else {
+      const uint16_t* qp = q_row0 + (here ? ht * kTileHeads + hcol : 0) * D;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        qf[s] = *reinterpret_cast<const v8h*>(qp + A::k_channel(s / SPP, g) + 8 * (s % SPP));
+    }
+    __builtin_amdgcn_sched_barrier(0);
     Tile x, y;
     int tile = w.t0 + (wave & (per - 1));  // uniform per wave
     if constexpr (EARLY) load(x, w, max(min(tile, w.t1 - 1), 0), g, col);
 
     // q in the operand order of the first product, and sum_d q_d for the rows'
     // lo.  Columns 8 .. 15: the same q, or what fp16 leaves of a rotated one.
-    const int hcol = col & 7, rem = col >> 3;
     const float frem = static_cast<float>(rem);
-    v8h qf[KS];
     float qsum = 0.0f;
-    constexpr int SPP = A::EPP / 8;  // k steps of a piece
     if constexpr (ROT) {
       float* q_lds = lds_o;  // [head][kRotLd]
-      const int c = tid & 15;
       for (int hd = tid >> 4; hd < (hrow + kTileHeads - 1) / kTileHeads * kTileHeads; hd += kAttnThreads / 16) {
         float u[8];  // uniform per wave: 16 lanes a head
-        const int hq = hd < hrow ? hd : 0;
-        const v4i raw = *reinterpret_cast<const v4i*>(a.q + b * a.ld_q + (w.hq0 + hq) * D + 8 * c);
-        signed8(raw, a.c.signs + 8 * c, u);
+        if (hd >= kAttnThreads / 16) qr = *reinterpret_cast<const v4i*>(q_row0 + min(hd, hrow - 1) * D + 8 * c);
+        signed8(qr, qsigns, u);
         hadamard128(u, c);
         const float f = hd < hrow ? 0.0078125f : 0.0f;
         float4* dst = reinterpret_cast<float4*>(q_lds + hd * kRotLd + 8 * c);
@@ -466,11 +490,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
       }
       lds_barrier();  // lds_o takes the vectors next
     } else {
-      const bool here = hcol < hs;
-      const uint16_t* qp = a.q + b * a.ld_q + (w.hq0 + (here ? ht * kTileHeads + hcol : 0)) * D;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const v8h raw = *reinterpret_cast<const v8h*>(qp + A::k_channel(s / SPP, g) + 8 * (s % SPP));
+        const v8h raw = qf[s];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const _Float16 v = here ? raw[A::k_order(i)] : static_cast<_Float16>(0.0f);
@@ -631,7 +653,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     }
     const bool whole = w.t1 - w.t0 == w.tiles;
     lds_barrier();
-    const int64_t slot = whole ? 0 : part_slot(blockIdx.x, row_at, share) * a.row_heads;
+    const int64_t slot = whole ? 0 : part_slot(blockIdx.x, row_at + A::PAD, share) * a.row_heads;
     for (int i = tid; i < hrow * (D / 4); i += kAttnThreads) {
       const int hd = i / (D / 4), d = i % (D / 4) * 4, w0 = hd / kTileHeads * per, hl = hd % kTileHeads;
       float mx = kNoRef;
@@ -658,19 +680,21 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     }
     if (a.groups == 0) return;
     // A row that begins here says where its first part is, and its last workgroup.
+    row_at += A::PAD;
     const int last_group = whole ? blockIdx.x : static_cast<int>(attn_div(row_at + w.tiles - 1, share));
     if (tid == 0 && at <= row_at)
       a.runs[static_cast<int64_t>(b) * rows_b + r] =
           make_int2(static_cast<int>(part_slot(blockIdx.x, row_at, share)), last_group);
     row_at = uniform_i64(row_at + w.tiles);
-    if (row_at >= stop) return;
+    if (row_at + A::PAD >= stop) return;
     at = row_at;
     if (++r == rows_b) {
       r = 0;
       int next_low, next_n;
       do {  // the next sequence with a tile; there is one, as row_at < stop
         ++b;
-        attn_range(a, scalar_i32(a.lens + b), next_low, next_n);
+        len = scalar_i32(a.lens + b);
+        attn_range(a, len, next_low, next_n);
       } while (next_n == 0);
     }
     lds_barrier();  // lds_o and lds_ml are read

@@ -168,8 +168,7 @@ __device__ __forceinline__ void hadamard128(float (&u)[8], int c) {
 
 // Eight fp16 values times the signs (a negative entry: -1), as fp32: the sign
 // bits (bit 7 of each byte) are moved to the fp16 pairs and flipped in.
-__device__ __forceinline__ void signed8(const v4i raw, const int8_t* signs, float (&f)[8]) {
-  const uint2 s = *reinterpret_cast<const uint2*>(signs);
+__device__ __forceinline__ void signed8(const v4i raw, const uint2 s, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t mask = __builtin_amdgcn_perm(0u, i < 2 ? s.x : s.y, (i & 1) ? 0x030c020cu : 0x010c000cu) & 0x80008000u;

@@ -45,7 +45,7 @@ __device__ __forceinline__ void store_row(const v4i raw, int c, uint8_t* dst, ui
   } else {
     float t[8];
     if constexpr (ROT) {
-      signed8(raw, signs + 8 * c, t);
+      signed8(raw, *reinterpret_cast<const uint2*>(signs + 8 * c), t);
       hadamard128(t, c);
     } else {
 #pragma unroll
