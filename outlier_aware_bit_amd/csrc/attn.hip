@@ -713,9 +713,12 @@ struct Parts {
   int count, step;
   __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? first : rest + static_cast<int64_t>(i) * step; }
 };
-__device__ __forceinline__ Parts attn_parts(const AttnArgs& a, int64_t row, int hd) {
+__device__ __forceinline__ int2 attn_run(const AttnArgs& a, int64_t row) {
+  const int32_t* p = reinterpret_cast<const int32_t*>(a.runs + row);
+  return a.groups == 0 ? make_int2(0, 0) : make_int2(scalar_i32(p), scalar_i32(p + 1));
+}
+__device__ __forceinline__ Parts attn_parts(const AttnArgs& a, const int2 run, int hd) {
   if (a.groups == 0) return Parts{0, 0, 1, 0};
-  const int2 run = a.runs[row];
   const int w0 = run.x >> 1;
   return Parts{static_cast<int64_t>(run.x) * a.row_heads + hd, static_cast<int64_t>(2 * w0) * a.row_heads + hd,
                run.y - w0 + 1, 2 * a.row_heads};
@@ -725,55 +728,59 @@ template <int D>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int join_blocks) {
   constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
   __shared__ float4 acc_lds[kJoinThreads];
-  __shared__ float red[kJoinThreads / 64];
-  __shared__ float sums[ROWS];
+  __shared__ float2 row_ml[ROWS];
   __shared__ float2 head_ml[kRowHeads];
   const int tid = threadIdx.x;
   const int h = blockIdx.y;
   const int64_t b = blockIdx.z;
+  const int len = scalar_i32(a.lens + b);
   int low, n;
-  attn_range(a, scalar_i32(a.lens + b), low, n);
   if (static_cast<int>(blockIdx.x) < join_blocks) {
     const int hd = blockIdx.x;
+    // (Of a row without slots, which left no run, nothing is done with it.)
+    const Parts p = attn_parts(a, attn_run(a, (b * a.c.heads + h) * a.parts + hd / kRowHeads), hd % kRowHeads);
+    attn_range(a, len, low, n);
     uint2* out = reinterpret_cast<uint2*>(a.out + (b * a.heads + h * a.group + hd) * D);
     if (n == 0) {
       if (tid < LANES) out[tid] = make_uint2(0, 0);
       return;
     }
-    const Parts p = attn_parts(a, (b * a.c.heads + h) * a.parts + hd / kRowHeads, hd % kRowHeads);
     if (p.count == 1) return;
-    float mx = kNoRef;
-    for (int i = tid; i < p.count; i += kJoinThreads) mx = fmaxf(mx, a.part_ml[p.at(i)].x);
-    mx = wave_max(mx);
-    if ((tid & 63) == 0) red[tid >> 6] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    // Thread r0 * LANES + d4 takes parts r0, r0 + ROWS, .. with a reference of
+    // its own, so no pass over the maxima comes first.
     const int d4 = tid % LANES, r0 = tid / LANES;
-    float sum = 0.0f;
+    float mx = kNoRef, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int i = r0; i < p.count; i += ROWS) {
       const int64_t at = p.at(i);
       const float2 x = a.part_ml[at];
       const float4 v = reinterpret_cast<const float4*>(a.part_o + at * D)[d4];
-      const float f = __builtin_amdgcn_exp2f(x.x - mx);
-      sum = __builtin_fmaf(x.y, f, sum);
-      acc.x = __builtin_fmaf(v.x, f, acc.x);
-      acc.y = __builtin_fmaf(v.y, f, acc.y);
-      acc.z = __builtin_fmaf(v.z, f, acc.z);
-      acc.w = __builtin_fmaf(v.w, f, acc.w);
+      const float to = fmaxf(mx, x.x), f0 = __builtin_amdgcn_exp2f(mx - to), f = __builtin_amdgcn_exp2f(x.x - to);
+      mx = to;
+      sum = __builtin_fmaf(x.y, f, sum * f0);
+      acc.x = __builtin_fmaf(v.x, f, acc.x * f0);
+      acc.y = __builtin_fmaf(v.y, f, acc.y * f0);
+      acc.z = __builtin_fmaf(v.z, f, acc.z * f0);
+      acc.w = __builtin_fmaf(v.w, f, acc.w * f0);
     }
     acc_lds[tid] = acc;
-    if (d4 == 0) sums[r0] = sum;
+    if (d4 == 0) row_ml[r0] = make_float2(mx, sum);
     __syncthreads();
     if (tid < LANES) {
-      float total = 0.0f;
+      float top = kNoRef, total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) top = fmaxf(top, row_ml[i].x);
       float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         const float4 v = acc_lds[i * LANES + tid];
-        total += sums[i];
-        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+        const float f = __builtin_amdgcn_exp2f(row_ml[i].x - top);
+        total = __builtin_fmaf(row_ml[i].y, f, total);
+        t.x = __builtin_fmaf(v.x, f, t.x);
+        t.y = __builtin_fmaf(v.y, f, t.y);
+        t.z = __builtin_fmaf(v.z, f, t.z);
+        t.w = __builtin_fmaf(v.w, f, t.w);
       }
       out[tid] = out4(t, total);
     }
@@ -781,45 +788,70 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   }
   // mass of slots [s0, s0 + kMassSlots) of one (row, kv head)
   const int64_t bh = b * a.c.heads + h;
+  int2 run = attn_run(a, bh * a.parts);
+  attn_range(a, len, low, n);
   const int s0 = (static_cast<int>(blockIdx.x) - join_blocks) * kMassSlots;
   if (s0 >= n) return;  // uniform
   const int64_t head0 = b * a.heads + h * a.group;
   const int slot0 = s0 + 4 * tid;  // four slots of each thread
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // What needs no statistics is loaded before they are known: mass, and the
+  // first four heads' logits (four at a time; a group's last ones again past
+  // its end).
+  const int64_t mass_at = bh * a.ld_mass + slot0;
+  const bool wide = ((a.ld_mass & 3) | ((reinterpret_cast<uintptr_t>(a.mass_out) | reinterpret_cast<uintptr_t>(a.mass_in)) & 15)) == 0;
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f}, base[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float4 s[4];
+  auto load = [&](int h0, int hd, int hs) {
+    const float* lp = a.logits + (head0 + h0) * a.ld_logits + slot0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[i] = slot0 < a.ld_logits ? *reinterpret_cast<const float4*>(lp + min(hd + i, hs - 1) * a.ld_logits)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  load(0, 0, min(kRowHeads, a.group));
+  if (a.mass_in != nullptr) {
+    if (wide) {
+      if (slot0 < a.ld_mass) {
+        const float4 v = *reinterpret_cast<const float4*>(a.mass_in + mass_at);
+        base[0] = v.x, base[1] = v.y, base[2] = v.z, base[3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (slot0 + i < n) base[i] = a.mass_in[mass_at + i];
+    }
+  }
   for (int h0 = 0; h0 < a.group; h0 += kRowHeads) {
     const int hs = min(kRowHeads, a.group - h0);
+    if (h0 > 0) run = attn_run(a, bh * a.parts + h0 / kRowHeads);
     __syncthreads();
     // Each wave takes heads in turn: maximum, then sum, over the parts.
     for (int hd = tid >> 6; hd < hs; hd += kJoinThreads / 64) {
-      const Parts p = attn_parts(a, bh * a.parts + h0 / kRowHeads, hd);
+      const Parts p = attn_parts(a, run, hd);
       float mx, sum;
       if (p.count == 1) {
         const float2 ml = a.head_ml[head0 + h0 + hd];
         mx = ml.x;
         sum = ml.y;
       } else {
-        mx = kNoRef;
-        for (int i = tid & 63; i < p.count; i += 64) mx = fmaxf(mx, a.part_ml[p.at(i)].x);
-        mx = wave_max(mx);
+        float own = kNoRef;
         sum = 0.0f;
         for (int i = tid & 63; i < p.count; i += 64) {
           const float2 ml = a.part_ml[p.at(i)];
-          sum = __builtin_fmaf(ml.y, __builtin_amdgcn_exp2f(ml.x - mx), sum);
+          const float to = fmaxf(own, ml.x);
+          sum = __builtin_fmaf(ml.y, __builtin_amdgcn_exp2f(ml.x - to), sum * __builtin_amdgcn_exp2f(own - to));
+          own = to;
         }
+        mx = wave_max(own);
+        sum *= __builtin_amdgcn_exp2f(own - mx);
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
       }
       if ((tid & 63) == 0) head_ml[hd] = make_float2(mx, sum == 0.0f ? 0.0f : div_rn(1.0f, sum));
     }
-    // Four heads' logits at a time; a group's last ones again past its end.
-    const float* lp = a.logits + (head0 + h0) * a.ld_logits + slot0;
+    __syncthreads();
     for (int hd = 0; hd < hs; hd += 4) {
-      float4 s[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s[i] = slot0 < a.ld_logits ? *reinterpret_cast<const float4*>(lp + min(hd + i, hs - 1) * a.ld_logits)
-                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (hd == 0) __syncthreads();  // head_ml
+      if (h0 + hd > 0) load(h0, hd, hs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (hd + i < hs) {
@@ -833,13 +865,13 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int slot = slot0 + i;
-    if (slot < n && slot < a.ld_mass) {
-      const int64_t at = bh * a.ld_mass + slot;
-      // Logits outside the range were never written.
-      a.mass_out[at] = (a.mass_in != nullptr ? a.mass_in[at] : 0.0f) + (slot >= low ? w[i] : 0.0f);
-    }
+  for (int i = 0; i < 4; ++i) base[i] += slot0 + i >= low ? w[i] : 0.0f;  // logits outside the range were never written
+  if (wide && slot0 + 3 < n) {
+    *reinterpret_cast<float4*>(a.mass_out + mass_at) = make_float4(base[0], base[1], base[2], base[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (slot0 + i < n) a.mass_out[mass_at + i] = base[i];
   }
 }
 
