@@ -150,11 +150,12 @@ template <int THREADS, int STEPS, int RB>
 __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   constexpr int WAVES = THREADS / 64;
   __shared__ uint4 hist4[2][kCopyLd * kCopies / 4];
+  __shared__ uint4 digits4[64];
   __shared__ int newest_lds[WAVES], ties_lds[WAVES];
   __shared__ int2 counts_lds[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
-  const int64_t b = row / a.c.heads;
+  const int64_t b = blockIdx.x / static_cast<uint32_t>(a.c.heads);
   const int n = evict_len(a, b);
   const int left = min(n, a.budget);
   const float* mass = a.mass + row * a.ld;
@@ -188,13 +189,16 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   }
   auto mass_at = [&](int s, int i) { return STEPS > 0 ? mv[s] : mass[i]; };
   auto pos_at = [&](int s, int i) { return STEPS > 0 ? pv[s] : pos[i]; };
+  // Slots below `left` as if all of them stayed; the moves overwrite those that
+  // do not (and read only slots from `left` on).
+  const bool copy_mass = mass_out != mass, copy_pos = pos_out != pos;
+  each([&](int s, int i, bool) {
+    if (i >= left) return;
+    kept[i] = i;
+    if (copy_mass) mass_out[i] = mass_at(s, i);
+    if (copy_pos) pos_out[i] = pos_at(s, i);
+  });
   if (n <= left) {  // uniform: nothing goes
-    each([&](int s, int i, bool in) {
-      if (!in) return;
-      kept[i] = i;
-      mass_out[i] = mass_at(s, i);
-      pos_out[i] = pos_at(s, i);
-    });
     if (RB == 0 && tid == 0) a.count[row] = 0;
     return;
   }
@@ -212,9 +216,14 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
 #pragma unroll
   for (int i = 0; i < WAVES; ++i) newest = max(newest, newest_lds[i]);
   const int64_t gone = static_cast<int64_t>(newest) - a.recent;  // positions up to here are not protected
+  // Past the row keys are 0: below it, or behind its zeros (a NaN's) in slot
+  // order, and fewer than n stay, so none of them does.
   uint32_t kv[STEPS > 0 ? STEPS : 1];
-  if constexpr (STEPS > 0) each([&](int s, int, bool) { kv[s] = evict_key(mv[s], pv[s], gone); });
-  auto key_at = [&](int s, int i) { return STEPS > 0 ? kv[s] : evict_key(mass[i], pos[i], gone); };
+  if constexpr (STEPS > 0) each([&](int s, int, bool in) { kv[s] = in ? evict_key(mv[s], pv[s], gone) : 0u; });
+  auto key_at = [&](int s, int i, bool in) {
+    if constexpr (STEPS > 0) return kv[s];
+    return in ? evict_key(mass[i], pos[i], gone) : 0u;
+  };
 
   // The left-th largest key, digit by digit: `prefix` holds the digits found,
   // `need` how many slots with that prefix stay.  Every wave sums the copies
@@ -226,22 +235,26 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   for (int shift = 24; shift >= 0; shift -= 8) {
     uint32_t* hist = (shift & 8) ? hist0 : hist1;
     uint32_t* next = (shift & 8) ? hist1 : hist0;
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+    // With the prefix (zero below it) taken off, what is left is below 2^(shift + 8).
+    const uint32_t bound = shift == 24 ? 0xffffffffu : (256u << shift) - 1u;
+    uint32_t* copy = hist + (lane & (kCopies - 1)) * kCopyLd + 255;
     each([&](int s, int i, bool in) {
-      if (!in) return;
-      const uint32_t k = key_at(s, i);
-      if ((k & mask) == prefix)
-        atomicAdd(&hist[(lane & (kCopies - 1)) * kCopyLd + (~(k >> shift) & 255u)], 1u);
+      const uint32_t k = key_at(s, i, in) ^ prefix;
+      if (k <= bound) atomicAdd(copy - (k >> shift), 1u);
     });
     __syncthreads();
     for (int i = tid; i < kCopyLd * kCopies / 4; i += THREADS) reinterpret_cast<uint4*>(next)[i] = make_uint4(0, 0, 0, 0);
-    // Lane l: digits 255 - 4l .. 252 - 4l, from the top.
-    uint32_t c[4] = {0, 0, 0, 0};
+    // A thread per digit sums the copies, then lane l of every wave takes digits
+    // 255 - 4l .. 252 - 4l, from the top.
+    if (tid < 256) {
+      uint32_t of_digit = 0;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(hist + i * kCopyLd)[lane];
-      c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w;
+      for (int i = 0; i < kCopies; ++i) of_digit += hist[i * kCopyLd + tid];
+      reinterpret_cast<uint32_t*>(digits4)[tid] = of_digit;
     }
+    __syncthreads();
+    const uint4 digits = digits4[lane];
+    const uint32_t c[4] = {digits.x, digits.y, digits.z, digits.w};
     const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t above = scan_wave(sum) - sum;
     uint32_t digit = 0, rest = 0, whole = 0, here = 0;
@@ -262,7 +275,6 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
     // it, already separates the rest.
     all_stay = static_cast<uint32_t>(__builtin_amdgcn_readlane(whole, at)) == need;
     if (all_stay) break;  // uniform
-    if (shift > 0) __syncthreads();  // the next counts are clear
   }
 
   // Ties at the threshold in slot order (the lowest stay), then the freed front
@@ -270,7 +282,7 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   int tie0 = 0;
   if (!all_stay) {
     int ties = 0;
-    each([&](int s, int i, bool in) { ties += __popcll(__ballot(in && key_at(s, i) == prefix)); });
+    each([&](int s, int i, bool in) { ties += __popcll(__ballot(key_at(s, i, in) == prefix)); });
     if (lane == 0) ties_lds[wave] = ties;
     __syncthreads();
 #pragma unroll
@@ -279,18 +291,18 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   auto walk = [&](auto&& f) {
     int tie = tie0;
     each([&](int s, int i, bool in) {
-      const uint32_t k = in ? key_at(s, i) : 0u;
-      bool keep = in && k >= prefix;
+      const uint32_t k = key_at(s, i, in);
+      bool keep = k >= prefix;
       if (!all_stay) {
-        const uint64_t eqs = __ballot(in && k == prefix);
+        const uint64_t eqs = __ballot(k == prefix);
         keep = keep && (k > prefix || tie + lanes_below(eqs) < static_cast<int>(need));
         tie += __popcll(eqs);
       }
-      f(s, i, keep, in && !keep && i < left, keep && i >= left);
+      f(!keep && i < left, keep && i >= left, i);
     });
   };
   int2 counts = make_int2(0, 0);
-  walk([&](int, int, bool, bool free_slot, bool move) {
+  walk([&](bool free_slot, bool move, int) {
     counts.x += __popcll(__ballot(free_slot));
     counts.y += __popcll(__ballot(move));
   });
@@ -309,18 +321,12 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
   int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
   if (RB == 0 && tid == 0) a.count[row] = total;
-  walk([&](int s, int i, bool keep, bool free_slot, bool move) {
+  walk([&](bool free_slot, bool move, int i) {
     const uint64_t fs = __ballot(free_slot), ms = __ballot(move);
     if (free_slot) to[free_at + lanes_below(fs)] = i;
     if (move) from[move_at + lanes_below(ms)] = i;
     free_at += __popcll(fs);
     move_at += __popcll(ms);
-    if (keep && !move) {
-      kept[i] = i;
-      // Read again where the registers do not hold them along with the keys.
-      mass_out[i] = STEPS > 0 && STEPS <= 8 ? mass_at(s, i) : mass[i];
-      pos_out[i] = STEPS > 0 && STEPS <= 8 ? pos_at(s, i) : pos[i];
-    }
   });
   if constexpr (RB > 0) {
     __syncthreads();  // the lists
