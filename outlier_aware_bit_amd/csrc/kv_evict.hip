@@ -32,11 +32,12 @@ struct EvictArgs {
   int32_t move_cap;
 };
 
-// Digit counts are kept in copies, one for every eighth lane: the masses of a
+// Digit counts are kept in copies, one for every fourth lane: the masses of a
 // row share their leading digits, and lanes that count into one word wait for
 // each other.  A copy holds the counts from digit 255 down; copies begin eight
-// banks apart.
-constexpr int kCopies = 8, kCopyLd = 264;
+// banks apart.  Selection of 256 rows of 3,000 - 9,000 slots: 21.4 us with one
+// copy, 17.8 with 4 and with 8, 18.0 with 16.
+constexpr int kCopies = 4, kCopyLd = 264;
 
 __device__ __forceinline__ int evict_len(const EvictArgs& a, int64_t b) {
   const int64_t cap = a.max_pages << a.c.page_shift;
@@ -81,7 +82,9 @@ __device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
 }
 
 // Rows of which no more bytes than this can move are moved by the workgroup
-// that selected them.
+// that selected them: 128 rows, 1 and 128 slots of 128 bytes over, 9.9 and 11.0
+// us against 9.2 and 3.8, 9.4 and 4.5 with a second launch; 512 slots over, 16.6
+// against 8.8 and 6.7.
 constexpr int64_t kOwnMoveBytes = 16384;
 constexpr int kMoveThreads = 256;
 constexpr int kMovesAtOnce = 4;
@@ -142,6 +145,12 @@ __device__ __forceinline__ void move_slots(const EvictArgs& a, int64_t row, cons
     }
   }
 }
+
+// Workgroups of 256 threads take rows up to this many times their size, and of
+// 1,024 longer ones: 128 rows of 1,025 slots 10.0 us against 10.5, of 2,000 slots
+// 10.4 against 8.1.  Rows of up to 8 and 20 slots a thread are held in registers
+// (20, with keys, mass and positions, is what 128 registers hold).
+constexpr int kSmallSteps = 6;
 
 // Selects the slots of one row.  Each wave holds a contiguous part of it, up to
 // STEPS times 64 slots in registers (STEPS == 0: any number, read from memory
@@ -345,11 +354,11 @@ template <int RB>
 void launch_evict(const EvictArgs& a, int64_t rows, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(rows));
   const bool own = static_cast<int64_t>(a.move_cap) * 2 * RB <= kOwnMoveBytes;
-  if (a.max_len <= 2048) {
+  if (a.max_len <= 256 * kSmallSteps) {
     if (own)
-      kv_select_kernel<256, 8, RB><<<grid, 256, 0, st>>>(a);
+      kv_select_kernel<256, kSmallSteps, RB><<<grid, 256, 0, st>>>(a);
     else
-      kv_select_kernel<256, 8, 0><<<grid, 256, 0, st>>>(a);
+      kv_select_kernel<256, kSmallSteps, 0><<<grid, 256, 0, st>>>(a);
   } else if (a.max_len <= 1024 * 8) {
     if (own)
       kv_select_kernel<1024, 8, RB><<<grid, 1024, 0, st>>>(a);
