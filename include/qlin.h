@@ -567,8 +567,9 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t* k, int64_
  * over the slots max(0, n - window) <= i < n (window == 0: all):
  *   s_i = scale * q . k_i,  p = softmax(s),  out = fp16(sum_i p_i v_i)
  * An empty range, or one whose logits are all -inf, gives zeros.  Logits,
- * maxima, sums and outputs are held in fp32; p is rounded to fp16 for the
- * product with V.  The same call gives the same bits.
+ * maxima, sums and outputs are held in fp32; p, and a q turned to meet turned
+ * rows, enter the matrix products as two fp16 parts each (2^-21).  The same call
+ * gives the same bits.
  *   q         fp16 [B x heads x head_dim], ld_q elements between sequences (a
  *             multiple of 8); heads a multiple of kv_heads, query head j reads
  *             kv head j / (heads / kv_heads)
@@ -584,7 +585,8 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t* k, int64_
  *   work      device workspace of qlin_attn_decode_work_bytes(..) bytes, 16-byte
  *             aligned (NULL if that is 0); its contents on entry do not matter.
  *             Calls that overlap must not share it.
- * One launch when a sequence is one chunk and mass_out is NULL, else two.
+ * One launch when mass_out is NULL and max_len (or the window) is short, else
+ * two.
  */
 qlin_status qlin_attn_decode(const qlin_kv_cache* cache, const uint16_t* q, int64_t ld_q, int32_t heads,
                              const int32_t* table, const int32_t* lens, int64_t B, int64_t max_pages,

@@ -13,12 +13,27 @@
 // eight slots by D / 16 channels per lane and transposed in registers by byte
 // permutes.  Nothing of K, V, S or P goes through LDS.
 //
+// Rows of codes stand for lo + step * code, and are never expanded to that: with
+// w_i = p_i step_i,  s_i = step_i (q . code_i) + lo_i sum(q)  and
+// o = sum_i w_i code_i + sum_i p_i lo_i,  so the codes enter the products as
+// small integers and each row costs two multiplications more.  K after the
+// Hadamard is met by q after the Hadamard: (k d H)(q d H) = 128 k q.
+//
 // The work is a sequence of tiles of 32 slots, row after row (a row: a sequence,
 // a kv head, and up to 32 of its query heads).  As many workgroups as the GPU
 // holds at a time take equal runs of it, wherever rows begin and end, so ragged
 // batches and single long rows fill it alike; a row that lies in several
 // workgroups leaves a maximum, a sum and a vector in each, which a second launch
 // joins.  Rows that are one short run each need no second launch.
+//
+// Bound by the bytes of K and V, read once: 32 sequences of 500 - 4,000 slots,
+// 32 kv heads of 128 channels, fp16, 1,180 MB, 206 us or 5.7 TB/s (a plain read
+// of that size reaches 6.4); 64 of 1,500 - 12,000, 8 kv heads, int4, 471 MB and
+// 55 MB of logits, 116 us or 4.5 TB/s (a copy reaches 5.2), vector instructions
+// 40 % and matrix instructions 9 % of the time.  Small calls are bound by their
+// chain of waits: launch, lens, page ids, q and the first tile, the join of the
+// waves: 7 us for 100 slots; 65,537 slots of 8 kv heads int4, 71 MB, 21 us and 4
+// for the second launch, of which reading is 10.
 #include <type_traits>
 
 #include "kv.hpp"
@@ -433,11 +448,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     asm volatile("" : "+v"(lane_again));
     const int g = lane_again >> 4, col = lane_again & 15;
 
-    // Two tiles, in turn: one is loaded while the other is computed on.  (A
-    // wave without a tile loads one as well: of the row, or of page 0 for a row
-    // without slots.)  The first is on its way while q is prepared, where the
-    // registers for both are there.
-    constexpr bool EARLY = D <= 128;
+    // Two tiles, in turn: one is loaded while the other is computed on; the
+    // first is on its way while q is prepared.  (A wave without a tile loads one
+    // as well: of the row, or of page 0 for a row without slots.)
     // q's loads go out before the tile's: loads are waited for in order.
     constexpr int SPP = A::EPP / 8;  // k steps of a piece
     const int hcol = col & 7, rem = col >> 3;
@@ -459,7 +472,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     __builtin_amdgcn_sched_barrier(0);
     Tile x, y;
     int tile = w.t0 + (wave & (per - 1));  // uniform per wave
-    if constexpr (EARLY) load(x, w, max(min(tile, w.t1 - 1), 0), g, col);
+    load(x, w, max(min(tile, w.t1 - 1), 0), g, col);
 
     // q in the operand order of the first product, and sum_d q_d for the rows'
     // lo.  Columns 8 .. 15: the same q, or what fp16 leaves of a rotated one.
@@ -606,7 +619,6 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
       }
     };
     if (hs > 0 && tile < w.t1) {
-      if constexpr (!EARLY) load(x, w, tile, g, col);
       // The last load of a row reads its last tile again: without a branch
       // around it, what is in flight is known, and only what is used is waited
       // for.
@@ -706,6 +718,12 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
   }
 }
 
+// The weights of every slot need the sums over all of them, and the logits are
+// 4 bytes per query head where K is D / 2 and more per kv head, so the first
+// kernel leaves its logits in memory and this one takes the exponential again:
+// 55 MB of logits and 28 MB of mass in 25 us (64 sequences as above); 4 us where
+// there is only the join, three dependent reads.
+//
 // Per (row, kv head): the first join_blocks workgroups (one for each query head
 // of the group, or none) join the parts of a row that several workgroups took;
 // each of the others adds the group's weights of kMassSlots slots to mass.

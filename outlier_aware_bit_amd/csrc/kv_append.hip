@@ -1,4 +1,15 @@
 // Appending rows to the paged key/value cache (qlin_kv_append).
+//
+// Per row and kv head: K after the Hadamard (t = (k d) H, a butterfly in
+// registers, 8 values a lane and four exchanges between 16 lanes), then for K
+// and V the row's minimum and maximum, its (step, lo) and codes, all in
+// registers; a row is read once and written once.
+//
+// One token per sequence is a launch: 2.6 us for one, 3.4 for 48 sequences.  For
+// prompts vector instructions are what is short: 18,381 tokens of 8 heads of 128
+// channels, int4 with the Hadamard, 97 MB, 25 us (3.9 TB/s; vector instructions
+// 68 % of the time, 175 of them per eight values); 18,786 of 4 heads of 256
+// channels, int8, 116 MB, 24 us (4.8 TB/s, where a copy reaches 5.2).
 #include <type_traits>
 
 #include "kv.hpp"
@@ -137,7 +148,9 @@ template <int BITS, int D, bool ROT>
 void launch(const AppendArgs& a, hipStream_t st) {
   constexpr int tokens = kAppendThreads / (D / 8);
   const int64_t lots = (a.T + tokens - 1) / tokens;
-  // Neighbouring workgroups take the heads of the same tokens, which lie side by side.
+  // Neighbouring workgroups take the heads of the same tokens, which lie side by
+  // side.  One lot each: 2,048 workgroups that go over the lots, the next one's
+  // rows loaded ahead, took 28 - 30 us where this takes 25.
   const dim3 grid(static_cast<unsigned>(a.c.heads), static_cast<unsigned>(lots < 65535 ? lots : 65535));
   kv_append_kernel<BITS, D, ROT><<<grid, kAppendThreads, 0, st>>>(a);
 }
