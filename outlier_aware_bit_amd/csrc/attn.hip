@@ -721,14 +721,18 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
 // The weights of every slot need the sums over all of them, and the logits are
 // 4 bytes per query head where K is D / 2 and more per kv head, so the first
 // kernel leaves its logits in memory and this one takes the exponential again:
-// 55 MB of logits and 28 MB of mass in 25 us (64 sequences as above); 4 us where
+// 55 MB of logits and 28 MB of mass in 20 us (64 sequences as above); 4 us where
 // there is only the join, three dependent reads.
 //
 // Per (row, kv head): the first join_blocks workgroups (one for each query head
 // of the group, or none) join the parts of a row that several workgroups took;
 // each of the others adds the group's weights of kMassSlots slots to mass.
 constexpr int kJoinThreads = 256;
-constexpr int kMassSlots = 4 * kJoinThreads;
+// Sets of 1,024 slots, and heads whose logits are loaded together: 64 sequences
+// as above, groups of 4 and 8 heads, 19.7 and 31 us; 26 and 29.5 with one set, 22
+// and 36 with four, 24 and 38 with eight heads.
+constexpr int kMassSets = 2, kMassHeads = 4;
+constexpr int kMassSlots = kMassSets * 4 * kJoinThreads;
 
 // The parts of one query head of a row: index of part i in part_ml.
 struct Parts {
@@ -816,35 +820,46 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   const int s0 = (static_cast<int>(blockIdx.x) - join_blocks) * kMassSlots;
   if (s0 >= n) return;  // uniform
   const int64_t head0 = b * a.heads + h * a.group;
-  const int slot0 = s0 + 4 * tid;  // four slots of each thread
   // What needs no statistics is loaded before they are known: mass, and the
-  // first four heads' logits (four at a time; a group's last ones again past
-  // its end).
-  const int64_t mass_at = bh * a.ld_mass + slot0;
+  // logits of the first heads.  Below the window there are none.
+  const bool any = s0 + kMassSlots > low;
   const bool wide = ((a.ld_mass & 3) | ((reinterpret_cast<uintptr_t>(a.mass_out) | reinterpret_cast<uintptr_t>(a.mass_in)) & 15)) == 0;
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f}, base[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float4 s[4];
+  float w[kMassSets][4], base[kMassSets][4];
+  float4 s[kMassSets][kMassHeads];
+  auto first = [&](int j) { return s0 + j * 4 * kJoinThreads + 4 * tid; };  // four slots each
   auto load = [&](int h0, int hd, int hs) {
-    const float* lp = a.logits + (head0 + h0) * a.ld_logits + slot0;
+    const float* lp = a.logits + (head0 + h0 + hd) * a.ld_logits;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s[i] = slot0 < a.ld_logits ? *reinterpret_cast<const float4*>(lp + min(hd + i, hs - 1) * a.ld_logits)
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < kMassSets; ++j) {
+      const bool seen = first(j) + 3 >= low && first(j) < n;
+#pragma unroll
+      for (int i = 0; i < kMassHeads; ++i) {
+        s[j][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (hd + i < hs && seen) s[j][i] = *reinterpret_cast<const float4*>(lp + i * a.ld_logits + first(j));
+      }
+    }
   };
   load(0, 0, min(kRowHeads, a.group));
-  if (a.mass_in != nullptr) {
-    if (wide) {
-      if (slot0 < a.ld_mass) {
-        const float4 v = *reinterpret_cast<const float4*>(a.mass_in + mass_at);
-        base[0] = v.x, base[1] = v.y, base[2] = v.z, base[3] = v.w;
-      }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (slot0 + i < n) base[i] = a.mass_in[mass_at + i];
+  for (int j = 0; j < kMassSets; ++j) {
+    const int slot0 = first(j);
+    const int64_t mass_at = bh * a.ld_mass + slot0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][i] = base[j][i] = 0.0f;
+    if (a.mass_in != nullptr) {
+      if (wide) {
+        if (slot0 < n) {
+          const float4 v = *reinterpret_cast<const float4*>(a.mass_in + mass_at);
+          base[j][0] = v.x, base[j][1] = v.y, base[j][2] = v.z, base[j][3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (slot0 + i < n) base[j][i] = a.mass_in[mass_at + i];
+      }
     }
   }
-  for (int h0 = 0; h0 < a.group; h0 += kRowHeads) {
+  for (int h0 = 0; any && h0 < a.group; h0 += kRowHeads) {  // uniform
     const int hs = min(kRowHeads, a.group - h0);
     if (h0 > 0) run = attn_run(a, bh * a.parts + h0 / kRowHeads);
     __syncthreads();
@@ -873,28 +888,36 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
       if ((tid & 63) == 0) head_ml[hd] = make_float2(mx, sum == 0.0f ? 0.0f : div_rn(1.0f, sum));
     }
     __syncthreads();
-    for (int hd = 0; hd < hs; hd += 4) {
+    for (int hd = 0; hd < hs; hd += kMassHeads) {
       if (h0 + hd > 0) load(h0, hd, hs);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kMassHeads; ++i) {
         if (hd + i < hs) {
           const float2 ml = head_ml[hd + i];
-          w[0] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].x - ml.x), ml.y, w[0]);
-          w[1] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].y - ml.x), ml.y, w[1]);
-          w[2] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].z - ml.x), ml.y, w[2]);
-          w[3] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[i].w - ml.x), ml.y, w[3]);
+#pragma unroll
+          for (int j = 0; j < kMassSets; ++j) {
+            w[j][0] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[j][i].x - ml.x), ml.y, w[j][0]);
+            w[j][1] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[j][i].y - ml.x), ml.y, w[j][1]);
+            w[j][2] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[j][i].z - ml.x), ml.y, w[j][2]);
+            w[j][3] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[j][i].w - ml.x), ml.y, w[j][3]);
+          }
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) base[i] += slot0 + i >= low ? w[i] : 0.0f;  // logits outside the range were never written
-  if (wide && slot0 + 3 < n) {
-    *reinterpret_cast<float4*>(a.mass_out + mass_at) = make_float4(base[0], base[1], base[2], base[3]);
-  } else {
+  for (int j = 0; j < kMassSets; ++j) {
+    const int slot0 = first(j);
+    const int64_t mass_at = bh * a.ld_mass + slot0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (slot0 + i < n) a.mass_out[mass_at + i] = base[i];
+    for (int i = 0; i < 4; ++i) base[j][i] += slot0 + i >= low ? w[j][i] : 0.0f;  // logits outside the range were never written
+    if (wide && slot0 + 3 < n) {
+      *reinterpret_cast<float4*>(a.mass_out + mass_at) = make_float4(base[j][0], base[j][1], base[j][2], base[j][3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (slot0 + i < n) a.mass_out[mass_at + i] = base[j][i];
+    }
   }
 }
 
