@@ -73,8 +73,8 @@ __device__ __forceinline__ void store_row(const v4i raw, int c, uint8_t* dst, ui
     mx = max_nan(mx, lane_xor<1>(mx));
     mn = min_nan(mn, lane_xor<2>(mn));
     mx = max_nan(mx, lane_xor<2>(mx));
-    mn = min_nan(mn, lane_xor<4>(mn));
-    mx = max_nan(mx, lane_xor<4>(mx));
+    mn = min_nan(mn, dpp_f32<0x141>(mn));  // eight lanes reversed: the quads are uniform
+    mx = max_nan(mx, dpp_f32<0x141>(mx));
     if constexpr (LANES >= 16) {
       mn = min_nan(mn, lane_xor<8>(mn));
       mx = max_nan(mx, lane_xor<8>(mx));
@@ -89,10 +89,14 @@ __device__ __forceinline__ void store_row(const v4i raw, int c, uint8_t* dst, ui
     const uint16_t step16 = f2h_mul(sub_rn(mx, lo), 1.0f / qmax);
     const float step = h2f(step16);
     const float inv = (step == 0.0f) ? 0.0f : inverse(step);
-    uint32_t w[2] = {0, 0};  // a code per byte
+    // A code per byte.  The conversion to a byte rounds to the nearest integer,
+    // ties to even, and saturates (all 2^32 arguments were compared with rint
+    // and a clamp to [0, 255]).
+    uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float code = __builtin_amdgcn_fmed3f(rint_f(mul_rn(sub_rn(t[i], lo), inv)), 0.0f, qmax);
+      float code = mul_rn(sub_rn(t[i], lo), inv);
+      if constexpr (BITS == 4) code = __builtin_amdgcn_fmed3f(code, 0.0f, qmax);
       w[i >> 2] = __builtin_amdgcn_cvt_pk_u8_f32(code, i & 3, w[i >> 2]);
     }
     if constexpr (BITS == 8) {
