@@ -7,9 +7,9 @@
 //
 // One token per sequence is a launch: 2.6 us for one, 3.4 for 48 sequences.  For
 // prompts vector instructions are what is short: 18,381 tokens of 8 heads of 128
-// channels, int4 with the Hadamard, 97 MB, 25 us (3.9 TB/s; vector instructions
-// 68 % of the time, 175 of them per eight values); 18,786 of 4 heads of 256
-// channels, int8, 116 MB, 24 us (4.8 TB/s, where a copy reaches 5.2).
+// channels, int4 with the Hadamard, 97 MB, 24.4 us (4.0 TB/s; vector
+// instructions 66 % of the time, 165 of them per eight values); 18,786 of 4 heads
+// of 256 channels, int8, 116 MB, 23.1 us (5.0 TB/s, where a copy reaches 5.2).
 #include <type_traits>
 
 #include "kv.hpp"
