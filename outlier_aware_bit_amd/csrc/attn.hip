@@ -823,7 +823,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   // What needs no statistics is loaded before they are known: mass, and the
   // logits of the first heads.  Below the window there are none.
   const bool any = s0 + kMassSlots > low;
-  const bool wide = ((a.ld_mass & 3) | ((reinterpret_cast<uintptr_t>(a.mass_out) | reinterpret_cast<uintptr_t>(a.mass_in)) & 15)) == 0;
+  const uintptr_t ends = reinterpret_cast<uintptr_t>(a.mass_out) | reinterpret_cast<uintptr_t>(a.mass_in);
+  const bool wide = ((a.ld_mass & 3) | (ends & 15)) == 0;  // four slots at once
   float w[kMassSets][4], base[kMassSets][4];
   float4 s[kMassSets][kMassHeads];
   auto first = [&](int j) { return s0 + j * 4 * kJoinThreads + 4 * tid; };  // four slots each
@@ -909,8 +910,9 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   for (int j = 0; j < kMassSets; ++j) {
     const int slot0 = first(j);
     const int64_t mass_at = bh * a.ld_mass + slot0;
+    // (Logits outside the range were never written.)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) base[j][i] += slot0 + i >= low ? w[j][i] : 0.0f;  // logits outside the range were never written
+    for (int i = 0; i < 4; ++i) base[j][i] += slot0 + i >= low ? w[j][i] : 0.0f;
     if (wide && slot0 + 3 < n) {
       *reinterpret_cast<float4*>(a.mass_out + mass_at) = make_float4(base[j][0], base[j][1], base[j][2], base[j][3]);
     } else {
@@ -986,8 +988,9 @@ using namespace qlin;
 
 extern "C" size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, int64_t B, int64_t max_len,
                                               int32_t window, int32_t mass) {
-  if (!kv_shape_ok(cache) || heads < 1 || heads % cache->kv_heads != 0 || B < 1 || max_len < 0 || max_len > kMaxDim / 2 || window < 0 ||
-      !dims_ok(B, max_len) || !dims_ok(B * heads, max_len + 1) || !dims_ok(B * heads, cache->head_dim))
+  if (!kv_shape_ok(cache) || heads < 1 || heads % cache->kv_heads != 0 || B < 1 || max_len < 0 ||
+      max_len > kMaxDim / 2 || window < 0 || !dims_ok(B, max_len) || !dims_ok(B * heads, max_len + 1) ||
+      !dims_ok(B * heads, cache->head_dim))
     return 0;
   const AttnPlan p = attn_plan(*cache, heads, B, max_len, window, mass != 0);
   return p.total();

@@ -115,8 +115,9 @@ __device__ __forceinline__ void move_slots(const EvictArgs& a, int64_t row, cons
   const int32_t* table = a.table + b * a.max_pages;
   uint8_t* pool = l < HALF ? a.c.k : a.c.v;
   uint32_t* metas = l < HALF ? a.c.kmeta : a.c.vmeta;
-  const uint32_t* tracked = reinterpret_cast<const uint32_t*>(l == 0 ? static_cast<const void*>(a.mass) : a.pos) + row * a.ld;
-  uint32_t* tracked_out = reinterpret_cast<uint32_t*>(l == 0 ? static_cast<void*>(a.mass_out) : a.pos_out) + row * a.ld;
+  const int64_t track = row * a.ld;
+  const uint32_t* tracked = reinterpret_cast<const uint32_t*>(l == 0 ? static_cast<const void*>(a.mass) : a.pos) + track;
+  uint32_t* tracked_out = reinterpret_cast<uint32_t*>(l == 0 ? static_cast<void*>(a.mass_out) : a.pos_out) + track;
   for (int i0 = first; i0 < count; i0 += groups * kMovesAtOnce * step) {
     int src[kMovesAtOnce], dst[kMovesAtOnce];
     int64_t s[kMovesAtOnce], d[kMovesAtOnce];
