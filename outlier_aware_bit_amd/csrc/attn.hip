@@ -76,11 +76,16 @@ constexpr int kTileHeads = 8;   // query heads of a wave
 constexpr int kRowHeads = kTileHeads * kAttnWaves;
 
 // A head's weights are exp2(s - m), for codes times the row's step, with m such
-// that the largest is 2^kTop when m is set; m moves when one would pass 2^kCeil,
-// so fp16 holds them (below 2^16), and slots down to 2^-(24 + kTop) of the
-// largest still count.  The sum's own terms may grow to 2^kSumTop where steps
-// are small (or zero: those weights are all 0).
-constexpr float kTop = 7.0f, kCeil = 0x1p15f, kSumTop = 30.0f, kSumCeil = 0x1p40f;
+// that the largest is 2^kTop when m is set; m moves when one would pass kCeil, so
+// fp16 holds them (below 2^16).  m begins as a guess, for logits near zero and V
+// near one, and is set if a lane's first weights lie below kFloor: the largest
+// is then never smaller, and slots down to 2^-26 of it still count.  (Set by the
+// first tile of every row, without a guess: 65,537 slots 24.2 us against 23.1.)
+// The sum's own terms may grow to 2^kSumTop where steps are small (or zero: those
+// weights are all 0).
+constexpr float kTop = 7.0f, kCeil = 0x1p15f, kFloor = 0x1p2f, kSumTop = 30.0f, kSumCeil = 0x1p40f;
+template <int BITS>
+constexpr float kFirstRef = BITS == 16 ? -8.0f : BITS == 8 ? -13.0f : -9.0f;
 // The reference of nothing: below any finite logit.
 constexpr float kNoRef = -3.0e38f;
 
@@ -525,7 +530,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     v4f o[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = 0.0f, l = 0.0f, olo = 0.0f;  // olo: the weights times the rows' lo
+    float m = kFirstRef<BITS>, l = 0.0f, olo = 0.0f;  // olo: the weights times the rows' lo
 
     auto compute = [&](Tile& x, int tile) {
       const int base = tile * kTile;
@@ -578,8 +583,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
         }
       };
       weights();
-      // Out of range, or nothing yet to be in range of.
-      if (__any(wmax > kCeil || sum > kSumCeil || !(l + sum > 0.0f))) {
+      // Out of range, or the lane's first weights and too small: against an m far
+      // above their logits fp16 keeps little of them, or nothing.
+      if (__any(wmax > kCeil || sum > kSumCeil || !(l > 0.0f || wmax >= kFloor))) {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
