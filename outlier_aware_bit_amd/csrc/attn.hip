@@ -590,8 +590,9 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           top = fmaxf(top, s[i] - kSumTop);
+          // A step that is not finite makes its own weight so, whatever m is.
           const float step = QUANT ? lo_half(x.vm[i]) : 1.0f;
-          if (step > 0.0f) top = fmaxf(top, s[i] + __builtin_amdgcn_logf(step) - kTop);
+          if (step > 0.0f && step < INFINITY) top = fmaxf(top, s[i] + __builtin_amdgcn_logf(step) - kTop);
         }
         top = max_groups(top);
         const bool none = sum_groups(l) == 0.0f;

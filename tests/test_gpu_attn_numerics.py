@@ -94,3 +94,18 @@ def test_logits_that_fall_and_rise_along_a_row(q, bits, rotate):
     qh = rng.standard_normal((2, 4, D)).astype(np.float16)
     qh[..., 5] = [1, 10, 100, 1000]
     _check(q, c, qh, D ** -0.5)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("step,lo", [(np.inf, -1.0), (np.inf, -np.inf), (np.nan, np.nan)])
+@pytest.mark.parametrize("n,group", [(20, 2), (33, 2), (600, 2), (600, 20), (900, 40)])
+def test_a_v_row_that_is_not_finite(q, bits, step, lo, n, group):
+    # Rows of an infinity or a NaN have no finite step; their heads' output is
+    # not finite, and the weights, which do not depend on V, are what they are.
+    log(f"attend V row step={step} lo={lo} bits={bits} n={n} group={group}")
+    rng = np.random.default_rng(n + group)
+    c = HostCache(rng, [n, 40], max(n, 40), 2, 128, 16, bits, bits == 4, outliers=False)
+    for slot in (7, n - 1):
+        c.vmeta[c.table[0, slot // 16], 1, slot % 16] = step, lo
+    qh = rng.standard_normal((2, 2 * group, 128)).astype(np.float16)
+    _check(q, c, qh, 128 ** -0.5, skip={(0, 1)})
