@@ -568,8 +568,10 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const uint16_t* k, int64_
  *   s_i = scale * q . k_i,  p = softmax(s),  out = fp16(sum_i p_i v_i)
  * An empty range, or one whose logits are all -inf, gives zeros.  Logits,
  * maxima, sums and outputs are held in fp32; p, and a q turned to meet turned
- * rows, enter the matrix products as two fp16 parts each (2^-21).  The same call
- * gives the same bits.
+ * rows, enter the matrix products as two fp16 parts each: 2^-22 of a value, and
+ * for the smallest 2^-27 of the row's largest p and 2^-35 of the head's largest
+ * |q| (as much, in an int4 cache, for a q that is not turned).  A K or V that is
+ * not finite makes the output so.  The same call gives the same bits.
  *   q         fp16 [B x heads x head_dim], ld_q elements between sequences (a
  *             multiple of 8); heads a multiple of kv_heads, query head j reads
  *             kv head j / (heads / kv_heads)

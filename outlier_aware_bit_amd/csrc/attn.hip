@@ -4,10 +4,11 @@
 //   S = K q^T   (slots x heads),   P = exp2(S - m),   O^T = V^T P^T  (D x heads)
 // on 16x16x32 fp16 matrix instructions, whose 16 columns hold every head twice:
 // columns 8 .. 15 carry what rounding P (and a rotated q) to fp16 left over, so
-// that both products are good to 2^-21 for no further matrix instruction.
-// Both results hold a head in lane & 7, so the softmax state and the rescaling
-// of O never leave the lane, and P comes
-// out of the first product in the registers where the second one takes it: the
+// that a weight or a channel of q is good to 2^-22 of itself, the smallest to
+// 2^-27 of the row's largest weight or 2^-35 of the head's largest channel, for no
+// further matrix instruction.  Both results hold a head in lane & 7, so the
+// softmax state and the rescaling of O never leave the lane, and P comes out of
+// the first product in the registers where the second one takes it: the
 // eight slots 8g .. 8g + 7 of lane group g = lane >> 4 are one k-group of the
 // second product.  K rows are read as its A operand directly; V rows are read
 // eight slots by D / 16 channels per lane and transposed in registers by byte
@@ -127,6 +128,15 @@ __device__ __forceinline__ int64_t uniform_i64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Powers of two (f, 1 / f) that bring a head's largest |q| to 2^14 .. 2^15, so
+// that rounding to fp16 goes by its own size: what the smallest channels lose is
+// 2^-39 of the largest, 2^-35 where int4 divides by 16.  (1, 1) for no size.
+__device__ __forceinline__ float2 q_power(float top) {
+  const uint32_t e = __builtin_bit_cast(uint32_t, top) >> 23;
+  if (top == 0.0f || !(top < INFINITY)) return make_float2(1.0f, 1.0f);
+  return make_float2(__builtin_bit_cast(float, (268u - e) << 23), __builtin_bit_cast(float, (e - 14u) << 23));
 }
 
 // First slot that a sequence of `len` attends to, and one past the last.
@@ -482,7 +492,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
     // q in the operand order of the first product, and sum_d q_d for the rows'
     // lo.  Columns 8 .. 15: the same q, or what fp16 leaves of a rotated one.
     const float frem = static_cast<float>(rem);
-    float qsum = 0.0f;
+    float qsum = 0.0f, unit = 1.0f;  // q is the operand times unit
     if constexpr (ROT) {
       float* q_lds = lds_o;  // [head][kRotLd]
       for (int hd = tid >> 4; hd < (hrow + kTileHeads - 1) / kTileHeads * kTileHeads; hd += kAttnThreads / 16) {
@@ -490,13 +500,23 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
         if (hd >= kAttnThreads / 16) qr = *reinterpret_cast<const v4i*>(q_row0 + min(hd, hrow - 1) * D + 8 * c);
         signed8(qr, qsigns, u);
         hadamard128(u, c);
-        const float f = hd < hrow ? 0.0078125f : 0.0f;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(u[i]));
+        top = fmaxf(top, lane_xor<1>(top));
+        top = fmaxf(top, lane_xor<2>(top));
+        top = fmaxf(top, lane_xor<4>(top));
+        top = fmaxf(top, lane_xor<8>(top));
+        const float2 power = q_power(top);
+        const float f = hd < hrow ? power.x : 0.0f;
+        if (c == 0) q_lds[hd * kRotLd + 128] = power.y * 0.0078125f;
         float4* dst = reinterpret_cast<float4*>(q_lds + hd * kRotLd + 8 * c);
         dst[0] = make_float4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
         dst[1] = make_float4(u[4] * f, u[5] * f, u[6] * f, u[7] * f);
       }
       lds_barrier();
       const float* q_row = q_lds + ((hs > 0 ? ht : 0) * kTileHeads + hcol) * kRotLd;
+      unit = q_row[128];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const float4* src = reinterpret_cast<const float4*>(q_row + A::k_channel(s / SPP, g) + 8 * (s % SPP));
@@ -513,6 +533,18 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
       }
       lds_barrier();  // lds_o takes the vectors next
     } else {
+      float f = 1.0f;
+      if constexpr (BITS == 4) {
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(static_cast<float>(qf[s][i])));
+        }
+        const float2 power = q_power(max_groups(top));
+        f = power.x;
+        unit = power.y;
+      }
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const v8h raw = qf[s];
@@ -520,12 +552,15 @@ __global__ __launch_bounds__(kAttnThreads, attn_resident(D)) void attn_kernel(At
         for (int i = 0; i < 8; ++i) {
           const _Float16 v = here ? raw[A::k_order(i)] : static_cast<_Float16>(0.0f);
           if constexpr (QUANT) qsum += static_cast<float>(v);
-          qf[s][i] = (BITS == 4 && (i & 2)) ? v * static_cast<_Float16>(0.0625f) : v;
+          if constexpr (BITS == 4)
+            qf[s][i] = static_cast<_Float16>(static_cast<float>(v) * ((i & 2) ? f * 0.0625f : f));
+          else
+            qf[s][i] = v;
         }
       }
     }
-    if constexpr (QUANT) qsum = sum_groups(qsum) * a.scale_log2;
-    const float qscale = QUANT ? a.scale_log2 * Codes<BITS>::k_unit : a.scale_log2;
+    if constexpr (QUANT) qsum = sum_groups(qsum) * (ROT ? a.scale_log2 * unit : a.scale_log2);
+    const float qscale = QUANT ? a.scale_log2 * Codes<BITS>::k_unit * unit : a.scale_log2;
 
     v4f o[NT];
 #pragma unroll

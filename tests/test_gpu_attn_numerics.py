@@ -109,3 +109,29 @@ def test_a_v_row_that_is_not_finite(q, bits, step, lo, n, group):
         c.vmeta[c.table[0, slot // 16], 1, slot % 16] = step, lo
     qh = rng.standard_normal((2, 2 * group, 128)).astype(np.float16)
     _check(q, c, qh, 128 ** -0.5, skip={(0, 1)})
+
+
+@pytest.mark.parametrize("bits,D,rotate", FORMS)
+@pytest.mark.parametrize("std", [1e4, 1.0, 1e-1, 1e-2, 1e-3, 1e-4])
+def test_queries_of_any_size(q, bits, D, rotate, std):
+    # Logits of the same size from large and small queries, one head a
+    # thousandth of the others, one all zeros.
+    log(f"attend q of {std} bits={bits} D={D} rotate={rotate}")
+    rng = np.random.default_rng(bits + D)
+    c = HostCache(rng, [100, 530], 530, 2, D, 16, bits, rotate, outliers=False)
+    qh = rng.standard_normal((2, 10, D)) * std
+    qh[:, 1] *= 1e-3
+    qh[:, 2] = 0
+    qh = np.clip(qh, -65504, 65504).astype(np.float16)
+    _check(q, c, qh, D ** -0.5 / std)
+
+
+@pytest.mark.parametrize("bits,D,rotate", [f for f in FORMS if f[0] < 16])
+def test_one_large_channel_of_the_query(q, bits, D, rotate):
+    # What a head's largest channel leaves to the others.
+    log(f"attend one large channel bits={bits} D={D} rotate={rotate}")
+    rng = np.random.default_rng(bits + D)
+    c = HostCache(rng, [100], 100, 1, D, 16, bits, rotate, outliers=False)
+    qh = rng.standard_normal((1, 3, D)).astype(np.float16)
+    qh[:, 0, 6], qh[:, 1, 7], qh[:, 2, D - 1] = 3000, -65504, 60000
+    _check(q, c, qh, D ** -0.5 / 100)
