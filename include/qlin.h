@@ -610,6 +610,9 @@ size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, in
  * the pool, mass and pos to mass_out and pos_out.  Attention is the same for
  * any order of slots.  Pages past ceil(left / page) are free afterwards.
  * A page must belong to one sequence only.
+ * Slots that do not exist (on pages outside the pool) decide nothing and take no
+ * row: one below `left` keeps its place, mass and pos and all, one past it goes,
+ * and as many others stay as there is room for among those below it.
  *   budget    at least 1;  recent in [0, budget]
  *   mass, pos [B x kv_heads x ld], ld >= max_len;  mass_out, pos_out the same
  *             shape, written at slots < left; each may be its input

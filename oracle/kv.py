@@ -73,19 +73,26 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, use: np.nd
     return p[:, use] @ v[use], p
 
 
-def evict(mass: np.ndarray, pos: np.ndarray, budget: int, recent: int):
+def evict(mass: np.ndarray, pos: np.ndarray, budget: int, recent: int, there=None):
     """Which slots of one row stay: (left, src [left]) with src[j] the old slot
     of new slot j.  The ``recent`` newest positions first, then the largest
     mass, ties to the lowest slot, a NaN least; slots that stay past ``left``
-    fill the freed ones before it, both in ascending order."""
+    fill the freed ones before it, both in ascending order.
+    Slots where ``there`` is false do not exist: one before ``left`` keeps its
+    place, one past it goes, and their mass and position decide nothing."""
     n = len(mass)
     left = min(n, budget)
-    newest = max((int(p) for p in pos), default=0)
+    there = [True] * n if there is None else there
+    newest = max((int(p) for p, t in zip(pos, there) if t), default=0)
+
     def rank(i):
+        if not there[i]:
+            return (0 if i < left else 3, False, 0.0, i)
         m = float(mass[i])
         late = int(pos[i]) > newest - recent
-        # NaN sorts below -inf.
-        return (not late, 0.0 if late else (np.inf if np.isnan(m) else -m), (not late) and np.isnan(m), i)
+        if late:
+            return (1, False, 0.0, i)
+        return (2, np.isnan(m), 0.0 if np.isnan(m) else -m, i)
     stay = sorted(sorted(range(n), key=rank)[:left])
     src = list(range(left))
     kept = set(stay)

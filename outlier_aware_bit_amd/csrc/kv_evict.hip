@@ -53,11 +53,13 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int64_t b) {
   return n > cap ? static_cast<int>(cap) : n;
 }
 
-// Larger keys stay: the newest tokens above everything, then by mass as an
-// ordered integer (-0 as +0; a NaN below everything).
+// Larger keys stay: the newest tokens, then by mass as an ordered integer (-0 as
+// +0; a NaN last).  Above and below them all are slots that do not exist: one
+// before `left` keeps its place, one past it goes.
+constexpr uint32_t kKeyHeld = 0xffffffffu, kKeyNewest = 0xfffffffeu, kKeyNan = 1u, kKeyGone = 0u;
 __device__ __forceinline__ uint32_t evict_key(float mass, int32_t pos, int64_t newest_gone) {
-  if (pos > newest_gone) return 0xffffffffu;
-  if (mass != mass) return 0u;
+  if (pos > newest_gone) return kKeyNewest;
+  if (mass != mass) return kKeyNan;
   const uint32_t u = __builtin_bit_cast(uint32_t, add_rn(mass, 0.0f));
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -132,7 +134,7 @@ __device__ __forceinline__ void move_slots(const EvictArgs& a, int64_t row, cons
     }
 #pragma unroll
     for (int u = 0; u < kMovesAtOnce; ++u) {
-      const int64_t sp = table[src[u] >> ps], dp = table[dst[u] >> ps];
+      const int64_t sp = table[src[u] >> ps], dp = table[dst[u] >> ps];  // in the pool, as when selected
       ok[u] = i0 + u * step < count && sp >= 0 && sp < a.c.pages && dp >= 0 && dp < a.c.pages;
       s[u] = (((ok[u] ? sp : 0) * a.c.heads + h) << ps) + (src[u] & mask);
       d[u] = (((ok[u] ? dp : 0) * a.c.heads + h) << ps) + (dst[u] & mask);
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   constexpr int WAVES = THREADS / 64;
   __shared__ uint4 hist4[2][kCopyLd * kCopies / 4];
   __shared__ uint4 digits4[64];
-  __shared__ int newest_lds[WAVES], ties_lds[WAVES];
+  __shared__ int newest_lds[WAVES], holes_lds[WAVES], ties_lds[WAVES];
   __shared__ int2 counts_lds[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
@@ -208,6 +210,14 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
       pv[s] = in ? pos[i] : INT32_MIN;
     });
   }
+  // Slots that do not exist lie on pages outside the pool.  The row's page ids:
+  // two a thread are enough for rows in registers, as pages hold 16 slots or more.
+  const int32_t* table = a.table + b * a.max_pages;
+  const int ps = a.c.page_shift;
+  auto outside = [&](int32_t id) { return static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.c.pages); };
+  auto absent = [&](int i) { return outside(table[i >> ps]); };
+  const int32_t id0 = table[tid << ps < n ? tid : 0];
+  const int32_t id1 = STEPS > 8 ? table[(tid + THREADS) << ps < n ? tid + THREADS : 0] : id0;
   auto mass_at = [&](int s, int i) { return STEPS > 0 ? mv[s] : mass[i]; };
   auto pos_at = [&](int s, int i) { return STEPS > 0 ? pv[s] : pos[i]; };
   // Slots below `left` as if all of them stayed; the moves overwrite those that
@@ -232,126 +242,173 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
     if (in) newest = max(newest, pos_at(s, i));
   });
   newest = max_wave(newest);
-  if (lane == 0) newest_lds[wave] = newest;
+  bool holes = outside(id0) || outside(id1);
+  if constexpr (STEPS == 0) {
+    for (int i = (THREADS + tid) << ps; i < n; i += THREADS << ps) holes = holes || absent(i);
+  }
+  holes = __any(holes);
+  if (lane == 0) {
+    newest_lds[wave] = newest;
+    holes_lds[wave] = holes;
+  }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < WAVES; ++i) newest = max(newest, newest_lds[i]);
+  for (int i = 0; i < WAVES; ++i) {
+    newest = max(newest, newest_lds[i]);
+    holes = holes || holes_lds[i] != 0;
+  }
+  if (holes) {  // uniform, and rare: only then are slots looked up
+    newest = INT32_MIN;
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+      if (slot(s) < n && !absent(slot(s))) newest = max(newest, pos[slot(s)]);
+    }
+    newest = max_wave(newest);
+    __syncthreads();
+    if (lane == 0) newest_lds[wave] = newest;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) newest = max(newest, newest_lds[i]);
+  }
   const int64_t gone = static_cast<int64_t>(newest) - a.recent;  // positions up to here are not protected
-  // Past the row keys are 0: below it, or behind its zeros (a NaN's) in slot
-  // order, and fewer than n stay, so none of them does.
-  uint32_t kv[STEPS > 0 ? STEPS : 1];
-  if constexpr (STEPS > 0) each([&](int s, int, bool in) { kv[s] = in ? evict_key(mv[s], pv[s], gone) : 0u; });
-  auto key_at = [&](int s, int i, bool in) {
-    if constexpr (STEPS > 0) return kv[s];
-    return in ? evict_key(mass[i], pos[i], gone) : 0u;
+  // Past the row keys are those of slots that go: as many slots as stay have
+  // larger ones.
+  auto key_of = [&](int i, bool in, float m, int32_t p, bool look_up) {
+    if (!in) return kKeyGone;
+    if (look_up && absent(i)) return i < left ? kKeyHeld : kKeyGone;
+    return evict_key(m, p, gone);
   };
 
   // The left-th largest key, digit by digit: `prefix` holds the digits found,
   // `need` how many slots with that prefix stay.  Every wave sums the copies
   // and finds the digit for itself; the next digit's counts are cleared
   // meanwhile.
-  uint32_t prefix = 0, need = static_cast<uint32_t>(left);
-  bool all_stay = false;
+  uint32_t prefix, need;
+  bool all_stay;
+  auto find = [&](auto&& key_at) {
+    prefix = 0;
+    need = static_cast<uint32_t>(left);
+    all_stay = false;
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    uint32_t* hist = (shift & 8) ? hist0 : hist1;
-    uint32_t* next = (shift & 8) ? hist1 : hist0;
-    // With the prefix (zero below it) taken off, what is left is below 2^(shift + 8).
-    const uint32_t bound = shift == 24 ? 0xffffffffu : (256u << shift) - 1u;
-    uint32_t* copy = hist + (lane & (kCopies - 1)) * kCopyLd + 255;
-    each([&](int s, int i, bool in) {
-      const uint32_t k = key_at(s, i, in) ^ prefix;
-      if (k <= bound) atomicAdd(copy - (k >> shift), 1u);
-    });
-    __syncthreads();
-    for (int i = tid; i < kCopyLd * kCopies / 4; i += THREADS) reinterpret_cast<uint4*>(next)[i] = make_uint4(0, 0, 0, 0);
-    // A thread per digit sums the copies, then lane l of every wave takes digits
-    // 255 - 4l .. 252 - 4l, from the top.
-    if (tid < 256) {
-      uint32_t of_digit = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      uint32_t* hist = (shift & 8) ? hist0 : hist1;
+      uint32_t* next = (shift & 8) ? hist1 : hist0;
+      // With the prefix (zero below it) taken off, what is left is below 2^(shift + 8).
+      const uint32_t bound = shift == 24 ? 0xffffffffu : (256u << shift) - 1u;
+      uint32_t* copy = hist + (lane & (kCopies - 1)) * kCopyLd + 255;
+      each([&](int s, int i, bool in) {
+        const uint32_t k = key_at(s, i, in) ^ prefix;
+        if (k <= bound) atomicAdd(copy - (k >> shift), 1u);
+      });
+      __syncthreads();
+      for (int i = tid; i < kCopyLd * kCopies / 4; i += THREADS) reinterpret_cast<uint4*>(next)[i] = make_uint4(0, 0, 0, 0);
+      // A thread per digit sums the copies, then lane l of every wave takes digits
+      // 255 - 4l .. 252 - 4l, from the top.
+      if (tid < 256) {
+        uint32_t of_digit = 0;
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) of_digit += hist[i * kCopyLd + tid];
-      reinterpret_cast<uint32_t*>(digits4)[tid] = of_digit;
-    }
-    __syncthreads();
-    const uint4 digits = digits4[lane];
-    const uint32_t c[4] = {digits.x, digits.y, digits.z, digits.w};
-    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
-    uint32_t above = scan_wave(sum) - sum;
-    uint32_t digit = 0, rest = 0, whole = 0, here = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (above < need && above + c[i] >= need) {
-        digit = static_cast<uint32_t>(255 - 4 * lane - i);
-        rest = need - above;
-        whole = c[i];
-        here = 1;
+        for (int i = 0; i < kCopies; ++i) of_digit += hist[i * kCopyLd + tid];
+        reinterpret_cast<uint32_t*>(digits4)[tid] = of_digit;
       }
-      above += c[i];
+      __syncthreads();
+      const uint4 digits = digits4[lane];
+      const uint32_t c[4] = {digits.x, digits.y, digits.z, digits.w};
+      const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+      uint32_t above = scan_wave(sum) - sum;
+      uint32_t digit = 0, rest = 0, whole = 0, here = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (above < need && above + c[i] >= need) {
+          digit = static_cast<uint32_t>(255 - 4 * lane - i);
+          rest = need - above;
+          whole = c[i];
+          here = 1;
+        }
+        above += c[i];
+      }
+      const int at = __builtin_ctzll(__ballot(here != 0));
+      prefix |= static_cast<uint32_t>(__builtin_amdgcn_readlane(digit, at)) << shift;
+      need = static_cast<uint32_t>(__builtin_amdgcn_readlane(rest, at));
+      // All slots with this prefix stay: the prefix, as the least key that has
+      // it, already separates the rest.
+      all_stay = static_cast<uint32_t>(__builtin_amdgcn_readlane(whole, at)) == need;
+      if (all_stay) break;  // uniform
     }
-    const int at = __builtin_ctzll(__ballot(here != 0));
-    prefix |= static_cast<uint32_t>(__builtin_amdgcn_readlane(digit, at)) << shift;
-    need = static_cast<uint32_t>(__builtin_amdgcn_readlane(rest, at));
-    // All slots with this prefix stay: the prefix, as the least key that has
-    // it, already separates the rest.
-    all_stay = static_cast<uint32_t>(__builtin_amdgcn_readlane(whole, at)) == need;
-    if (all_stay) break;  // uniform
-  }
+  };
 
   // Ties at the threshold in slot order (the lowest stay), then the freed front
   // slots and the slots that move, numbered over the row.
-  int tie0 = 0;
-  if (!all_stay) {
-    int ties = 0;
-    each([&](int s, int i, bool in) { ties += __popcll(__ballot(key_at(s, i, in) == prefix)); });
-    if (lane == 0) ties_lds[wave] = ties;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) tie0 += i < wave ? ties_lds[i] : 0;
-  }
-  auto walk = [&](auto&& f) {
-    int tie = tie0;
-    each([&](int s, int i, bool in) {
-      const uint32_t k = key_at(s, i, in);
-      bool keep = k >= prefix;
-      if (!all_stay) {
-        const uint64_t eqs = __ballot(k == prefix);
-        keep = keep && (k > prefix || tie + lanes_below(eqs) < static_cast<int>(need));
-        tie += __popcll(eqs);
-      }
-      f(!keep && i < left, keep && i >= left, i);
-    });
-  };
-  int2 counts = make_int2(0, 0);
-  walk([&](bool free_slot, bool move, int) {
-    counts.x += __popcll(__ballot(free_slot));
-    counts.y += __popcll(__ballot(move));
-  });
-  if (lane == 0) counts_lds[wave] = counts;
-  __syncthreads();
-  int free_at = 0, move_at = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < WAVES; ++i) {
-    const int2 x = counts_lds[i];
-    free_at += i < wave ? x.x : 0;
-    move_at += i < wave ? x.y : 0;
-    total += x.y;
-  }
-  // The lists of the moves: for the second launch, or in LDS.
   __shared__ int32_t own_lists[RB > 0 ? 2 * kOwnMoveBytes / (2 * RB) : 1];
-  int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
-  int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
-  if (RB == 0 && tid == 0) a.count[row] = total;
-  walk([&](bool free_slot, bool move, int i) {
-    const uint64_t fs = __ballot(free_slot), ms = __ballot(move);
-    if (free_slot) to[free_at + lanes_below(fs)] = i;
-    if (move) from[move_at + lanes_below(ms)] = i;
-    free_at += __popcll(fs);
-    move_at += __popcll(ms);
-  });
-  if constexpr (RB > 0) {
-    __syncthreads();  // the lists
-    move_slots<RB, THREADS>(a, row, from, to, total, 0, 1);
+  auto finish = [&](auto&& key_at) {
+    int tie0 = 0;
+    if (!all_stay) {
+      int ties = 0;
+      each([&](int s, int i, bool in) { ties += __popcll(__ballot(key_at(s, i, in) == prefix)); });
+      if (lane == 0) ties_lds[wave] = ties;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) tie0 += i < wave ? ties_lds[i] : 0;
+    }
+    auto walk = [&](auto&& f) {
+      int tie = tie0;
+      each([&](int s, int i, bool in) {
+        const uint32_t k = key_at(s, i, in);
+        bool keep = k >= prefix;
+        if (!all_stay) {
+          const uint64_t eqs = __ballot(k == prefix);
+          keep = keep && (k > prefix || tie + lanes_below(eqs) < static_cast<int>(need));
+          tie += __popcll(eqs);
+        }
+        f(!keep && i < left, keep && i >= left, i);
+      });
+    };
+    int2 counts = make_int2(0, 0);
+    walk([&](bool free_slot, bool move, int) {
+      counts.x += __popcll(__ballot(free_slot));
+      counts.y += __popcll(__ballot(move));
+    });
+    if (lane == 0) counts_lds[wave] = counts;
+    __syncthreads();
+    int free_at = 0, move_at = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      const int2 x = counts_lds[i];
+      free_at += i < wave ? x.x : 0;
+      move_at += i < wave ? x.y : 0;
+      total += x.y;
+    }
+    // The lists of the moves: for the second launch, or in LDS.
+    int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
+    int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
+    if (RB == 0 && tid == 0) a.count[row] = total;
+    walk([&](bool free_slot, bool move, int i) {
+      const uint64_t fs = __ballot(free_slot), ms = __ballot(move);
+      if (free_slot) to[free_at + lanes_below(fs)] = i;
+      if (move) from[move_at + lanes_below(ms)] = i;
+      free_at += __popcll(fs);
+      move_at += __popcll(ms);
+    });
+    if constexpr (RB > 0) {
+      __syncthreads();  // the lists
+      move_slots<RB, THREADS>(a, row, from, to, total, 0, 1);
+    }
+  };
+
+  if constexpr (STEPS > 0) {
+    uint32_t kv[STEPS];
+    each([&](int s, int i, bool in) { kv[s] = key_of(i, in, mv[s], pv[s], false); });
+    if (holes) each([&](int s, int i, bool in) { kv[s] = in ? key_of(i, in, mass[i], pos[i], true) : kKeyGone; });
+    auto key_at = [&](int s, int, bool) { return kv[s]; };
+    find(key_at);
+    finish(key_at);
+  } else if (holes) {
+    auto key_at = [&](int, int i, bool in) { return in ? key_of(i, in, mass[i], pos[i], true) : kKeyGone; };
+    find(key_at);
+    finish(key_at);
+  } else {
+    auto key_at = [&](int, int i, bool in) { return in ? key_of(i, in, mass[i], pos[i], false) : kKeyGone; };
+    find(key_at);
+    finish(key_at);
   }
 }
 
