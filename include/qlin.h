@@ -604,8 +604,8 @@ size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, in
  * qlin_kv_evict -- bring every sequence back to at most `budget` slots per kv
  * head.  Per row b and kv head, n as in qlin_attn_decode, left = min(n, budget):
  * the slots of the `recent` newest positions (pos > max pos - recent) stay
- * first, then those of largest mass, ties to the lowest slot (a NaN mass
- * counts least).  Slots that stay and lie past `left` move, in ascending order,
+ * first, then the others, each by mass, the largest first, ties to the lowest
+ * slot (a NaN mass counts least).  Slots that stay and lie past `left` move, in ascending order,
  * into the freed slots below it, in ascending order: K and V rows in place in
  * the pool, mass and pos to mass_out and pos_out.  Attention is the same for
  * any order of slots.  Pages past ceil(left / page) are free afterwards.

@@ -75,9 +75,9 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, use: np.nd
 
 def evict(mass: np.ndarray, pos: np.ndarray, budget: int, recent: int, there=None):
     """Which slots of one row stay: (left, src [left]) with src[j] the old slot
-    of new slot j.  The ``recent`` newest positions first, then the largest
-    mass, ties to the lowest slot, a NaN least; slots that stay past ``left``
-    fill the freed ones before it, both in ascending order.
+    of new slot j.  The ``recent`` newest positions first, then the others, each
+    by mass, the largest first, a NaN least, ties to the lowest slot; slots that
+    stay past ``left`` fill the freed ones before it, both in ascending order.
     Slots where ``there`` is false do not exist: one before ``left`` keeps its
     place, one past it goes, and their mass and position decide nothing."""
     n = len(mass)
@@ -90,9 +90,7 @@ def evict(mass: np.ndarray, pos: np.ndarray, budget: int, recent: int, there=Non
             return (0 if i < left else 3, False, 0.0, i)
         m = float(mass[i])
         late = int(pos[i]) > newest - recent
-        if late:
-            return (1, False, 0.0, i)
-        return (2, np.isnan(m), 0.0 if np.isnan(m) else -m, i)
+        return (1 if late else 2, np.isnan(m), 0.0 if np.isnan(m) else -m, i)
     stay = sorted(sorted(range(n), key=rank)[:left])
     src = list(range(left))
     kept = set(stay)

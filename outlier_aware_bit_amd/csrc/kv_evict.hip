@@ -57,8 +57,7 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int64_t b) {
 // +0; a NaN last).  Above and below them all are slots that do not exist: one
 // before `left` keeps its place, one past it goes.
 constexpr uint32_t kKeyHeld = 0xffffffffu, kKeyNewest = 0xfffffffeu, kKeyNan = 1u, kKeyGone = 0u;
-__device__ __forceinline__ uint32_t evict_key(float mass, int32_t pos, int64_t newest_gone) {
-  if (pos > newest_gone) return kKeyNewest;
+__device__ __forceinline__ uint32_t mass_key(float mass) {
   if (mass != mass) return kKeyNan;
   const uint32_t u = __builtin_bit_cast(uint32_t, add_rn(mass, 0.0f));
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
@@ -273,10 +272,21 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   const int64_t gone = static_cast<int64_t>(newest) - a.recent;  // positions up to here are not protected
   // Past the row keys are those of slots that go: as many slots as stay have
   // larger ones.
-  auto key_of = [&](int i, bool in, float m, int32_t p, bool look_up) {
+  auto key_of = [&](bool in, float m, int32_t p) {
+    return !in ? kKeyGone : p > gone ? kKeyNewest : mass_key(m);
+  };
+  // The same from memory and slot by slot, for rows with holes, and where there are
+  // more of the newest than can stay (positions that repeat): those by mass, and
+  // no others.
+  bool crowded = false;
+  auto each_slot = [&](auto&& f) {
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) f(s, slot(s), slot(s) < n);
+  };
+  auto careful_key = [&](int, int i, bool in) {
     if (!in) return kKeyGone;
-    if (look_up && absent(i)) return i < left ? kKeyHeld : kKeyGone;
-    return evict_key(m, p, gone);
+    if (holes && absent(i)) return i < left ? kKeyHeld : kKeyGone;
+    return crowded ? (pos[i] > gone ? mass_key(mass[i]) : kKeyGone) : key_of(true, mass[i], pos[i]);
   };
 
   // The left-th largest key, digit by digit: `prefix` holds the digits found,
@@ -285,7 +295,7 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
   // meanwhile.
   uint32_t prefix, need;
   bool all_stay;
-  auto find = [&](auto&& key_at) {
+  auto find = [&](auto&& each, auto&& key_at) {
     prefix = 0;
     need = static_cast<uint32_t>(left);
     all_stay = false;
@@ -338,8 +348,12 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
 
   // Ties at the threshold in slot order (the lowest stay), then the freed front
   // slots and the slots that move, numbered over the row.
+  // The lists of the moves: for the second launch, or in LDS.
   __shared__ int32_t own_lists[RB > 0 ? 2 * kOwnMoveBytes / (2 * RB) : 1];
-  auto finish = [&](auto&& key_at) {
+  int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
+  int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
+  int total = 0;
+  auto list = [&](auto&& each, auto&& key_at) {
     int tie0 = 0;
     if (!all_stay) {
       int ties = 0;
@@ -369,7 +383,7 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
     });
     if (lane == 0) counts_lds[wave] = counts;
     __syncthreads();
-    int free_at = 0, move_at = 0, total = 0;
+    int free_at = 0, move_at = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       const int2 x = counts_lds[i];
@@ -377,10 +391,6 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
       move_at += i < wave ? x.y : 0;
       total += x.y;
     }
-    // The lists of the moves: for the second launch, or in LDS.
-    int32_t* from = RB > 0 ? own_lists : a.from + row * a.move_cap;
-    int32_t* to = RB > 0 ? own_lists + a.move_cap : a.to + row * a.move_cap;
-    if (RB == 0 && tid == 0) a.count[row] = total;
     walk([&](bool free_slot, bool move, int i) {
       const uint64_t fs = __ballot(free_slot), ms = __ballot(move);
       if (free_slot) to[free_at + lanes_below(fs)] = i;
@@ -388,27 +398,32 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
       free_at += __popcll(fs);
       move_at += __popcll(ms);
     });
-    if constexpr (RB > 0) {
-      __syncthreads();  // the lists
-      move_slots<RB, THREADS>(a, row, from, to, total, 0, 1);
-    }
   };
 
-  if constexpr (STEPS > 0) {
-    uint32_t kv[STEPS];
-    each([&](int s, int i, bool in) { kv[s] = key_of(i, in, mv[s], pv[s], false); });
-    if (holes) each([&](int s, int i, bool in) { kv[s] = in ? key_of(i, in, mass[i], pos[i], true) : kKeyGone; });
-    auto key_at = [&](int s, int, bool) { return kv[s]; };
-    find(key_at);
-    finish(key_at);
-  } else if (holes) {
-    auto key_at = [&](int, int i, bool in) { return in ? key_of(i, in, mass[i], pos[i], true) : kKeyGone; };
-    find(key_at);
-    finish(key_at);
+  if (!holes) {
+    uint32_t kv[STEPS > 0 ? STEPS : 1];
+    if constexpr (STEPS > 0) each([&](int s, int, bool in) { kv[s] = key_of(in, mv[s], pv[s]); });
+    auto key_at = [&](int s, int i, bool in) {
+      if constexpr (STEPS > 0) return kv[s];
+      return in ? key_of(true, mass[i], pos[i]) : kKeyGone;
+    };
+    find(each, key_at);
+    crowded = !all_stay && prefix == kKeyNewest;
+    if (!crowded) list(each, key_at);
+  }
+  if (holes || crowded) {
+    find(each_slot, careful_key);
+    if (!crowded && !all_stay && prefix == kKeyNewest) {
+      crowded = true;
+      find(each_slot, careful_key);
+    }
+    list(each_slot, careful_key);
+  }
+  if constexpr (RB > 0) {
+    __syncthreads();  // the lists
+    move_slots<RB, THREADS>(a, row, from, to, total, 0, 1);
   } else {
-    auto key_at = [&](int, int i, bool in) { return in ? key_of(i, in, mass[i], pos[i], false) : kKeyGone; };
-    find(key_at);
-    finish(key_at);
+    if (tid == 0) a.count[row] = total;
   }
 }
 

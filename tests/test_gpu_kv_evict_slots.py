@@ -106,3 +106,23 @@ def test_attention_after_an_eviction_with_unmapped_pages(q):
     k, v = (x[0][src] for x in c.values[0])
     ref, _ = kv.attend(qh[0].astype(np.float64), k, v, 0.125, use)
     assert np.allclose(host(out)[0], ref, rtol=2 ** -9, atol=2e-4)
+
+
+@pytest.mark.parametrize("n", [40, 1500, 3000, 15000, 21000])
+@pytest.mark.parametrize("kind", ["spread", "odd"])
+def test_more_newest_slots_than_fit(q, n, kind):
+    # Positions repeat (the tokens of one image, say): of the newest, those of
+    # largest mass stay.
+    log(f"evict repeated positions n={n} {kind}")
+    rng = np.random.default_rng(n)
+    c = HostCache(rng, [n, n - 1, 7], n, 2, 64, 128, 4)
+    mass, pos = _rows(rng, c, kind)
+    for spread in (1, 3, n // 4 + 1):
+        pos = rng.integers(0, spread, pos.shape).astype(np.int32) + 9
+        for budget, recent in ((1, 1), (n // 3, 1), (n // 2, n // 2), (n - 2, 2)):
+            _check(q, c, mass, pos, budget, min(recent, budget), n, False)
+    # The same where slots that do not exist leave less room.
+    c.table[0, 0] = -1
+    _check(q, c, mass, np.zeros_like(pos), n // 2, 1, n, True)
+    mass, pos = _rows(rng, c, kind)
+    _check(q, c, mass, pos, n // 2, n // 2, n, False)

@@ -1,4 +1,4 @@
-"""The eviction oracle where slots do not exist (CPU)."""
+"""The eviction oracle where slots do not exist or positions repeat (CPU)."""
 import numpy as np
 
 from oracle import kv
@@ -28,3 +28,12 @@ def test_every_existing_slot_that_stays_has_a_place_of_its_own():
         assert left == min(n, budget) and len(set(src.tolist())) == left
         for j, i in enumerate(src):
             assert there[j] == there[i] and (there[j] or i == j)
+
+
+def test_more_newest_slots_than_fit_stay_by_mass():
+    m = np.array([1, 9, 5, 20, np.nan, 9], np.float32)
+    p = np.array([7, 7, 7, 2, 7, 7])
+    assert kv.evict(m, p, 1, 1)[1].tolist() == [1]
+    assert kv.evict(m, p, 2, 2)[1].tolist() == [5, 1]
+    assert kv.evict(m, p, 4, 3)[1].tolist() == [0, 1, 2, 5]
+    assert kv.evict(m, p, 5, 1)[1].tolist() == [0, 1, 2, 5, 4]
