@@ -613,7 +613,8 @@ size_t qlin_attn_decode_work_bytes(const qlin_kv_cache* cache, int32_t heads, in
  * Slots that do not exist (on pages outside the pool) decide nothing and take no
  * row: one below `left` keeps its place, mass and pos and all, one past it goes,
  * and as many others stay as there is room for among those below it.
- *   budget    at least 1;  recent in [0, budget]
+ *   max_len   as in qlin_attn_decode: at most 2^30
+ *   budget    1 .. 2^30;  recent in [0, budget]
  *   mass, pos [B x kv_heads x ld], ld >= max_len;  mass_out, pos_out the same
  *             shape, written at slots < left; each may be its input
  *   lens_out  int32 [B]: left (not the array `lens`)

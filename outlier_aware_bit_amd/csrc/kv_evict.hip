@@ -469,6 +469,10 @@ inline int64_t evict_move_cap(int64_t max_len, int64_t budget) {
   return over < budget ? over : budget;
 }
 
+// Slots and budgets at most: the kernels step past them by up to a workgroup's
+// reach (2^21 slots) in 32 bits.
+constexpr int64_t kMaxSlots = kMaxDim / 2;
+
 inline size_t evict_count_bytes(int64_t rows) { return (static_cast<size_t>(rows) * 4 + 255) / 256 * 256; }
 
 }  // namespace
@@ -477,8 +481,8 @@ inline size_t evict_count_bytes(int64_t rows) { return (static_cast<size_t>(rows
 using namespace qlin;
 
 extern "C" size_t qlin_kv_evict_work_bytes(const qlin_kv_cache* cache, int64_t B, int64_t max_len, int32_t budget) {
-  if (!kv_shape_ok(cache) || B < 1 || B >= kMaxDim / cache->kv_heads || max_len < 0 || max_len >= kMaxDim - 1 ||
-      budget < 0 || !dims_ok(B * cache->kv_heads, max_len + 1))
+  if (!kv_shape_ok(cache) || B < 1 || B >= kMaxDim / cache->kv_heads || max_len < 0 || max_len > kMaxSlots ||
+      budget < 0 || budget > kMaxSlots || !dims_ok(B * cache->kv_heads, max_len + 1))
     return 0;
   const int64_t rows = B * cache->kv_heads;
   return evict_count_bytes(rows) + static_cast<size_t>(rows) * evict_move_cap(max_len, budget) * 8;
@@ -493,6 +497,8 @@ extern "C" qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const int32_t* 
   QLIN_REQUIRE(max_len >= 0, QLIN_ERR_INVALID_ARG, "max_len=%lld is negative", (long long)max_len);
   QLIN_REQUIRE(max_len <= max_pages * cache->page, QLIN_ERR_SHAPE, "max_len=%lld: the table holds %lld slots",
                (long long)max_len, (long long)(max_pages * cache->page));
+  QLIN_REQUIRE(max_len <= kMaxSlots, QLIN_ERR_SHAPE, "max_len=%lld: at most 2^30", (long long)max_len);
+  QLIN_REQUIRE(budget <= kMaxSlots, QLIN_ERR_SHAPE, "budget=%d: at most 2^30", budget);
   QLIN_REQUIRE(budget >= 1, QLIN_ERR_INVALID_ARG, "budget=%d must be at least 1", budget);
   QLIN_REQUIRE(recent >= 0 && recent <= budget, QLIN_ERR_INVALID_ARG, "recent=%d must be in [0, budget]", recent);
   QLIN_KV_TRACK(cache, B, ld);
