@@ -513,6 +513,7 @@ extern "C" qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const int32_t* 
   QLIN_PTR(mass_out);
   QLIN_PTR(pos_out);
   QLIN_PTR(lens_out);
+  QLIN_REQUIRE(lens_out != lens, QLIN_ERR_INVALID_ARG, "lens_out: must not be the array lens");
   QLIN_PTR(kept);
   QLIN_PTR(work);
   const int64_t rows = B * cache->kv_heads;

@@ -5,7 +5,7 @@ import ctypes as C
 import pytest
 
 from outlier_aware_bit_amd import _lib
-from tests.test_kv_abi import S, cache, evict
+from tests.test_kv_abi import A, I, S, cache, evict
 
 M = 1 << 30  # slots and budgets: kernels add up to a workgroup's reach in 32 bits
 
@@ -22,3 +22,9 @@ def test_workspace_sizes_end_there():
     assert lib.qlin_kv_evict_work_bytes(c, 1, M, M) > 0 and lib.qlin_kv_evict_work_bytes(c, 1, M, 16) > 0
     for max_len, budget in ((M + 1, 16), (2 * M - 2, 16), (64, M + 1), (64, 2 * M - 1)):
         assert lib.qlin_kv_evict_work_bytes(c, 1, max_len, budget) == 0
+
+
+def test_lens_out_is_not_lens():
+    # The kv heads of a sequence read lens while another writes lens_out.
+    assert evict(lens=A, lens_out=A) == I, _lib.load().qlin_last_error()
+    assert b"lens_out" in _lib.load().qlin_last_error()
