@@ -468,7 +468,8 @@ class KVCache:
     = even channel) with kmeta, vmeta fp16 [pages, kv_heads, page, 2]: (step,
     lo) of each row, which stands for lo + step * code.  signs: int8 [128] for
     stored K rows (k * signs) H_128 (head_dim 128, bits below 16), or None.
-    The tensors are checked here, once, and kept.
+    The tensors are checked here, once, and kept.  The calls take tensors of the
+    same GPU, and that GPU has to be the current one.
     """
 
     def __init__(self, k, v, head_dim, bits, kmeta=None, vmeta=None, signs=None):
@@ -494,7 +495,7 @@ class KVCache:
                 raise ValueError(f"the cache's tensors are on {k.device} and {t.device}")
         self.k, self.v, self.kmeta, self.vmeta, self.signs = k, v, kmeta, vmeta, signs
         self.pages, self.kv_heads, self.page, self.head_dim, self.bits = pages, kv_heads, page, head_dim, bits
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self._struct = _lib.KVCacheStruct(k.data_ptr(), v.data_ptr(), _ptr(kmeta), _ptr(vmeta), _ptr(signs), pages,
                                           page, kv_heads, head_dim, bits)
         self._ref = ctypes.addressof(self._struct)
@@ -516,27 +517,38 @@ class KVCache:
 # The calls below are made once a layer and token, so their checks are kept
 # short: one expression per tensor, and the full check, which names what is
 # wrong, where it does not hold.
-def _is(t, name, dtype, shape):
-    if not (t is not None and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
-        _req(t, name, dtype, shape)
+_current_device = torch._C._cuda_getDevice
+
+
+def _elsewhere(t, name, index):
+    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+
+
+def _is(t, name, dtype, shape, index):
+    if not (t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        _elsewhere(_req(t, name, dtype, shape), name, index)
     return t.data_ptr()
 
 
-def _maybe(t, name, dtype, shape):
-    return None if t is None else _is(t, name, dtype, shape)
+def _maybe(t, name, dtype, shape, index):
+    return None if t is None else _is(t, name, dtype, shape, index)
 
 
 def _raw_stream(cache):
-    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+    if _current_device() != cache.index:  # where a launch goes
+        raise ValueError(f"the cache is on cuda:{cache.index}, the current device is cuda:{_current_device()}")
+    return torch._C._cuda_getCurrentRawStream(cache.index)
 
 
-def _rows3(t, name, heads, head_dim):
+def _rows3(t, name, heads, head_dim, index):
     """fp16 [n, heads, head_dim] whose tokens lie any multiple of 8 elements
     apart (a slice of a fused projection's output): (n, elements apart)."""
     if t.dtype is not torch.float16:
         raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        _elsewhere(t, name, index)
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError(f"{name}: expected shape (n, {heads}, {head_dim}), got {tuple(shape)}")
@@ -549,29 +561,31 @@ def _rows3(t, name, heads, head_dim):
     return n, ld if n > 1 else heads * head_dim
 
 
-def _table(table):
-    if not (table is not None and table.dtype is torch.int32 and table.is_cuda and table.is_contiguous()):
-        _req(table, "table", torch.int32)
+def _table(table, index):
+    if not (table is not None and table.dtype is torch.int32 and table.get_device() == index and
+            table.is_contiguous()):
+        _elsewhere(_req(table, "table", torch.int32), "table", index)
     if table.dim() != 2:
         raise ValueError(f"table: expected [B, max_pages], got {tuple(table.shape)}")
     return table.shape
 
 
-def _tracked(t, name, dtype, B, heads):
-    if not (t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
-        _req(t, name, dtype)
+def _tracked(t, name, dtype, B, heads, index):
+    if not (t is not None and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _elsewhere(_req(t, name, dtype), name, index)
     shape = t.shape
     if len(shape) != 3 or shape[0] != B or shape[1] != heads:
         raise ValueError(f"{name}: expected shape ({B}, {heads}, ld), got {tuple(shape)}")
     return shape[2]
 
 
-def _work(work, need, like):
+def _work(work, need, cache):
     if not need:
         return None
     if work is None:
-        return torch.empty((need,), dtype=torch.uint8, device=like.device)
-    _req(work, "work", torch.uint8)
+        return torch.empty((need,), dtype=torch.uint8, device=cache.device)
+    if _req(work, "work", torch.uint8).get_device() != cache.index:
+        _elsewhere(work, "work", cache.index)
     if work.numel() < need:
         raise ValueError(f"work: {work.numel()} bytes, needs {need}")
     return work
@@ -583,22 +597,22 @@ def qlin_kv_append(cache, k, v, table, slot, row=None, position=None, mass=None,
     (None: token t is row t), quantized as the cache holds them.  With mass
     (float32) and pos (int32) [B, kv_heads, ld] and position int32 [T]: mass = 0
     and pos = position at the new slots."""
-    lib = _lib.load()
-    B, max_pages = _table(table)
-    T, ld_k = _rows3(k, "k", cache.kv_heads, cache.head_dim)
-    Tv, ld_v = _rows3(v, "v", cache.kv_heads, cache.head_dim)
+    lib, index = _lib.load(), cache.index
+    B, max_pages = _table(table, index)
+    T, ld_k = _rows3(k, "k", cache.kv_heads, cache.head_dim, index)
+    Tv, ld_v = _rows3(v, "v", cache.kv_heads, cache.head_dim, index)
     if Tv != T:
         raise ValueError(f"k holds {T} tokens, v {Tv}")
     tokens = (T,)
-    slot_p = _is(slot, "slot", torch.int32, tokens)
-    row_p = _maybe(row, "row", torch.int32, tokens)
+    slot_p = _is(slot, "slot", torch.int32, tokens, index)
+    row_p = _maybe(row, "row", torch.int32, tokens, index)
     ld = 0
     mass_p = pos_p = position_p = None
     if mass is not None or pos is not None or position is not None:
-        ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads)
+        ld = _tracked(mass, "mass", torch.float32, B, cache.kv_heads, index)
         mass_p = mass.data_ptr()
-        pos_p = _is(pos, "pos", torch.int32, mass.shape)
-        position_p = _is(position, "position", torch.int32, tokens)
+        pos_p = _is(pos, "pos", torch.int32, mass.shape, index)
+        position_p = _is(position, "position", torch.int32, tokens, index)
     if T == 0:
         return
     st = lib.qlin_kv_append(cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, row_p, slot_p, table.data_ptr(), B,
@@ -621,26 +635,26 @@ def qlin_attn_decode(cache, q, table, lens, max_len, scale=None, window=0, mass=
     be mass itself.  work: a uint8 workspace of at least
     qlin_attn_decode_work_bytes(cache, heads, B, max_len, window, mass_out is
     not None) bytes, or None to allocate one.  Returns (out, mass_out)."""
-    lib = _lib.load()
-    B, max_pages = _table(table)
+    lib, index = _lib.load(), cache.index
+    B, max_pages = _table(table, index)
     shape = q.shape
     if len(shape) != 3:
         raise ValueError(f"q: expected [B, heads, {cache.head_dim}], got {tuple(shape)}")
     heads = shape[1]
-    Bq, ld_q = _rows3(q, "q", heads, cache.head_dim)
+    Bq, ld_q = _rows3(q, "q", heads, cache.head_dim, index)
     if Bq != B:
         raise ValueError(f"q holds {Bq} sequences, table {B}")
-    lens_p = _is(lens, "lens", torch.int32, (B,))
+    lens_p = _is(lens, "lens", torch.int32, (B,), index)
     if out is None:
         out = torch.empty(shape, dtype=torch.float16, device=cache.device)
     else:
-        _is(out, "out", torch.float16, shape)
+        _is(out, "out", torch.float16, shape, index)
     ld = 0
     mass_p = mass_out_p = None
     if mass_out is not None:
-        ld = _tracked(mass_out, "mass_out", torch.float32, B, cache.kv_heads)
+        ld = _tracked(mass_out, "mass_out", torch.float32, B, cache.kv_heads, index)
         mass_out_p = mass_out.data_ptr()
-        mass_p = _maybe(mass, "mass", torch.float32, mass_out.shape)
+        mass_p = _maybe(mass, "mass", torch.float32, mass_out.shape, index)
     elif mass is not None:
         raise ValueError("mass needs mass_out")
     if B == 0:
@@ -648,7 +662,7 @@ def qlin_attn_decode(cache, q, table, lens, max_len, scale=None, window=0, mass=
     if scale is None:
         scale = cache.head_dim ** -0.5
     need = lib.qlin_attn_decode_work_bytes(cache._ref, heads, B, max_len, window, mass_out is not None)
-    work = _work(work, need, q)
+    work = _work(work, need, cache)
     st = lib.qlin_attn_decode(cache._ref, q.data_ptr(), ld_q, heads, table.data_ptr(), lens_p, B, max_pages, max_len,
                               scale, window, out.data_ptr(), mass_p, mass_out_p, ld, _ptr(work), _raw_stream(cache))
     if st:
@@ -669,13 +683,13 @@ def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_o
     qlin_kv_evict_work_bytes(cache, B, max_len, budget) bytes, or None to
     allocate one.  Returns (lens_out [B], kept [B, kv_heads, budget], mass_out,
     pos_out); kept holds the old slot of each new one, -1 past lens_out."""
-    lib = _lib.load()
-    B, max_pages = _table(table)
+    lib, index = _lib.load(), cache.index
+    B, max_pages = _table(table, index)
     heads = cache.kv_heads
-    lens_p = _is(lens, "lens", torch.int32, (B,))
-    ld = _tracked(mass, "mass", torch.float32, B, heads)
+    lens_p = _is(lens, "lens", torch.int32, (B,), index)
+    ld = _tracked(mass, "mass", torch.float32, B, heads, index)
     shape = mass.shape
-    mass_p, pos_p = mass.data_ptr(), _is(pos, "pos", torch.int32, shape)
+    mass_p, pos_p = mass.data_ptr(), _is(pos, "pos", torch.int32, shape, index)
     if mass_out is None:
         mass_out = mass
     if pos_out is None:
@@ -684,13 +698,15 @@ def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_o
         lens_out = torch.empty_like(lens)
     if kept is None:
         kept = torch.empty((B, heads, budget), dtype=torch.int32, device=cache.device)
-    mass_out_p, pos_out_p = _is(mass_out, "mass_out", torch.float32, shape), _is(pos_out, "pos_out", torch.int32, shape)
-    lens_out_p, kept_p = _is(lens_out, "lens_out", torch.int32, (B,)), _is(kept, "kept", torch.int32, (B, heads, budget))
+    mass_out_p = _is(mass_out, "mass_out", torch.float32, shape, index)
+    pos_out_p = _is(pos_out, "pos_out", torch.int32, shape, index)
+    lens_out_p = _is(lens_out, "lens_out", torch.int32, (B,), index)
+    kept_p = _is(kept, "kept", torch.int32, (B, heads, budget), index)
     if B == 0:
         return lens_out, kept, mass_out, pos_out
     if lens_out_p == lens_p:
         raise ValueError("lens_out must not be lens")
-    work = _work(work, lib.qlin_kv_evict_work_bytes(cache._ref, B, max_len, budget), lens)
+    work = _work(work, lib.qlin_kv_evict_work_bytes(cache._ref, B, max_len, budget), cache)
     st = lib.qlin_kv_evict(cache._ref, table.data_ptr(), lens_p, B, max_pages, max_len, budget, recent, mass_p, pos_p, ld,
                            mass_out_p, pos_out_p, lens_out_p, kept_p, _ptr(work), _raw_stream(cache))
     if st:
