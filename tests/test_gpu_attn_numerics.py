@@ -135,3 +135,28 @@ def test_one_large_channel_of_the_query(q, bits, D, rotate):
     qh = rng.standard_normal((1, 3, D)).astype(np.float16)
     qh[:, 0, 6], qh[:, 1, 7], qh[:, 2, D - 1] = 3000, -65504, 60000
     _check(q, c, qh, D ** -0.5 / 100)
+
+
+@pytest.mark.parametrize("bits,D,rotate", FORMS)
+@pytest.mark.parametrize("step", [2.0 ** -3, 2.0 ** -7])
+def test_weights_in_two_parts(q, bits, D, rotate, step):
+    # V in pairs that cancel, weights nearly equal: the output's rounding hides
+    # little of what the weights lose.
+    log(f"attend cancelling V bits={bits} D={D} rotate={rotate} step={step}")
+    rng = np.random.default_rng(bits + D)
+    c = HostCache(rng, [20, 200], 200, 2, D, 16, bits, rotate, outliers=False)
+    for b, n in enumerate((20, 200)):
+        kv_cases.cancelling_v(rng, c, b, n, step)
+    qh = rng.standard_normal((2, 8, D)).astype(np.float16)
+    _check(q, c, qh, D ** -0.5 / 64)
+
+
+@pytest.mark.parametrize("bits,D,rotate", FORMS)
+def test_rows_of_one_workgroup_and_of_several(q, bits, D, rotate):
+    # Both sides of the length from which rows are divided, and outliers in K.
+    log(f"attend 512 and 513 slots bits={bits} D={D} rotate={rotate}")
+    for n in (511, 512, 513):
+        rng = np.random.default_rng(n)
+        c = HostCache(rng, [n, 3, 0, 480], n, 2, D, 32, bits, rotate)
+        qh = rng.standard_normal((4, 6, D)).astype(np.float16)
+        _check(q, c, qh, D ** -0.5, max_len=n)
