@@ -126,3 +126,26 @@ def test_more_newest_slots_than_fit(q, n, kind):
     _check(q, c, mass, np.zeros_like(pos), n // 2, 1, n, True)
     mass, pos = _rows(rng, c, kind)
     _check(q, c, mass, pos, n // 2, n // 2, n, False)
+
+
+@pytest.mark.parametrize("n", [1535, 1536, 1537, 8191, 20479])
+def test_rows_as_long_as_a_kernel_takes(q, n):
+    # The lengths at which another kernel takes over: 1,536, 8,192 and 20,480.
+    log(f"evict n={n}")
+    rng = np.random.default_rng(n)
+    c = HostCache(rng, [n, n - 1, 700], n, 1, 64, 64, 4)
+    for kind in ("spread", "odd"):
+        mass, pos = _rows(rng, c, kind)
+        _check(q, c, mass, pos, n - 1, 9, n, False)
+        _check(q, c, mass, pos, n // 2, 100, n, True)
+
+
+@pytest.mark.parametrize("over", [63, 64, 65, 127, 128, 129])
+def test_moves_by_the_selecting_workgroup_and_by_a_second_launch(q, over):
+    # 16 KiB of moves: 64 slots of 128-byte rows.
+    log(f"evict {over} over")
+    rng = np.random.default_rng(over)
+    for bits, D in ((4, 128), (8, 128), (4, 256)):
+        c = HostCache(rng, [400 + over, 400, 399], 400 + over, 2, D, 16, bits)
+        mass, pos = _rows(rng, c)
+        _check(q, c, mass, pos, 400, 20, 400 + over, False)
