@@ -545,7 +545,8 @@ typedef struct qlin_kv_cache {
  * 1, 2, .., 64 for K with signs), qmax = 2^bits - 1:
  *   lo = fp16(min t), step = fp16((max t - lo) * fp32(1 / qmax)),
  *   code = clamp(rint((t - lo) * (1 / step)), 0, qmax)   (0 if step == 0)
- * A row that is not finite reads back as not finite.
+ * A row that is not finite reads back as not finite; so does a turned one whose
+ * least value, or step, lies beyond fp16's range.
  *   k, v      fp16 [T x kv_heads x head_dim], ld_k and ld_v elements between
  *             tokens (a multiple of 8, so a slice of a fused projection's
  *             output will do)
