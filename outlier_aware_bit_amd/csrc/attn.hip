@@ -150,16 +150,6 @@ __device__ __forceinline__ void attn_tiles(int low, int n, int& t0, int& t1) {
   t0 = low / kTile;
   t1 = (n + kTile - 1) / kTile;
 }
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // one lane up, in rows of 16
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
-  return v;
-}
 // x / y of numbers that are the same in every lane, y > 0: 32 bits where they do.
 __device__ __forceinline__ int64_t attn_div(int64_t x, int64_t y) {
   if (x <= 0x7fffffff && y <= 0x7fffffff) return uniform_i32(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));

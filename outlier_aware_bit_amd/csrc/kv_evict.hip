@@ -77,16 +77,6 @@ __device__ __forceinline__ int max_wave(int v) {
   v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));  // lane 31 to rows 2 and 3
   return __builtin_amdgcn_readlane(v, 63);
 }
-// Inclusive sum over the lanes.
-__device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // one lane up, in rows of 16
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
-  return v;
-}
 
 // Rows of which no more bytes than this can move are moved by the workgroup
 // that selected them: 128 rows, 1 and 128 slots of 128 bytes over, 9.9 and 11.0
@@ -324,7 +314,7 @@ __global__ __launch_bounds__(THREADS) void kv_select_kernel(EvictArgs a) {
       const uint4 digits = digits4[lane];
       const uint32_t c[4] = {digits.x, digits.y, digits.z, digits.w};
       const uint32_t sum = c[0] + c[1] + c[2] + c[3];
-      uint32_t above = scan_wave(sum) - sum;
+      uint32_t above = wave_scan(sum) - sum;
       uint32_t digit = 0, rest = 0, whole = 0, here = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
