@@ -8,8 +8,9 @@ those with the largest weight, and decoding goes on in the same memory.
 
     python examples/decode_kv4.py [--bits 4] [--batch 8] [--steps 512] ...
 
-Weights and hidden states are random; one line per eviction and a summary are
-printed.  Needs the GPU and a built library.
+Prompts are stored without attending to them, so their slots begin with no
+weight.  Weights and hidden states are random; a summary is printed.  Needs the
+GPU and a built library.
 """
 import argparse
 import os

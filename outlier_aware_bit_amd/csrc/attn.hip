@@ -27,10 +27,11 @@
 // workgroups leaves a maximum, a sum and a vector in each, which a second launch
 // joins.  Rows that are one short run each need no second launch.
 //
-// Bound by the bytes of K and V, read once: 32 sequences of 500 - 4,000 slots,
-// 32 kv heads of 128 channels, fp16, 1,180 MB, 206 us or 5.7 TB/s (a plain read
+// Bound by the bytes of K and V, read once (each eight query heads of a larger
+// group read them again, from cache where it holds them): 32 sequences of 500 - 4,000 slots,
+// 32 kv heads of 128 channels, fp16, 1,180 MB, 209 us or 5.6 TB/s (a plain read
 // of that size reaches 6.4); 64 of 1,500 - 12,000, 8 kv heads, int4, 471 MB and
-// 55 MB of logits, 116 us or 4.5 TB/s (a copy reaches 5.2), vector instructions
+// 55 MB of logits, 118 us or 4.5 TB/s (a copy reaches 5.2), vector instructions
 // 40 % and matrix instructions 9 % of the time.  Small calls are bound by their
 // chain of waits: launch, lens, page ids, q and the first tile, the join of the
 // waves: 7 us for 100 slots; 65,537 slots of 8 kv heads int4, 71 MB, 21 us and 4
@@ -299,7 +300,9 @@ inline size_t attn_lds(int D, int row_heads, bool rot) {
 
 // Workgroups that a CU holds: as many as fit with two tiles in registers, so
 // that the next one is on its way while one is computed on.  One more spills
-// (D = 256, int4, 64 sequences: 282 us against 192).  The launch has as many as
+// (D = 256, int4, 64 sequences: 282 us against 192).  fp16 rows of D = 256 do not
+// quite fit even so: 5 registers a lane go to scratch, 12 with logits (16 sequences
+// of 2,000 - 8,000 slots, 4 kv heads, 72 us, 4.5 TB/s).  The launch has as many as
 // the GPU holds at a time; twice or three times as many, each with half or a
 // third of the work, took 38 and 47 us where one does 65,537 slots in 29.
 constexpr int attn_resident(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
