@@ -968,8 +968,13 @@ struct AttnPlan {
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Rows of at most this many tiles are one workgroup each: no second launch.
-// One sequence, 32 kv heads, fp16: 512 slots 10.2 us as one workgroup each, 8.4
-// and 3.2 us divided and joined; 1,024 slots 16.2 against 8.9 and 3.3 us.
+// Both launches, replayed from a graph, 128 channels, 4 query heads a kv head, as
+// one workgroup each against divided and joined: one row of 512 slots 8.9 against
+// 9.1 us (fp16), 7.7 against 9.4 (int8), 8.1 against 10.0 (int4), of 1,024 13.1
+// against 9.4, 10.6 against 9.2, 10.8 against 10.0; 32 rows of 512 9.2 against 10.4,
+// 8.0 against 10.0, 8.5 against 10.5, of 1,024 14.6 against 11.6, 11.3 against 10.4,
+// 11.5 against 10.8.  (128 rows of 1,024 would be faster whole: 15.4 against 18.7,
+// 12.2 against 17.6, 12.3 against 14.8.)
 constexpr int64_t kWholeTiles = 16;
 
 AttnPlan attn_plan(const qlin_kv_cache& c, int32_t heads, int64_t B, int64_t max_len, int32_t window, bool mass) {
