@@ -633,6 +633,174 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const int32_t* table, cons
 /* Bytes of the qlin_kv_evict workspace (0 for invalid arguments). Host only. */
 size_t qlin_kv_evict_work_bytes(const qlin_kv_cache* cache, int64_t B, int64_t max_len, int32_t budget);
 
+/* ------------------------------------------------------------------------
+ * Around the cache's decoding step: where new tokens go, their positions, and
+ * attention over whole prompts, forward and backward (OffQ serves models, Quaff
+ * trains them; both pages take the rest of the layer as given)
+ * --------------------------------------------------------------------- */
+
+/*
+ * qlin_kv_slots -- where a step's new tokens go.  Sequence b, with lens[b]
+ * slots, takes add[b] tokens; the tokens of all sequences follow one another.
+ * A negative length counts as 0.
+ *   lens, add int32 [B] (B at most 65535); first int32 [B]: the position of the
+ *             sequence's next token, or NULL (lens: nothing was evicted)
+ *   T         tokens that the arrays have room for; those past T have no place
+ *   cu        int32 [B + 1] out: cu[b] is the first token of sequence b (at most
+ *             T), as qlin_attn_prompt takes it
+ *   row, slot, position  int32 [T] out, as qlin_kv_append and qlin_rope take
+ *             them: b, lens[b] + i and first[b] + i for token i of sequence b; -1
+ *             in all three behind the last token
+ *   lens_out  int32 [B] out: lens + add (not the array lens, add or first)
+ */
+qlin_status qlin_kv_slots(const int32_t* lens, const int32_t* add, const int32_t* first, int64_t B,
+                          int64_t T, int32_t* cu, int32_t* row, int32_t* slot, int32_t* position,
+                          int32_t* lens_out, void* stream);
+
+/*
+ * qlin_kv_pages -- bring every sequence's pages to its length: row b of the
+ * table needs ceil(want[b] / page) pages.  Free pages are a ring: `count` ids
+ * from ring[head] on, around the end of the array.  In row order, rows that
+ * lack pages take them from the head, as long as they last: the first row whose
+ * pages are not all there, and every later one that lacks any, gets none and
+ * keeps what it holds (a row that needs more than max_pages does, too, but
+ * takes no one's place).  Pages past a row's need go to the tail, in row order, and their
+ * entries become -1; a call does not hand them out again itself.
+ *   want      int32 [B] slots (a negative one counts as 0); B at most 65535
+ *   page      slots per page, a power of two from 16 to 1024
+ *   table     int32 [B x max_pages];  held int32 [B]: entries of each row in use,
+ *             from the first on
+ *   ring      int32 [pages] in/out, with room for every page;  state int32 [2]:
+ *             head, count
+ *   table_out, held_out, state_out  the same shapes; each may be its input
+ *   missing   int32 [1] out: pages that rows lack after the call
+ * No page id is looked at; a ring or a table whose counts contradict each other
+ * gives unspecified ids, and nothing out of bounds.
+ */
+qlin_status qlin_kv_pages(const int32_t* want, int64_t B, int64_t max_pages, int32_t page,
+                          const int32_t* table, const int32_t* held, int32_t* ring, int64_t pages,
+                          const int32_t* state, int32_t* table_out, int32_t* held_out,
+                          int32_t* state_out, int32_t* missing, void* stream);
+
+/* How qlin_rope_freqs scales frequencies for contexts longer than trained on. */
+#define QLIN_ROPE_PLAIN 0  /* not at all                                              */
+#define QLIN_ROPE_LINEAR 1 /* every frequency over the factor                         */
+#define QLIN_ROPE_BASE 2   /* base * factor^(rot_dim / (rot_dim - 2)): the slowest    */
+                           /* pair over the factor, the fastest as it was             */
+#define QLIN_ROPE_RAMP 3   /* pairs that turn more than `fast` times in original_len  */
+                           /* positions as they were, fewer than `slow` times over    */
+                           /* the factor, linearly in the pair in between;            */
+                           /* amplitude 0.1 ln(factor) + 1                            */
+
+/*
+ * qlin_rope_freqs -- the frequencies of a model's rotary positions, in radians
+ * per position: freq[i] = base^(-2 i / rot_dim), scaled.  Host only: freq (float64
+ * [rot_dim / 2]) and amplitude are HOST pointers.
+ *   rot_dim  a multiple of 16, from 16 to 256;  base above 1;  factor at least 1
+ *   original_len, fast, slow   for QLIN_ROPE_RAMP (0 < slow < fast)
+ */
+qlin_status qlin_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                            int64_t original_len, double fast, double slow, double* freq,
+                            float* amplitude);
+
+/*
+ * qlin_rope -- turn the first rot_dim channels of every q and k row by its
+ * token's position: with a = position * freq[i] (reduced in 64 bits),
+ *   (x, y) -> amplitude * (x cos a - y sin a, x sin a + y cos a)
+ * for the channels (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved;
+ * other channels are copied.  fp32 products, one rounding to fp16.
+ *   q, k      fp16 [T x heads x head_dim] and [T x kv_heads x head_dim], ld_q and
+ *             ld_k elements between tokens (multiples of 8); k and k_out may be
+ *             NULL with kv_heads == 0.  head_dim 64, 128 or 256
+ *   rot_dim   a multiple of 16, at most head_dim
+ *   position  int32 [T]; a token with a negative one is left as it was, in the
+ *             outputs too
+ *   freq      float64 [rot_dim / 2] (qlin_rope_freqs, or any other)
+ *   inverse   non-zero: by -a, which with the same amplitude is the backward pass
+ *   q_out, k_out  fp16, ld_qo and ld_ko elements between tokens; each either its
+ *             input (then with the same stride) or apart from both inputs
+ */
+qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k, int64_t ld_k,
+                      int32_t kv_heads, int64_t T, int32_t head_dim, int32_t rot_dim,
+                      int32_t interleaved, const int32_t* position, const double* freq,
+                      float amplitude, int32_t inverse, uint16_t* q_out, int64_t ld_qo,
+                      uint16_t* k_out, int64_t ld_ko, void* stream);
+
+/*
+ * qlin_attn_prompt -- attention of whole prompts: B sequences, their tokens one
+ * after another, sequence b's queries q[cu_q[b] .. cu_q[b + 1]) and keys
+ * cu_k[b] .. cu_k[b + 1].  With nq and nk of them, query i sees key j if
+ *   causal:      j <= i + nk - nq (the last query sees the last key), and, with a
+ *                window, j > i + nk - nq - window
+ *   not causal:  always
+ *   s_j = scale * q_i . k_j,  p = softmax(s),  out_i = fp16(sum_j p_j v_j),
+ *   lse_i = log sum_j exp(s_j)
+ * A query that sees no key, or whose logits are all -inf, gives zeros and lse =
+ * -inf.  Logits, maxima, sums and outputs are held in fp32; p enters the second
+ * product as fp16, to 2^-11 of itself (below 2^-21 of the row's largest, to 2^-32
+ * of that).  A K or V that is not finite makes those rows' outputs so that see
+ * it, and no others.  The same call gives the same bits.
+ *   q         fp16 [Tq x heads x head_dim], ld_q elements between tokens; k, v
+ *             fp16 [Tk x kv_heads x head_dim], ld_k and ld_v: multiples of 8, at
+ *             most 2^22 (slices of a fused projection's output will do).  heads a
+ *             multiple of kv_heads, query head j reads kv head
+ *             j / (heads / kv_heads); head_dim 64, 128 or 256
+ *   cu_q, cu_k  int32 [B + 1] (device), not decreasing; may be one array.  B at
+ *             most 65535.  Borders past Tq or Tk are taken to be there
+ *   causal    0 or not;  window  0 (none), or with causal the keys a query sees
+ *   out       fp16 [Tq x heads x head_dim], contiguous; rows of no sequence are
+ *             left as they were
+ *   lse       fp32 [heads x Tq] or NULL
+ *   work      device workspace of qlin_attn_prompt_work_bytes(..) bytes, 16-byte
+ *             aligned (NULL if that is 0); its contents on entry do not matter.
+ *             Calls that overlap must not share it.
+ */
+qlin_status qlin_attn_prompt(const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k,
+                             int64_t ld_k, const uint16_t* v, int64_t ld_v, int32_t kv_heads,
+                             int32_t head_dim, const int32_t* cu_q, const int32_t* cu_k, int64_t B,
+                             int64_t Tq, int64_t Tk, float scale, int32_t causal, int32_t window,
+                             uint16_t* out, float* lse, void* work, void* stream);
+
+/* Bytes of the qlin_attn_prompt workspace (0 for invalid arguments). Host only. */
+size_t qlin_attn_prompt_work_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B,
+                                   int64_t Tq, int64_t Tk, int32_t causal, int32_t window);
+
+/*
+ * qlin_attn_prompt_backward -- gradients of qlin_attn_prompt's out with respect
+ * to q, k and v.  With p = exp(s - lse), delta_i = dout_i . out_i and
+ * dp_ij = dout_i . v_j:
+ *   ds = p (dp - delta),  dq_i = fp16(scale sum_j ds_ij k_j),
+ *   dk_j = fp16(scale sum_i ds_ij q_i),  dv_j = fp16(sum_i p_ij dout_i)
+ * the last two over all query heads of the kv head.  Sums are held in fp32; p
+ * and ds enter their products as fp16, to 2^-11 of themselves, ds times a power
+ * of two that follows its size (2^-25 of the largest of the row, for dk of the
+ * rows before, is still a normal number), so gradients of any size keep their
+ * bits.  A key that no query sees, and a query that sees no key, has zeros.  A
+ * value that is not finite makes its own sequence's gradients so, wherever it
+ * stands there, and no other's.  The same call gives the same bits.
+ *   dout      fp16 [Tq x heads x head_dim], ld_dout elements between tokens; the
+ *             strides' rules are those of ld_q
+ *   q, k, v, cu_q, cu_k, scale, causal, window   as in the forward call, and out
+ *             (contiguous) and lse as it wrote them
+ *   dq, dk, dv  fp16, shaped as q, k and v, ld_dq, ld_dk and ld_dv elements
+ *             between tokens (slices of one gradient of the projection will do);
+ *             rows of no sequence are left as they were
+ *   work      device workspace of qlin_attn_prompt_backward_work_bytes(heads, Tq)
+ *             bytes, 16-byte aligned; its contents on entry do not matter.  Calls
+ *             that overlap must not share it.
+ * Two launches.
+ */
+qlin_status qlin_attn_prompt_backward(
+    const uint16_t* dout, int64_t ld_dout, const uint16_t* q, int64_t ld_q, int32_t heads,
+    const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int32_t kv_heads,
+    int32_t head_dim, const uint16_t* out, const float* lse, const int32_t* cu_q,
+    const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, float scale, int32_t causal,
+    int32_t window, uint16_t* dq, int64_t ld_dq, uint16_t* dk, int64_t ld_dk, uint16_t* dv,
+    int64_t ld_dv, void* work, void* stream);
+
+/* Bytes of the qlin_attn_prompt_backward workspace (0 for invalid arguments). Host only. */
+size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int64_t Tq);
+
 #ifdef __cplusplus
 }
 #endif

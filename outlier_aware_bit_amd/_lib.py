@@ -15,6 +15,7 @@ p = C.c_void_p
 i32 = C.c_int32
 i64 = C.c_int64
 f32 = C.c_float
+f64 = C.c_double
 
 # name -> (restype, argtypes); mirrors include/qlin.h
 SIGNATURES = {
@@ -52,6 +53,15 @@ SIGNATURES = {
     "qlin_attn_decode_work_bytes": (C.c_size_t, [p, i32, i64, i64, i32, i32]),
     "qlin_kv_evict": (i32, [p, p, p, i64, i64, i64, i32, i32, p, p, i64, p, p, p, p, p, p]),
     "qlin_kv_evict_work_bytes": (C.c_size_t, [p, i64, i64, i32]),
+    "qlin_kv_slots": (i32, [p, p, p, i64, i64, p, p, p, p, p, p]),
+    "qlin_kv_pages": (i32, [p, i64, i64, i32, p, p, p, i64, p, p, p, p, p, p]),
+    "qlin_rope_freqs": (i32, [i32, f64, i32, f64, i64, f64, f64, p, p]),
+    "qlin_rope": (i32, [p, i64, i32, p, i64, i32, i64, i32, i32, i32, p, p, f32, i32, p, i64, p, i64, p]),
+    "qlin_attn_prompt": (i32, [p, i64, i32, p, i64, p, i64, i32, i32, p, p, i64, i64, i64, f32, i32, i32, p, p, p, p]),
+    "qlin_attn_prompt_work_bytes": (C.c_size_t, [i32, i32, i32, i64, i64, i64, i32, i32]),
+    "qlin_attn_prompt_backward": (i32, [p, i64, p, i64, i32, p, i64, p, i64, i32, i32, p, p, p, p, i64, i64, i64, f32,
+                                        i32, i32, p, i64, p, i64, p, i64, p, p]),
+    "qlin_attn_prompt_backward_work_bytes": (C.c_size_t, [i32, i64]),
     "qlin_quaff_backward": (i32, [p, i64, i64, i64, p, p, p, p, p, i32, p, p, p, p, p, p, p]),
 }
 
@@ -73,6 +83,10 @@ QLIN_LAYOUT_W4S = 2
 QLIN_LAYOUT_W4U = 3
 QLIN_LAYOUT_WO = 4
 QLIN_LAYOUT_W8T = 5
+QLIN_ROPE_PLAIN = 0
+QLIN_ROPE_LINEAR = 1
+QLIN_ROPE_BASE = 2
+QLIN_ROPE_RAMP = 3
 
 _lib = None
 

@@ -1,0 +1,390 @@
+// Attention over whole prompts (qlin_attn_prompt).
+//
+// Per workgroup 128 queries of one head, 32 of them to a wave; the keys in tiles
+// of 64.  On 32x32x16 fp16 matrix instructions
+//   S^T = K Q^T (keys x queries),  P = exp2(c S - m),  O^T = V^T P^T (D x queries)
+// so that a lane holds one query in both products: the softmax's maximum and
+// sum are taken down a lane's registers and across one exchange, the rescaling
+// of O is one factor per lane, and P leaves the first product in the registers
+// where the second takes it, if the keys of each 16 are taken in the order
+// {0-3, 8-11 | 4-7, 12-15}.  K and V go through LDS, loaded there directly; V is
+// read from it transposed.
+#include <math.h>
+
+#include "prompt.hpp"
+
+namespace qlin {
+namespace {
+
+struct PromptArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t ld_q, ld_k, ld_v;
+  int32_t heads, group;
+  Borders s;
+  float c;       // |scale| log2(e)
+  uint32_t flip;  // sign bits of a pair of q's values: scale is negative
+  int32_t causal;
+  int32_t window;  // 0: none
+  uint16_t* out;
+  float* lse;  // [heads x Tq] or null
+  int32_t splits;
+  float* part_o;    // [splits x heads x Tq x D], with splits > 1
+  float2* part_ml;  // [splits x heads x Tq]: reference exponent and sum
+};
+
+constexpr int kKeys = 64;
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;
+
+// Weights are exp2(c s - m + kTop); m is the largest c s seen when it was last
+// set, and is set again where one passes it by kSlack: weights stay below 2^15,
+// the largest at or above 2^kTop, and fp16 has them to 2^-11 down to 2^-21 of the
+// largest, and to 2^-32 of it below.
+constexpr float kTop = 7.0f, kSlack = 8.0f;
+constexpr float kNoRef = -1.0e30f;  // the reference of nothing
+
+// Infinities and NaN as 0.
+__device__ __forceinline__ v4i finite_only(v4i x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = x[i];
+    x[i] = w & (((w & 0x7c00u) == 0x7c00u ? 0u : 0xffffu) | ((w & 0x7c000000u) == 0x7c000000u ? 0u : 0xffff0000u));
+  }
+  return x;
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt_kernel(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32;
+  constexpr int kBytes = kKeys * D * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  uint32_t head, slot;
+  head_and_slot(blockIdx.x, a.heads, head, slot);
+  slot = gridDim.x / a.heads - 1 - slot;  // causal rows at the end see the most: they begin first
+  int64_t tile;
+  const int64_t b = find_tile<kRows>(a.s.cu_q, a.s.B, slot, tile);
+  const Seq s = sequence(a.s, b);
+  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
+  if (tile < 0 || tile * kRows >= nq) return;
+  const int row0 = static_cast<int>(tile) * kRows;
+  const int i0 = row0 + 32 * wave;  // the wave's first query, in its sequence
+  const int i = i0 + col;
+  const int kvh = head / a.group;
+
+  // Keys [lo, lo + span) are the ones that a query sees.
+  const int hi = a.causal ? clamp_i32(i + shift + 1, 0, nk) : nk;
+  const int lo = a.window > 0 ? clamp_i32(i + shift + 1 - a.window, 0, hi) : 0;
+  const uint32_t span = hi - lo;
+  // ... and the wave's first and last query, and the workgroup's.
+  auto top_of = [&](int r) { return a.causal ? clamp_i32(r + shift + 1, 0, nk) : nk; };
+  auto low_of = [&](int r) { return a.window > 0 ? clamp_i32(r + shift + 1 - a.window, 0, nk) : 0; };
+  const int hi_first = top_of(i0), hi_last = top_of(i0 + 31), lo_first = low_of(i0), lo_last = low_of(i0 + 31);
+  int kbeg = low_of(row0);
+  const int kend = top_of((row0 + kRows < nq ? row0 + kRows : nq) - 1);
+  int tiles = kend > kbeg ? (kend - kbeg + kKeys - 1) / kKeys : 0;
+  if (a.splits > 1) {
+    const int from = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.y / a.splits);
+    const int to = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.y + 1) / a.splits);
+    kbeg += from * kKeys;
+    tiles = to - from;
+  }
+
+  // Q^T as the second operand: a lane holds 8 channels of its query per step.
+  v8h qf[KS];
+  {
+    const bool there = i < nq;
+    const uint16_t* q = a.q + (s.q0 + (there ? i : 0)) * a.ld_q + head * D + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      v4i w = *reinterpret_cast<const v4i*>(q + 16 * ks);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = there ? w[j] ^ a.flip : 0;
+      qf[ks] = __builtin_bit_cast(v8h, w);
+    }
+  }
+
+  const uint16_t* kb = a.k + s.k0 * a.ld_k + kvh * D;
+  const uint16_t* vb = a.v + s.k0 * a.ld_v + kvh * D;
+  TileLoad<D, kKeys, kWaves> kl, vl;
+  kl.init(a.ld_k, wave, lane);
+  vl.init(a.ld_v, wave, lane);
+  auto fetch = [&](int t) {
+    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+    const int64_t at = kbeg + t * kKeys;
+    kl.load(kb + at * a.ld_k, a.ld_k, nk - static_cast<int>(at), to, wave);
+    vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
+  };
+
+  // The lane's part of a transposing read: key lane / 4 of four, four channels.
+  const int key4 = (lane & 15) >> 2, ch = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  auto v_of = [&](const uint8_t* vt, int x, int d) {
+    const int r = 16 * x + 4 * half + key4, e = 32 * d + ch;
+    return join_halves(lds_transposed(vt + lds_at<D>(r, e >> 3) + 2 * (e & 7)),
+                       lds_transposed(vt + lds_at<D>(r + 8, e >> 3) + 2 * (e & 7)));
+  };
+  // Some of the wave's, or of the workgroup's, queries do not see some of these keys.
+  const int all_lo = low_of(row0 + kRows - 1), all_hi = top_of(row0);
+  auto shared_cut = [&](int k0) { return k0 < all_lo || k0 + kKeys > all_hi; };
+  auto cut = [&](int k0) { return k0 < lo_last || k0 + kKeys > hi_first; };
+  auto skipped = [&](int k0) { return k0 >= hi_last || k0 + kKeys <= lo_first; };
+
+  v16f o[DT];
+  float m, l;
+  bool careful = false;
+again:
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+  m = kNoRef;
+  l = 0.0f;
+  if (tiles > 0) fetch(0);
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();  // tile t has arrived; the tile before it is used up
+    if (t + 1 < tiles) fetch(t + 1);
+    const int k0 = kbeg + t * kKeys;
+    if (careful && shared_cut(k0)) {
+      v4i* v = reinterpret_cast<v4i*>(lds + (t & 1) * 2 * kBytes + kBytes);
+      for (int x = tid; x < kBytes / 16; x += 64 * kWaves) v[x] = finite_only(v[x]);
+      tile_barrier();
+    }
+    if (skipped(k0)) continue;
+    const uint8_t* kt = lds + (t & 1) * 2 * kBytes;
+    const uint8_t* vt = kt + kBytes;
+    v16f st[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st[n][r] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const v8h kf = *reinterpret_cast<const v8h*>(kt + lds_at<D>(32 * n + col, 2 * ks + half));
+        st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], st[n], 0, 0, 0);
+      }
+    }
+    if (cut(k0)) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const uint32_t j = k0 + 32 * n + frag_row(r, lane) - lo;
+          st[n][r] = j < span ? st[n][r] : -INFINITY;
+        }
+    }
+    float top = st[0][0];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, st[n][r]);
+    top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.c;
+    if (__any(top > m + kSlack)) {
+      // Each query by itself: its bits do not depend on its neighbours'.
+      const float now = top > m + kSlack ? top : m, f = __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] *= f;
+    }
+    const float ref = kTop - m;
+    v8h pf[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        st[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][r], a.c, ref));
+        l += st[n][r];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        pf[2 * n + x] = pack8(st[n][8 * x], st[n][8 * x + 1], st[n][8 * x + 2], st[n][8 * x + 3], st[n][8 * x + 4],
+                              st[n][8 * x + 5], st[n][8 * x + 6], st[n][8 * x + 7]);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_of(vt, x, d), pf[x], o[d], 0, 0, 0);
+  }
+
+  // A weight of 0 does not keep a V that is not finite out of a sum.  Where a row
+  // of the workgroup is not finite, all of it is done again with such values of V
+  // as 0 in the tiles that some query does not see whole, and the queries that do
+  // see one are marked after that.
+  if (!careful) {
+    float any = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) any = __builtin_fmaf(o[d][r], 0.0f, any);
+    careful = __syncthreads_or(any != 0.0f);
+    if (careful) goto again;
+  } else {
+    for (int t = 0; t < tiles; ++t) {
+      const int k0 = kbeg + t * kKeys;
+      if (!shared_cut(k0)) continue;
+      for (int j = k0; j < k0 + kKeys && j < nk; ++j) {
+        const bool seen = static_cast<uint32_t>(j - lo) < span;
+        const uint16_t* v = vb + j * a.ld_v + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v4h w = *reinterpret_cast<const v4h*>(v + 32 * d + 8 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = static_cast<float>(w[e]);
+              if (seen && x - x != 0.0f) o[d][4 * g + e] = __builtin_nanf("");
+            }
+          }
+      }
+    }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (a.splits > 1) {
+    if (i >= nq) return;
+    const int64_t at = (static_cast<int64_t>(blockIdx.y) * a.heads + head) * a.s.Tq + s.q0 + i;
+    if (half == 0) a.part_ml[at] = make_float2(m, l);
+    float* to = a.part_o + at * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(to + 32 * d + 8 * g) =
+            make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
+    return;
+  }
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  if (a.lse != nullptr && half == 0 && i < nq)
+    a.lse[static_cast<int64_t>(head) * a.s.Tq + s.q0 + i] =
+        l == 0.0f ? -INFINITY : (m - kTop + __builtin_amdgcn_logf(l)) * kLn2;
+  uint16_t* to = a.out + (static_cast<int64_t>(s.q0 + i) * a.heads + head) * D + 8 * half;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      // Channels 8 g + 4 half .. of this lane and the one across: each takes one whole run of eight.
+      const uint32_t a0 = pack_half(o[d][4 * g] * f, o[d][4 * g + 1] * f);
+      const uint32_t a1 = pack_half(o[d][4 * g + 2] * f, o[d][4 * g + 3] * f);
+      const uint32_t b0 = pack_half(o[d][4 * g + 4] * f, o[d][4 * g + 5] * f);
+      const uint32_t b1 = pack_half(o[d][4 * g + 6] * f, o[d][4 * g + 7] * f);
+      const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+      const v4i w = {static_cast<int>(x[0]), static_cast<int>(y[0]), static_cast<int>(x[1]), static_cast<int>(y[1])};
+      if (i < nq) *reinterpret_cast<v4i*>(to + 32 * d + 8 * g) = w;
+    }
+}
+
+// The parts of rows whose keys were divided: each thread joins eight channels.
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t d_shift) {
+  const int64_t rows = static_cast<int64_t>(a.heads) * a.s.Tq;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t at = u >> (d_shift - 3);
+  const int c = 8 * (static_cast<int>(u) & ((1 << (d_shift - 3)) - 1));
+  if (at >= rows) return;
+  const int64_t head = at / a.s.Tq, row = at - head * a.s.Tq;
+  // Rows of no sequence have no parts, and are left as they are.
+  const int32_t begin = a.s.cu_q[0], end = a.s.cu_q[a.s.B];
+  if (row < begin || row >= end) return;
+  float m = kNoRef;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * rows + at].x);
+  float l = 0.0f, o[8] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 p = a.part_ml[s * rows + at];
+    const float f = __builtin_amdgcn_exp2f(p.x - m);
+    l = __builtin_fmaf(p.y, f, l);
+    const float* x = a.part_o + ((s * rows + at) << d_shift) + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+  }
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  const v4i w = {static_cast<int>(pack_half(o[0] * f, o[1] * f)), static_cast<int>(pack_half(o[2] * f, o[3] * f)),
+                 static_cast<int>(pack_half(o[4] * f, o[5] * f)), static_cast<int>(pack_half(o[6] * f, o[7] * f))};
+  *reinterpret_cast<v4i*>(a.out + ((row * a.heads + head) << d_shift) + c) = w;
+  if (a.lse != nullptr && c == 0)
+    a.lse[at] = l == 0.0f ? -INFINITY : (m - kTop + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// How many workgroups share a row's keys: as many as fill the GPU, each with
+// eight tiles or more of an average sequence.
+int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
+  const int64_t groups = (Tq / kRows + B) * heads, room = head_dim == 256 ? 256 : 512;
+  int64_t keys = Tk / B;
+  if (window > 0 && window + kRows < keys) keys = window + kRows;
+  int64_t n = room / groups;
+  if (n > keys / (8 * kKeys)) n = keys / (8 * kKeys);
+  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+size_t prompt_work(int64_t rows, int32_t head_dim, int splits) {
+  return splits == 1 ? 0 : static_cast<size_t>(splits) * rows * (head_dim * 4 + 8);
+}
+
+template <int D>
+void launch(const PromptArgs& a, hipStream_t st) {
+  const int64_t slots = a.s.Tq / kRows + a.s.B;
+  const dim3 grid(static_cast<unsigned>(slots * a.heads), static_cast<unsigned>(a.splits));
+  prompt_kernel<D><<<grid, 64 * kWaves, 0, st>>>(a);
+  if (a.splits > 1) {
+    const int64_t threads = static_cast<int64_t>(a.heads) * a.s.Tq * (D / 8);
+    prompt_join_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a, D == 64 ? 6 : D == 128 ? 7 : 8);
+  }
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" qlin_status qlin_attn_prompt(const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k, int64_t ld_k,
+                                        const uint16_t* v, int64_t ld_v, int32_t kv_heads, int32_t head_dim,
+                                        const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk,
+                                        float scale, int32_t causal, int32_t window, uint16_t* out, float* lse,
+                                        void* work, void* stream) {
+  QLIN_PROMPT_SHAPE(heads, kv_heads, head_dim, B, Tq, Tk, scale, causal, window);
+  QLIN_PROMPT_ROWS("ld_q", Tq, ld_q, heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_k", Tk, ld_k, kv_heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_v", Tk, ld_v, kv_heads, head_dim);
+  if (Tq == 0 || B == 0) return QLIN_OK;
+  QLIN_PTR(q);
+  if (Tk > 0) {
+    QLIN_PTR(k);
+    QLIN_PTR(v);
+  }
+  QLIN_PTR(cu_q);
+  QLIN_PTR(cu_k);
+  QLIN_PTR(out);
+  QLIN_OPT_PTR(lse);
+  QLIN_OPT_PTR(work);
+  PromptArgs a{q,   k,   v, ld_q, ld_k, ld_v, heads, heads / kv_heads, {cu_q, cu_k, B, (int32_t)Tq, (int32_t)Tk}, 0.0f, 0,
+               causal, prompt_window(window), out, lse, 1, nullptr, nullptr};
+  a.splits = prompt_splits(heads, head_dim, B, Tq, Tk, window);
+  if (a.splits > 1) {
+    QLIN_REQUIRE(work != nullptr, QLIN_ERR_INVALID_ARG, "work: null pointer");
+    const int64_t rows = static_cast<int64_t>(heads) * Tq;
+    a.part_o = static_cast<float*>(work);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + a.splits * rows * head_dim);
+  }
+  a.c = prompt_scale(scale);
+  a.flip = scale < 0.0f ? 0x80008000u : 0u;
+  hipStream_t st = as_stream(stream);
+  if (head_dim == 64)
+    launch<64>(a, st);
+  else if (head_dim == 128)
+    launch<128>(a, st);
+  else
+    launch<256>(a, st);
+  QLIN_LAUNCH_CHECK("prompt_kernel");
+  return QLIN_OK;
+}
+
+extern "C" size_t qlin_attn_prompt_work_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq,
+                                              int64_t Tk, int32_t causal, int32_t window) {
+  if (!prompt_shape_ok(heads, kv_heads, head_dim, B, Tq, Tk, causal, window) || B == 0 || Tq == 0) return 0;
+  return prompt_work(static_cast<int64_t>(heads) * Tq, head_dim, prompt_splits(heads, head_dim, B, Tq, Tk, window));
+}

@@ -1,0 +1,430 @@
+// Gradients of attention over whole prompts (qlin_attn_prompt_backward).
+//
+// With p = exp(s - lse), delta_i = dout_i . out_i and dp_ij = dout_i . v_j:
+//   dv_j = sum_i p_ij dout_i,   ds = p (dp - delta),
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
+// p and ds are made again where they are needed, by two kernels, so that every sum
+// stays in one wave's registers and no two of them add to the same place: the
+// same call gives the same bits.  Seven products where five would do with sums
+// across workgroups.
+//   1. dq: a workgroup has 128 queries of one head, a lane one query, and goes over
+//      the keys:  S^T = K Q^T,  dP^T = V dO^T,  dQ^T += K^T dS^T.  It also leaves
+//      delta and lse for the second kernel.
+//   2. dk, dv: a workgroup has 128 keys of one kv head, a lane one key, and goes
+//      over the queries of all its heads:  S = Q K^T,  dP = dO V^T,
+//      dV^T += dO^T P,  dK^T += Q^T dS.
+// As in the forward pass, P and dS leave one product in the registers where the
+// next takes them.
+#include <math.h>
+
+#include "prompt.hpp"
+
+namespace qlin {
+namespace {
+
+struct GradArgs {
+  const uint16_t* dout;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* out;
+  const float* lse;
+  int64_t ld_do, ld_q, ld_k, ld_v;
+  int32_t heads, group;
+  Borders s;
+  float c, scale;  // c = scale log2(e)
+  int32_t causal, window;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  int64_t ld_dq, ld_dk, ld_dv;
+  float* neg_lse;  // [heads x Tq]: kTop - lse log2(e)
+  float* delta;    // [heads x Tq]
+};
+
+constexpr int kStep = 64;  // keys, or queries, of a tile (load64 takes their statistics)
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;
+
+// p is held times 2^kTop, so that fp16 has weights down to 2^-28 to 2^-11 of
+// themselves.
+constexpr float kTop = 14.0f;
+// ds enters its products as fp16 times a power of two that follows the largest
+// |ds| seen: set so that this one is at 2^kAim, and again where one passes 2^15.
+// What is added up so far is brought to the new power then.
+constexpr float kCeil = 32768.0f;
+constexpr int kAim = 11;
+
+// The power of two that brings x > 0 to 2^kAim .. 2^(kAim + 1).
+__device__ __forceinline__ float power_for(float x) {
+  const int e = static_cast<int>(__builtin_bit_cast(uint32_t, x) >> 23);  // at most 255
+  const int p = 254 + kAim - e;
+  return __builtin_bit_cast(float, static_cast<uint32_t>(p < 1 ? 1 : p > 254 ? 254 : p) << 23);
+}
+
+__device__ __forceinline__ v16f zeros() {
+  v16f x;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x[r] = 0.0f;
+  return x;
+}
+template <int N>
+__device__ __forceinline__ void times(v16f (&x)[N], float f) {
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[d][r] *= f;
+}
+__device__ __forceinline__ v8h eight(const v16f& x, int b) {
+  return pack8(x[8 * b], x[8 * b + 1], x[8 * b + 2], x[8 * b + 3], x[8 * b + 4], x[8 * b + 5], x[8 * b + 6], x[8 * b + 7]);
+}
+
+// A lane's row of D values as the second operand of D / 16 steps; zeros if it is
+// not there.
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t* row, bool there, v8h (&f)[D / 16]) {
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    v4i w = *reinterpret_cast<const v4i*>(row + 16 * ks);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = there ? w[j] : 0;
+    f[ks] = __builtin_bit_cast(v8h, w);
+  }
+}
+
+// x (D x 32, a lane one column) times f as a row of D fp16 values per column.
+template <int D>
+__device__ __forceinline__ void store_rows(const v16f (&x)[D / 32], float f, uint16_t* row, int half, bool there) {
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      const uint32_t a0 = pack_half(x[d][4 * g] * f, x[d][4 * g + 1] * f);
+      const uint32_t a1 = pack_half(x[d][4 * g + 2] * f, x[d][4 * g + 3] * f);
+      const uint32_t b0 = pack_half(x[d][4 * g + 4] * f, x[d][4 * g + 5] * f);
+      const uint32_t b1 = pack_half(x[d][4 * g + 6] * f, x[d][4 * g + 7] * f);
+      const auto y = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+      const auto z = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+      const v4i w = {static_cast<int>(y[0]), static_cast<int>(z[0]), static_cast<int>(y[1]), static_cast<int>(z[1])};
+      if (there) *reinterpret_cast<v4i*>(row + 32 * d + 8 * g + 8 * half) = w;
+    }
+}
+
+// 16 rows (from r0 on) of a tile by 32 columns (from 32 d on) as the first operand
+// of a product over the rows, in the order in which a lane holds them.
+template <int D>
+__device__ __forceinline__ v8h transposed(const uint8_t* tile, int r0, int d, int lane) {
+  const int r = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2), e = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  return join_halves(lds_transposed(tile + lds_at<D>(r, e >> 3) + 2 * (e & 7)),
+                     lds_transposed(tile + lds_at<D>(r + 8, e >> 3) + 2 * (e & 7)));
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel(GradArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, kBytes = kStep * D * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  uint32_t head, slot;
+  head_and_slot(blockIdx.x, a.heads, head, slot);
+  slot = gridDim.x / a.heads - 1 - slot;
+  int64_t tile;
+  const int64_t b = find_tile<kRows>(a.s.cu_q, a.s.B, slot, tile);
+  const Seq s = sequence(a.s, b);
+  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
+  if (tile < 0 || tile * kRows >= nq) return;
+  const int row0 = static_cast<int>(tile) * kRows, i0 = row0 + 32 * wave, i = i0 + col;
+  const int kvh = head / a.group;
+  auto top_of = [&](int r) { return a.causal ? clamp_i32(r + shift + 1, 0, nk) : nk; };
+  auto low_of = [&](int r) { return a.window > 0 ? clamp_i32(r + shift + 1 - a.window, 0, nk) : 0; };
+  const int lo = low_of(i), hi = top_of(i);
+  const uint32_t span = hi > lo ? hi - lo : 0;
+  const int hi_first = top_of(i0), hi_last = top_of(i0 + 31), lo_first = low_of(i0), lo_last = low_of(i0 + 31);
+  const int kbeg = low_of(row0), kend = top_of((row0 + kRows < nq ? row0 + kRows : nq) - 1);
+  const int tiles = kend > kbeg ? (kend - kbeg + kStep - 1) / kStep : 0;
+
+  const uint16_t* kb = a.k + s.k0 * a.ld_k + kvh * D;
+  const uint16_t* vb = a.v + s.k0 * a.ld_v + kvh * D;
+  TileLoad<D, kStep, kWaves> kl, vl;
+  kl.init(a.ld_k, wave, lane);
+  vl.init(a.ld_v, wave, lane);
+  auto fetch = [&](int t) {
+    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+    const int64_t at = kbeg + t * kStep;
+    kl.load(kb + at * a.ld_k, a.ld_k, nk - static_cast<int>(at), to, wave);
+    vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
+  };
+  if (tiles > 0) fetch(0);
+
+  const bool there = i < nq;
+  const int64_t token = s.q0 + (there ? i : 0);
+  v8h qf[KS], df[KS];
+  load_row<D>(a.q + token * a.ld_q + head * D + 8 * half, there, qf);
+  load_row<D>(a.dout + token * a.ld_do + head * D + 8 * half, there, df);
+  float delta = 0.0f, neg = 0.0f;
+  {
+    v8h of[KS];
+    load_row<D>(a.out + (token * a.heads + head) * D + 8 * half, there, of);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        delta = __builtin_fmaf(static_cast<float>(df[ks][j]), static_cast<float>(of[ks][j]), delta);
+    delta += __shfl_xor(delta, 32, 64);
+    const int64_t at = static_cast<int64_t>(head) * a.s.Tq + token;
+    const float lse = a.lse[at];
+    // A query without weight: its p are exp2(-inf).
+    neg = lse == -INFINITY || !there ? -INFINITY : __builtin_fmaf(-kLog2e, lse, kTop);
+    if (there && half == 0) {
+      a.neg_lse[at] = neg;
+      a.delta[at] = delta;
+    }
+  }
+
+  v16f dq[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) dq[d] = zeros();
+  float power = 0.0f;  // of ds, the query's own
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();
+    if (t + 1 < tiles) fetch(t + 1);
+    const int k0 = kbeg + t * kStep;
+    if (k0 >= hi_last || k0 + kStep <= lo_first) continue;
+    const bool cut = k0 < lo_last || k0 + kStep > hi_first;
+    const uint8_t* kt = lds + (t & 1) * 2 * kBytes;
+    const uint8_t* vt = kt + kBytes;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      v16f st = zeros(), dp = zeros();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const v8h*>(kt + lds_at<D>(32 * n + col, 2 * ks + half)), qf[ks], st, 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const v8h*>(vt + lds_at<D>(32 * n + col, 2 * ks + half)), df[ks], dp, 0, 0, 0);
+      float top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg));
+        st[r] = p * (dp[r] - delta);
+        if (cut) st[r] = static_cast<uint32_t>(k0 + 32 * n + frag_row(r, lane) - lo) < span ? st[r] : 0.0f;
+        top = fmaxf(top, __builtin_fabsf(st[r]));
+      }
+      if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
+        const float next = now ? power_for(top) : power;
+        times(dq, power == 0.0f ? 1.0f : next / power);
+        power = next;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st[r] *= power;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const v8h ds = eight(st, x);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          dq[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(kt, 32 * n + 16 * x, d, lane), ds, dq[d], 0, 0, 0);
+      }
+    }
+  }
+  const float f = power == 0.0f ? 0.0f : a.scale * 0x1p-14f / power;
+  store_rows<D>(dq, f, a.dq + (s.q0 + static_cast<int64_t>(i)) * a.ld_dq + head * D, half, there);
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kernel(GradArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, kBytes = kStep * D * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
+  __shared__ __attribute__((aligned(1024))) float stats[2][2][kStep];  // -lse and delta of their rows
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int kv_heads = a.heads / a.group;
+  uint32_t kvh, slot;
+  head_and_slot(blockIdx.x, kv_heads, kvh, slot);
+  int64_t tile;
+  const int64_t b = find_tile<kRows>(a.s.cu_k, a.s.B, slot, tile);
+  const Seq s = sequence(a.s, b);
+  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
+  if (tile < 0 || tile * kRows >= nk) return;
+  const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;
+  // Queries [first, last) see a key.
+  auto first_of = [&](int r) { return a.causal ? clamp_i32(r - shift, 0, nq) : 0; };
+  auto last_of = [&](int r) {
+    return a.window > 0 && r - shift < nq - a.window ? clamp_i32(r - shift + a.window, 0, nq) : nq;
+  };
+  const int first = first_of(j), last = last_of(j);
+  const uint32_t span = last > first ? last - first : 0;
+  const int first_lo = first_of(j0), first_hi = first_of(j0 + 31), last_lo = last_of(j0), last_hi = last_of(j0 + 31);
+  const int qbeg = first_of(row0), qend = last_of(row0 + kRows - 1);
+  const int per_head = qend > qbeg ? (qend - qbeg + kStep - 1) / kStep : 0;
+  const int tiles = per_head * a.group;
+
+  const int64_t qw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_q, dw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_do;
+  TileLoad<D, kStep, kWaves> ql, dl;
+  ql.init(a.ld_q, wave, lane);
+  dl.init(a.ld_do, wave, lane);
+  int f_head = kvh * a.group, f_tile = 0;  // the next tile to fetch
+  auto fetch = [&](int t) {
+    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+    const int64_t at = f_tile * kStep;
+    const int rows = nq - qbeg - static_cast<int>(at);
+    ql.load(a.q + qw + at * a.ld_q + f_head * D, a.ld_q, rows, to, wave);
+    dl.load(a.dout + dw + at * a.ld_do + f_head * D, a.ld_do, rows, to + kBytes, wave);
+    if (wave < 2) {
+      const float* src = wave == 0 ? a.neg_lse : a.delta;
+      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows, stats[t & 1][wave], lane);
+    }
+    if (++f_tile == per_head) {
+      f_tile = 0;
+      ++f_head;
+    }
+  };
+  if (tiles > 0) fetch(0);
+
+  const bool there = j < nk;
+  const int64_t token = s.k0 + (there ? j : 0);
+  v8h kf[KS], vf[KS];
+  load_row<D>(a.k + token * a.ld_k + kvh * D + 8 * half, there, kf);
+  load_row<D>(a.v + token * a.ld_v + kvh * D + 8 * half, there, vf);
+  v16f dk[DT], dv[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zeros();
+  float power = 0.0f;  // of ds, the key's own
+
+  int c_tile = 0;
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();
+    if (t + 1 < tiles) fetch(t + 1);
+    const int i0 = qbeg + c_tile * kStep;
+    if (++c_tile == per_head) c_tile = 0;
+    if (i0 >= last_hi || i0 + kStep <= first_lo) continue;
+    const bool cut = i0 < first_hi || i0 + kStep > last_lo;
+    const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
+    const uint8_t* dt = qt + kBytes;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      v16f st = zeros(), dp = zeros();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const v8h*>(qt + lds_at<D>(32 * n + col, 2 * ks + half)), kf[ks], st, 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const v8h*>(dt + lds_at<D>(32 * n + col, 2 * ks + half)), vf[ks], dp, 0, 0, 0);
+      float top = 0.0f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 neg = *reinterpret_cast<const float4*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
+        const float4 del = *reinterpret_cast<const float4*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
+        const float nl[4] = {neg.x, neg.y, neg.z, neg.w}, de[4] = {del.x, del.y, del.z, del.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * g + e;
+          const bool seen = !cut || static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, nl[e]));
+          st[r] = seen ? p : 0.0f;
+          dp[r] = seen ? p * (dp[r] - de[e]) : 0.0f;
+          top = fmaxf(top, __builtin_fabsf(dp[r]));
+        }
+      }
+      if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
+        const float next = now ? power_for(top) : power;
+        times(dk, power == 0.0f ? 1.0f : next / power);
+        power = next;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] *= power;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const v8h p8 = eight(st, x), s8 = eight(dp, x);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          dv[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(dt, 32 * n + 16 * x, d, lane), p8, dv[d], 0, 0, 0);
+          dk[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(qt, 32 * n + 16 * x, d, lane), s8, dk[d], 0, 0, 0);
+        }
+      }
+    }
+  }
+  const float f = power == 0.0f ? 0.0f : a.scale * 0x1p-14f / power;
+  const int64_t row = s.k0 + static_cast<int64_t>(j);
+  store_rows<D>(dk, f, a.dk + row * a.ld_dk + kvh * D, half, there);
+  store_rows<D>(dv, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
+}
+
+template <int D>
+qlin_status launch(const GradArgs& a, hipStream_t st) {
+  if (a.s.Tq > 0) {
+    const int64_t wgs = (a.s.Tq / kRows + a.s.B) * a.heads;
+    prompt_dq_kernel<D><<<static_cast<unsigned>(wgs), 64 * kWaves, 0, st>>>(a);
+    QLIN_LAUNCH_CHECK("prompt_dq_kernel");
+  }
+  if (a.s.Tk > 0) {
+    const int64_t wgs = (a.s.Tk / kRows + a.s.B) * (a.heads / a.group);
+    prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 64 * kWaves, 0, st>>>(a);
+    QLIN_LAUNCH_CHECK("prompt_dkv_kernel");
+  }
+  return QLIN_OK;
+}
+
+size_t grad_work(int32_t heads, int64_t Tq) {  // two arrays, each a multiple of 16 bytes
+  return 2 * ((static_cast<size_t>(heads) * Tq * 4 + 15) / 16 * 16);
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" qlin_status qlin_attn_prompt_backward(
+    const uint16_t* dout, int64_t ld_dout, const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k,
+    int64_t ld_k, const uint16_t* v, int64_t ld_v, int32_t kv_heads, int32_t head_dim, const uint16_t* out,
+    const float* lse, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, float scale,
+    int32_t causal, int32_t window, uint16_t* dq, int64_t ld_dq, uint16_t* dk, int64_t ld_dk, uint16_t* dv,
+    int64_t ld_dv, void* work, void* stream) {
+  QLIN_PROMPT_SHAPE(heads, kv_heads, head_dim, B, Tq, Tk, scale, causal, window);
+  QLIN_PROMPT_ROWS("ld_dout", Tq, ld_dout, heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_q", Tq, ld_q, heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_k", Tk, ld_k, kv_heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_v", Tk, ld_v, kv_heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_dq", Tq, ld_dq, heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_dk", Tk, ld_dk, kv_heads, head_dim);
+  QLIN_PROMPT_ROWS("ld_dv", Tk, ld_dv, kv_heads, head_dim);
+  if (B == 0 || (Tq == 0 && Tk == 0)) return QLIN_OK;
+  if (Tq > 0) {
+    QLIN_PTR(dout);
+    QLIN_PTR(q);
+    QLIN_PTR(out);
+    QLIN_PTR(lse);
+    QLIN_PTR(dq);
+    QLIN_PTR(work);
+  }
+  if (Tk > 0) {
+    QLIN_PTR(k);
+    QLIN_PTR(v);
+    QLIN_PTR(dk);
+    QLIN_PTR(dv);
+  }
+  QLIN_PTR(cu_q);
+  QLIN_PTR(cu_k);
+  GradArgs a{};
+  a.dout = dout, a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
+  a.ld_do = ld_dout, a.ld_q = ld_q, a.ld_k = ld_k, a.ld_v = ld_v;
+  a.heads = heads, a.group = heads / kv_heads;
+  a.s = Borders{cu_q, cu_k, B, static_cast<int32_t>(Tq), static_cast<int32_t>(Tk)};
+  a.c = scale * kLog2e, a.scale = scale, a.causal = causal, a.window = prompt_window(window);
+  a.dq = dq, a.dk = dk, a.dv = dv, a.ld_dq = ld_dq, a.ld_dk = ld_dk, a.ld_dv = ld_dv;
+  a.neg_lse = static_cast<float*>(work);
+  a.delta = a.neg_lse + grad_work(heads, Tq) / 8;
+  hipStream_t st = as_stream(stream);
+  return head_dim == 64 ? launch<64>(a, st) : head_dim == 128 ? launch<128>(a, st) : launch<256>(a, st);
+}
+
+extern "C" size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int64_t Tq) {
+  return heads < 1 || heads > 65535 || Tq < 0 || Tq >= kMaxDim ? 0 : grad_work(heads, Tq);
+}

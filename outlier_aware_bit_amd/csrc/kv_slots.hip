@@ -1,0 +1,331 @@
+// Where a step's tokens go (qlin_kv_slots) and which pages its sequences hold
+// (qlin_kv_pages): prefix sums over the sequences, then one write per token or
+// page.  Both are bound by their chain of waits, launch, lengths, sums, stores;
+// each is one launch.
+#include "kv.hpp"
+
+namespace qlin {
+namespace {
+
+// Exclusive sum over a workgroup's threads, and the total, of two values at a
+// time.  `lds` holds two values per wave; it may be used again after the call.
+template <int WAVES>
+__device__ __forceinline__ void block_scan(int64_t& x, int64_t& y, int64_t& sum_x, int64_t& sum_y, int64_t (*lds)[2]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t x0 = x, y0 = y;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t u = __shfl_up(x, o, 64), v = __shfl_up(y, o, 64);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  if (lane == 63) {
+    lds[wave][0] = x;
+    lds[wave][1] = y;
+  }
+  __syncthreads();
+  x -= x0;
+  y -= y0;
+  sum_x = sum_y = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int64_t u = lds[w][0], v = lds[w][1];
+    if (w < wave) {
+      x += u;
+      y += v;
+    }
+    sum_x += u;
+    sum_y += v;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- slots
+struct SlotArgs {
+  const int32_t* lens;
+  const int32_t* add;
+  const int32_t* first;  // null: lens
+  int64_t B, T;
+  int32_t* cu;
+  int32_t* row;
+  int32_t* slot;
+  int32_t* position;
+  int32_t* lens_out;
+};
+
+constexpr int kSlotThreads = 256;
+constexpr int kSlotWaves = kSlotThreads / 64;
+constexpr int kSlotTokens = 4 * kSlotThreads;  // of a workgroup
+
+__device__ __forceinline__ int32_t at_least_zero(int32_t v) { return v < 0 ? 0 : v; }
+
+// Every workgroup sums the lengths itself (each thread a run of sequences), marks
+// in LDS where sequences begin among its tokens, and a running maximum over the
+// marks gives each token its sequence.
+__global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
+  __shared__ int64_t sums[kSlotWaves][2];
+  __shared__ int32_t mark[kSlotTokens];   // the sequence that begins here, or -1
+  __shared__ int32_t begin[kSlotTokens];  // its first token, from this workgroup's first
+  __shared__ int32_t last[kSlotWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSlotTokens;
+  const int64_t each = (a.B + kSlotThreads - 1) / kSlotThreads;
+  const int64_t b0 = tid * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mark[tid + i * kSlotThreads] = -1;
+  int64_t at = 0, none = 0, total, unused;
+  for (int64_t b = b0; b < b1; ++b) at += at_least_zero(a.add[b]);
+  block_scan<kSlotWaves>(at, none, total, unused, sums);  // the marks are cleared behind its barriers
+  for (int64_t b = b0; b < b1; ++b) {
+    const int64_t end = at + at_least_zero(a.add[b]);
+    if (end > at && at < t0 + kSlotTokens && end > t0) {
+      const int i = at > t0 ? static_cast<int>(at - t0) : 0;
+      mark[i] = static_cast<int32_t>(b);
+      begin[i] = static_cast<int32_t>(at - t0);  // at <= t0 + kSlotTokens, t0 < 2^31 + kSlotTokens
+    }
+    if (blockIdx.x == 0) {
+      const int64_t lo = at < a.T ? at : a.T, hi = end < a.T ? end : a.T;
+      a.cu[b] = static_cast<int32_t>(lo);
+      a.lens_out[b] = static_cast<int32_t>(static_cast<uint32_t>(at_least_zero(a.lens[b])) +
+                                           static_cast<uint32_t>(hi - lo));
+    }
+    at = end;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.cu[a.B] = static_cast<int32_t>(total < a.T ? total : a.T);
+  __syncthreads();
+  // The nearest mark at or before each of the thread's four tokens.
+  int near[4], m = -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (mark[4 * tid + i] >= 0) m = 4 * tid + i;
+    near[i] = m;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(m, o, 64);
+    if (lane >= o && u > m) m = u;
+  }
+  if (lane == 63) last[wave] = m;
+  int before = __shfl_up(m, 1, 64);
+  if (lane == 0) before = -1;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) before = last[w] > before ? last[w] : before;
+  int32_t row[4], slot[4], pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = near[i] >= 0 ? near[i] : before;
+    row[i] = slot[i] = pos[i] = -1;
+    if (j >= 0 && t0 + 4 * tid + i < total) {
+      const int32_t b = mark[j];
+      const uint32_t off = static_cast<uint32_t>(4 * tid + i) - static_cast<uint32_t>(begin[j]);
+      const uint32_t held = static_cast<uint32_t>(at_least_zero(a.lens[b]));
+      row[i] = b;
+      slot[i] = static_cast<int32_t>(held + off);
+      pos[i] = static_cast<int32_t>((a.first != nullptr ? static_cast<uint32_t>(a.first[b]) : held) + off);
+    }
+  }
+  const int64_t t = t0 + 4 * tid;
+  if (t + 4 <= a.T) {
+    *reinterpret_cast<v4i*>(a.row + t) = v4i{row[0], row[1], row[2], row[3]};
+    *reinterpret_cast<v4i*>(a.slot + t) = v4i{slot[0], slot[1], slot[2], slot[3]};
+    *reinterpret_cast<v4i*>(a.position + t) = v4i{pos[0], pos[1], pos[2], pos[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t + i < a.T) {
+        a.row[t + i] = row[i];
+        a.slot[t + i] = slot[i];
+        a.position[t + i] = pos[i];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- pages
+struct PageArgs {
+  const int32_t* want;
+  int64_t B, max_pages;
+  int32_t page_shift;
+  const int32_t* table;
+  const int32_t* held;
+  int32_t* ring;
+  int64_t pages;  // of the ring
+  const int32_t* state;
+  int32_t* table_out;
+  int32_t* held_out;
+  int32_t* state_out;
+  int32_t* missing;
+};
+
+constexpr int kPageThreads = 1024;
+constexpr int kPageWaves = kPageThreads / 64;
+
+// A workgroup goes over the sequences 1024 at a time, one per thread, and leaves
+// in LDS how many pages each holds and will hold and where its changes begin in
+// the ring.  Then the changed entries are moved, each found by a search among
+// the sequences' sums, and, where the table is written elsewhere, the others are
+// copied.  Several workgroups take every so many entries each; each makes the
+// sums for itself.
+__global__ __launch_bounds__(kPageThreads) void kv_pages_kernel(PageArgs a) {
+  __shared__ int64_t sums[kPageWaves][2];
+  __shared__ int32_t held_of[kPageThreads], left_of[kPageThreads];
+  __shared__ int64_t grow_at[kPageThreads], give_at[kPageThreads];
+  __shared__ int64_t move_at[kPageThreads];
+  const int tid = threadIdx.x;
+  const int64_t head = static_cast<uint32_t>(a.state[0]) % static_cast<uint32_t>(a.pages);
+  int64_t count = at_least_zero(a.state[1]);
+  if (count > a.pages) count = a.pages;
+  int64_t asked = 0, given = 0, taken = 0, missing = 0;  // over the sequences so far
+  for (int64_t base = 0; base < a.B; base += kPageThreads) {
+    const int64_t b = base + tid;
+    int32_t held = 0, left = 0;
+    int64_t need = 0, grow = 0;
+    bool fits = true;
+    if (b < a.B) {
+      held = at_least_zero(a.held[b]);
+      if (held > a.max_pages) held = static_cast<int32_t>(a.max_pages);
+      need = (static_cast<int64_t>(at_least_zero(a.want[b])) + (1 << a.page_shift) - 1) >> a.page_shift;
+      fits = need <= a.max_pages;
+      grow = fits && need > held ? need - held : 0;
+    }
+    int64_t ahead = grow, none = 0, all, unused;
+    block_scan<kPageWaves>(ahead, none, all, unused, sums);
+    const bool served = fits && (grow == 0 || asked + ahead + grow <= count);
+    left = served ? static_cast<int32_t>(need) : held;
+    int64_t back = held > left ? held - left : 0, lacks = served ? 0 : need - held, all_back, all_lacks;
+    const int64_t given_here = back;
+    block_scan<kPageWaves>(back, lacks, all_back, all_lacks, sums);
+    int64_t moved = served ? grow + given_here : 0, got = served ? grow : 0, all_moved, all_got;
+    block_scan<kPageWaves>(moved, got, all_moved, all_got, sums);
+    held_of[tid] = held;
+    left_of[tid] = left;
+    grow_at[tid] = taken + got;
+    give_at[tid] = given + back;
+    move_at[tid] = moved;
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kPageThreads;
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * kPageThreads + tid;
+    for (int64_t i = mine; i < all_moved; i += stride) {
+      int r = 0;  // the last sequence whose changes begin at or before i
+#pragma unroll
+      for (int o = kPageThreads / 2; o > 0; o >>= 1)
+        if (move_at[r + o] <= i) r += o;
+      const int64_t n = i - move_at[r];
+      const int32_t h = held_of[r], l = left_of[r];
+      const int64_t row = (base + r) * a.max_pages;
+      if (l > h) {
+        a.table_out[row + h + n] = a.ring[(head + grow_at[r] + n) % a.pages];
+      } else {
+        a.ring[(head + count + give_at[r] + n) % a.pages] = a.table[row + l + n];
+        a.table_out[row + l + n] = -1;
+      }
+    }
+    if (a.table_out != a.table) {
+      const int64_t rows = a.B - base < kPageThreads ? a.B - base : kPageThreads;
+      const int64_t entries = rows * a.max_pages, from = base * a.max_pages;
+      for (int64_t f = mine; f < entries; f += 4 * stride) {
+        int32_t id[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) id[j] = f + j * stride < entries ? a.table[from + f + j * stride] : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t g = f + j * stride;
+          if (g < entries) {
+            const int r = static_cast<int>(g >> 31 ? g / a.max_pages
+                                                   : static_cast<uint32_t>(g) / static_cast<uint32_t>(a.max_pages));
+            const int64_t e = g - r * a.max_pages;
+            const int32_t h = held_of[r], l = left_of[r];
+            if (e < (h < l ? h : l) || e >= (h < l ? l : h)) a.table_out[from + g] = id[j];
+          }
+        }
+      }
+    }
+    if (blockIdx.x == 0 && b < a.B) a.held_out[b] = left;
+    asked += all;
+    taken += all_got;
+    given += all_back;
+    missing += all_lacks;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    int64_t now = count - taken + given;
+    if (now > a.pages) now = a.pages;
+    a.state_out[0] = static_cast<int32_t>((head + taken) % a.pages);
+    a.state_out[1] = static_cast<int32_t>(now);
+    a.missing[0] = static_cast<int32_t>(missing < 0x7fffffff ? missing : 0x7fffffff);
+  }
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" qlin_status qlin_kv_slots(const int32_t* lens, const int32_t* add, const int32_t* first, int64_t B,
+                                     int64_t T, int32_t* cu, int32_t* row, int32_t* slot, int32_t* position,
+                                     int32_t* lens_out, void* stream) {
+  QLIN_REQUIRE(B >= 0, QLIN_ERR_INVALID_ARG, "B=%lld is negative", (long long)B);
+  QLIN_REQUIRE(T >= 0, QLIN_ERR_INVALID_ARG, "T=%lld is negative", (long long)T);
+  QLIN_REQUIRE(B <= 65535, QLIN_ERR_SHAPE, "B=%lld: at most 65535", (long long)B);
+  QLIN_REQUIRE(T < kMaxDim, QLIN_ERR_SHAPE, "T=%lld: fewer than 2^31", (long long)T);
+  if (B > 0) {
+    QLIN_PTR(lens);
+    QLIN_PTR(add);
+    QLIN_PTR(lens_out);
+    QLIN_REQUIRE(lens_out != lens && lens_out != add && lens_out != first, QLIN_ERR_INVALID_ARG,
+                 "lens_out must not be lens, add or first: they are read while it is written");
+  }
+  QLIN_OPT_PTR(first);
+  QLIN_PTR(cu);
+  if (T > 0) {
+    QLIN_PTR(row);
+    QLIN_PTR(slot);
+    QLIN_PTR(position);
+  }
+  const SlotArgs a{lens, add, first, B, T, cu, row, slot, position, lens_out};
+  const int64_t blocks = T > 0 ? (T + kSlotTokens - 1) / kSlotTokens : 1;
+  kv_slots_kernel<<<static_cast<unsigned>(blocks), kSlotThreads, 0, as_stream(stream)>>>(a);
+  QLIN_LAUNCH_CHECK("kv_slots_kernel");
+  return QLIN_OK;
+}
+
+extern "C" qlin_status qlin_kv_pages(const int32_t* want, int64_t B, int64_t max_pages, int32_t page,
+                                     const int32_t* table, const int32_t* held, int32_t* ring, int64_t pages,
+                                     const int32_t* state, int32_t* table_out, int32_t* held_out, int32_t* state_out,
+                                     int32_t* missing, void* stream) {
+  QLIN_REQUIRE(page >= 16 && page <= 1024 && (page & (page - 1)) == 0, QLIN_ERR_UNSUPPORTED,
+               "page=%d: a power of two from 16 to 1024", page);
+  QLIN_REQUIRE(B >= 0, QLIN_ERR_INVALID_ARG, "B=%lld is negative", (long long)B);
+  QLIN_REQUIRE(B <= 65535, QLIN_ERR_SHAPE, "B=%lld: at most 65535", (long long)B);
+  QLIN_REQUIRE(max_pages >= 1 && max_pages <= (kMaxDim - 1) / page, QLIN_ERR_SHAPE,
+               "max_pages=%lld: at least 1, and fewer than 2^31 slots", (long long)max_pages);
+  QLIN_REQUIRE(pages >= 1 && pages < kMaxDim, QLIN_ERR_SHAPE, "pages=%lld: from 1 to 2^31 - 1", (long long)pages);
+  QLIN_DIMS(B, max_pages);
+  if (B > 0) {
+    QLIN_PTR(want);
+    QLIN_PTR(table);
+    QLIN_PTR(held);
+    QLIN_PTR(table_out);
+    QLIN_PTR(held_out);
+    QLIN_REQUIRE(held_out != want, QLIN_ERR_INVALID_ARG, "held_out must not be want");
+  }
+  QLIN_PTR(ring);
+  QLIN_PTR(state);
+  QLIN_PTR(state_out);
+  QLIN_PTR(missing);
+  const PageArgs a{want,  B,    max_pages, kv_page_shift(page), table,     held,    ring,
+                   pages, state, table_out, held_out,            state_out, missing};
+  // Several workgroups where a table is written anew.  They read what others of
+  // them write if held or state is updated in place: then, and where only changed
+  // entries are written, one.
+  int64_t blocks = 1;
+  if (table_out != table && held_out != held && state_out != state) {
+    blocks = (B * max_pages) / (4 * kPageThreads);
+    blocks = blocks < 1 ? 1 : blocks > 64 ? 64 : blocks;
+  }
+  kv_pages_kernel<<<static_cast<unsigned>(blocks), kPageThreads, 0, as_stream(stream)>>>(a);
+  QLIN_LAUNCH_CHECK("kv_pages_kernel");
+  return QLIN_OK;
+}

@@ -1,0 +1,226 @@
+// Rotary positions (qlin_rope, qlin_rope_freqs): pair i of a token at position p
+// is turned by the angle p * freq[i].
+//
+// The angle is reduced in 64 bits: turns = p * (freq / 2 pi), less the nearest
+// quarter, leaves at most an eighth of a turn, good to 2^-22 of a turn at p =
+// 2^31 and better than fp32 up to p = 2^29.  Sine and cosine of what is left are
+// their Taylor polynomials of degree 9 and 8: within pi / 4 the first term left
+// out is below 2^-25.  The products are fp32 and rounded to fp16 once.
+//
+// Bound by memory, each row read and written once.  A thread keeps the sines and
+// cosines of eight pairs and goes over heads with them.
+#include <math.h>
+
+#include "common.hpp"
+
+namespace qlin {
+namespace {
+
+struct RopeArgs {
+  const uint16_t* x[2];  // q and k
+  uint16_t* y[2];
+  int64_t ld_x[2], ld_y[2];  // elements between two tokens
+  int32_t heads, all;        // query heads; query and key heads
+  int64_t T;
+  int32_t chunk_shift;  // 16-channel units of a head: 4, 8 or 16
+  int32_t turned;       // of these, the first that are turned
+  int32_t split_shift;  // threads that share a unit's heads: a power of two
+  const int32_t* position;
+  const double* freq;
+  float amplitude;
+  float sign;  // -1: backwards
+};
+
+constexpr int kRopeThreads = 256;
+
+// sin and cos of p * freq.
+__device__ __forceinline__ void unit_of(double p, double freq, float& s, float& c) {
+  const double turns = p * (freq * 0.15915494309189533577);  // 1 / (2 pi)
+  const double t = turns - rint(turns);
+  const double quarter = rint(4.0 * t);  // -2 .. 2
+  const float a = static_cast<float>((t - 0.25 * quarter) * 6.28318530717958647693);
+  const float z = a * a;
+  float u = __builtin_fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  u = __builtin_fmaf(z, u, 1.0f / 120.0f);
+  u = __builtin_fmaf(z, u, -1.0f / 6.0f);
+  u = __builtin_fmaf(a * z, u, a);
+  float v = __builtin_fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
+  v = __builtin_fmaf(z, v, 1.0f / 24.0f);
+  v = __builtin_fmaf(z, v, -0.5f);
+  v = __builtin_fmaf(z, v, 1.0f);
+  const int k = static_cast<int>(quarter) & 3;
+  s = (k & 1) ? v : u;
+  c = (k & 1) ? u : v;
+  s = (k & 2) ? -s : s;
+  c = (k == 1 || k == 2) ? -c : c;
+}
+
+__device__ __forceinline__ void to_float(const v4i w, float (&f)[8]) {
+  const v8h h = __builtin_bit_cast(v8h, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(h[i]);
+}
+__device__ __forceinline__ v4i to_half(const float (&f)[8]) {
+  v8h h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(f[i]);
+  return __builtin_bit_cast(v4i, h);
+}
+
+// Pairs (i, i + rot / 2), or (2 i, 2 i + 1) when PAIRED.
+template <bool PAIRED>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
+  const int splits = 1 << a.split_shift;
+  const int64_t units = a.T << (a.split_shift + a.chunk_shift), step = static_cast<int64_t>(gridDim.x) * kRopeThreads;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; u < units; u += step) {
+    const int c = static_cast<int>(u) & ((1 << a.chunk_shift) - 1);
+    const int h0 = static_cast<int>(u >> a.chunk_shift) & (splits - 1);
+    const int64_t t = u >> (a.split_shift + a.chunk_shift);
+    const int32_t p = a.position[t];
+    if (p < 0) continue;
+    // The unit's channels: two runs of eight.
+    const bool turn = c < a.turned;
+    const int e0 = (PAIRED || !turn) ? 16 * c : 8 * c, e1 = (PAIRED || !turn) ? e0 + 8 : e0 + 8 * a.turned;
+    float sn[8], cs[8];
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        unit_of(static_cast<double>(p), a.freq[8 * c + i], sn[i], cs[i]);
+        sn[i] *= a.amplitude * a.sign;
+        cs[i] *= a.amplitude;
+      }
+    }
+    for (int h = h0; h < a.all; h += splits) {
+      const int which = h < a.heads ? 0 : 1;
+      const int64_t at = static_cast<int64_t>(h - (which ? a.heads : 0)) << (4 + a.chunk_shift);
+      const uint16_t* x = a.x[which] + t * a.ld_x[which] + at;
+      uint16_t* y = a.y[which] + t * a.ld_y[which] + at;
+      if (!turn && x == y) continue;
+      v4i w0 = *reinterpret_cast<const v4i*>(x + e0), w1 = *reinterpret_cast<const v4i*>(x + e1);
+      if (turn) {
+        float f0[8], f1[8], g0[8], g1[8];
+        to_float(w0, f0);
+        to_float(w1, f1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // PAIRED: pair i of eight is channels 2 i and 2 i + 1 of the sixteen.
+          const float x0 = PAIRED ? (i < 4 ? f0[2 * (i & 3)] : f1[2 * (i & 3)]) : f0[i];
+          const float x1 = PAIRED ? (i < 4 ? f0[2 * (i & 3) + 1] : f1[2 * (i & 3) + 1]) : f1[i];
+          const float r0 = __builtin_fmaf(x0, cs[i], -(x1 * sn[i])), r1 = __builtin_fmaf(x0, sn[i], x1 * cs[i]);
+          if (PAIRED) {
+            (i < 4 ? g0 : g1)[2 * (i & 3)] = r0;
+            (i < 4 ? g0 : g1)[2 * (i & 3) + 1] = r1;
+          } else {
+            g0[i] = r0;
+            g1[i] = r1;
+          }
+        }
+        w0 = to_half(g0);
+        w1 = to_half(g1);
+      }
+      *reinterpret_cast<v4i*>(y + e0) = w0;
+      *reinterpret_cast<v4i*>(y + e1) = w1;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" qlin_status qlin_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                       int64_t original_len, double fast, double slow, double* freq,
+                                       float* amplitude) {
+  QLIN_REQUIRE(rot_dim >= 16 && rot_dim <= 256 && rot_dim % 16 == 0, QLIN_ERR_UNSUPPORTED,
+               "rot_dim=%d: a multiple of 16 from 16 to 256", rot_dim);
+  QLIN_REQUIRE(scaling >= QLIN_ROPE_PLAIN && scaling <= QLIN_ROPE_RAMP, QLIN_ERR_INVALID_ARG, "scaling=%d", scaling);
+  QLIN_REQUIRE(base > 1.0 && base < INFINITY, QLIN_ERR_INVALID_ARG, "base=%g must be above 1", base);
+  QLIN_REQUIRE(freq != nullptr, QLIN_ERR_INVALID_ARG, "freq: null pointer");
+  QLIN_REQUIRE(amplitude != nullptr, QLIN_ERR_INVALID_ARG, "amplitude: null pointer");
+  if (scaling != QLIN_ROPE_PLAIN)
+    QLIN_REQUIRE(factor >= 1.0 && factor < INFINITY, QLIN_ERR_INVALID_ARG, "factor=%g must be at least 1", factor);
+  const double two_pi = 6.28318530717958647693;
+  if (scaling == QLIN_ROPE_RAMP) {
+    QLIN_REQUIRE(original_len >= 1 && original_len < kMaxDim, QLIN_ERR_INVALID_ARG, "original_len=%lld",
+                 (long long)original_len);
+    QLIN_REQUIRE(slow > 0.0 && fast > slow && fast < INFINITY, QLIN_ERR_INVALID_ARG, "fast=%g, slow=%g: 0 < slow < fast",
+                 fast, slow);
+  }
+  if (scaling == QLIN_ROPE_BASE) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  double lo = 0.0, width = 1.0;
+  if (scaling == QLIN_ROPE_RAMP) {
+    // The pair that turns `turns` times within original_len positions.
+    lo = floor(rot_dim * log(original_len / (two_pi * fast)) / (2.0 * log(base)));
+    double hi = ceil(rot_dim * log(original_len / (two_pi * slow)) / (2.0 * log(base)));
+    if (lo < 0.0) lo = 0.0;
+    if (hi > rot_dim - 1.0) hi = rot_dim - 1.0;
+    width = hi - lo > 0.001 ? hi - lo : 0.001;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == QLIN_ROPE_LINEAR) f /= factor;
+    if (scaling == QLIN_ROPE_RAMP) {
+      double part = (i - lo) / width;
+      part = part < 0.0 ? 0.0 : part > 1.0 ? 1.0 : part;
+      f = f * (1.0 - part) + f / factor * part;
+    }
+    freq[i] = f;
+  }
+  *amplitude = scaling == QLIN_ROPE_RAMP ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return QLIN_OK;
+}
+
+extern "C" qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k, int64_t ld_k,
+                                 int32_t kv_heads, int64_t T, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                 const int32_t* position, const double* freq, float amplitude, int32_t inverse,
+                                 uint16_t* q_out, int64_t ld_qo, uint16_t* k_out, int64_t ld_ko, void* stream) {
+  QLIN_REQUIRE(head_dim == 64 || head_dim == 128 || head_dim == 256, QLIN_ERR_UNSUPPORTED,
+               "head_dim=%d: 64, 128 and 256 are provided", head_dim);
+  QLIN_REQUIRE(rot_dim >= 16 && rot_dim <= head_dim && rot_dim % 16 == 0, QLIN_ERR_UNSUPPORTED,
+               "rot_dim=%d: a multiple of 16 from 16 to head_dim", rot_dim);
+  QLIN_REQUIRE(heads >= 1 && heads <= 65535, QLIN_ERR_SHAPE, "heads=%d must be in [1, 65535]", heads);
+  QLIN_REQUIRE(kv_heads >= 0 && kv_heads <= 65535, QLIN_ERR_SHAPE, "kv_heads=%d must be in [0, 65535]", kv_heads);
+  QLIN_REQUIRE(T >= 0, QLIN_ERR_INVALID_ARG, "T=%lld is negative", (long long)T);
+  QLIN_REQUIRE(amplitude == amplitude, QLIN_ERR_INVALID_ARG, "amplitude is not a number");
+  QLIN_REQUIRE((k != nullptr) == (kv_heads > 0) && (k_out != nullptr) == (kv_heads > 0), QLIN_ERR_INVALID_ARG,
+               "k and k_out come with kv_heads, or are NULL with kv_heads == 0");
+  const int64_t qw = static_cast<int64_t>(heads) * head_dim, kw = static_cast<int64_t>(kv_heads) * head_dim;
+  QLIN_REQUIRE(ld_q >= qw && ld_q % 8 == 0 && ld_qo >= qw && ld_qo % 8 == 0, QLIN_ERR_SHAPE,
+               "ld_q=%lld, ld_qo=%lld: multiples of 8, at least heads * head_dim", (long long)ld_q, (long long)ld_qo);
+  QLIN_DIMS(T, ld_q);
+  QLIN_DIMS(T, ld_qo);
+  if (kv_heads > 0) {
+    QLIN_REQUIRE(ld_k >= kw && ld_k % 8 == 0 && ld_ko >= kw && ld_ko % 8 == 0, QLIN_ERR_SHAPE,
+                 "ld_k=%lld, ld_ko=%lld: multiples of 8, at least kv_heads * head_dim", (long long)ld_k,
+                 (long long)ld_ko);
+    QLIN_DIMS(T, ld_k);
+    QLIN_DIMS(T, ld_ko);
+  }
+  QLIN_REQUIRE(q != q_out || q == nullptr || ld_q == ld_qo, QLIN_ERR_SHAPE, "q in place: ld_qo must be ld_q");
+  QLIN_REQUIRE(k != k_out || k == nullptr || ld_k == ld_ko, QLIN_ERR_SHAPE, "k in place: ld_ko must be ld_k");
+  if (T == 0) return QLIN_OK;
+  QLIN_PTR(q);
+  QLIN_OPT_PTR(k);
+  QLIN_PTR(position);
+  QLIN_PTR(freq);
+  QLIN_PTR(q_out);
+  QLIN_OPT_PTR(k_out);
+  const int chunk_shift = head_dim == 64 ? 2 : head_dim == 128 ? 3 : 4, all = heads + kv_heads;
+  // A thread per unit and head where tokens are few; eight threads share a unit's
+  // heads where they are many.
+  int split_shift = 0;
+  while ((1 << split_shift) < all) ++split_shift;
+  while (split_shift > 3 && T << (chunk_shift + split_shift - 1) >= 256 * 2048) --split_shift;
+  const RopeArgs a{{q, k},      {q_out, k_out},  {ld_q, ld_k},  {ld_qo, ld_ko}, heads,
+                   all,         T,               chunk_shift,   rot_dim / 16,   split_shift,
+                   position,    freq,            amplitude,     inverse ? -1.0f : 1.0f};
+  const int64_t blocks = ((T << (chunk_shift + split_shift)) + kRopeThreads - 1) / kRopeThreads;
+  const unsigned grid = static_cast<unsigned>(blocks < (1 << 24) ? blocks : (1 << 24));
+  if (interleaved)
+    rope_kernel<true><<<grid, kRopeThreads, 0, as_stream(stream)>>>(a);
+  else
+    rope_kernel<false><<<grid, kRopeThreads, 0, as_stream(stream)>>>(a);
+  QLIN_LAUNCH_CHECK("rope_kernel");
+  return QLIN_OK;
+}

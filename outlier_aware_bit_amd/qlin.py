@@ -712,3 +712,261 @@ def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_o
     if st:
         _lib.check("qlin_kv_evict", st)
     return lens_out, kept, mass_out, pos_out
+
+
+# ---------------------------------------------------------------- around the decoding step
+def _gpu_of(t, name):
+    """The index of t's GPU, which has to be the current one: that is where a launch goes."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    index = t.get_device()
+    if _current_device() != index:
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
+    return index
+
+
+def _same(t, name, dtype, shape, index):
+    if not (t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        _req(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    return t.data_ptr()
+
+
+def _given(t, name, dtype, shape, index, like):
+    """The tensor that was passed, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _same(t, name, dtype, shape, index)
+    return t
+
+
+def qlin_kv_slots(lens, add, T, first=None, cu=None, row=None, slot=None, position=None, lens_out=None):
+    """Where a step's tokens go: add int32 [B] new tokens for sequences of lens
+    int32 [B] slots, their next positions first int32 [B] (None: lens).  T: the
+    tokens that the arrays have room for.  Returns (cu [B + 1], row, slot,
+    position [T], lens_out [B]), int32; row, slot and position are -1 behind the
+    last token, and cu is what qlin_attn_prompt takes."""
+    lib, index = _lib.load(), _gpu_of(lens, "lens")
+    if lens.dim() != 1:
+        raise ValueError(f"lens: expected [B], got {tuple(lens.shape)}")
+    B, i32 = lens.shape[0], torch.int32
+    lens_p, add_p = _same(lens, "lens", i32, (B,), index), _same(add, "add", i32, (B,), index)
+    first_p = None if first is None else _same(first, "first", i32, (B,), index)
+    if T < 0:
+        raise ValueError(f"T={T} is negative")
+    cu = _given(cu, "cu", i32, (B + 1,), index, lens)
+    row, slot, position = (_given(t, n, i32, (T,), index, lens)
+                           for t, n in ((row, "row"), (slot, "slot"), (position, "position")))
+    lens_out = _given(lens_out, "lens_out", i32, (B,), index, lens)
+    st = lib.qlin_kv_slots(lens_p or None, add_p or None, first_p or None, B, T, cu.data_ptr(), row.data_ptr() or None,
+                           slot.data_ptr() or None, position.data_ptr() or None, lens_out.data_ptr() or None,
+                           torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check("qlin_kv_slots", st)
+    return cu, row, slot, position, lens_out
+
+
+def qlin_kv_pages(want, page, table, held, ring, state, table_out=None, held_out=None, state_out=None, missing=None):
+    """Brings each row of table int32 [B, max_pages] to the pages that want int32
+    [B] slots need, held int32 [B] of them in use before.  Free pages: count ids
+    of ring int32 [pages] from head on, state int32 [2] = (head, count).  Table,
+    held and state are updated in place unless others are given; the ring always
+    is.  Returns (table_out, held_out, state_out, missing int32 [1]): missing
+    counts the pages that rows lack, which keep what they hold."""
+    lib, index = _lib.load(), _gpu_of(want, "want")
+    i32 = torch.int32
+    if table.dim() != 2 or want.dim() != 1 or ring.dim() != 1:
+        raise ValueError("expected want [B], table [B, max_pages] and ring [pages]")
+    B, most = table.shape
+    want_p = _same(want, "want", i32, (B,), index)
+    table_p, held_p = _same(table, "table", i32, (B, most), index), _same(held, "held", i32, (B,), index)
+    ring_p, state_p = _same(ring, "ring", i32, ring.shape, index), _same(state, "state", i32, (2,), index)
+    table_out, held_out, state_out = (old if new is None else new for old, new in
+                                      ((table, table_out), (held, held_out), (state, state_out)))
+    _same(table_out, "table_out", i32, (B, most), index)
+    _same(held_out, "held_out", i32, (B,), index)
+    _same(state_out, "state_out", i32, (2,), index)
+    missing = _given(missing, "missing", i32, (1,), index, want)
+    st = lib.qlin_kv_pages(want_p or None, B, most, page, table_p or None, held_p or None, ring_p, ring.shape[0],
+                           state_p, table_out.data_ptr() or None, held_out.data_ptr() or None, state_out.data_ptr(),
+                           missing.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check("qlin_kv_pages", st)
+    return table_out, held_out, state_out, missing
+
+
+_ROPE_SCALINGS = {"plain": _lib.QLIN_ROPE_PLAIN, "linear": _lib.QLIN_ROPE_LINEAR, "base": _lib.QLIN_ROPE_BASE,
+                  "ramp": _lib.QLIN_ROPE_RAMP}
+
+
+def qlin_rope_freqs(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0, fast=32.0, slow=1.0,
+                    device="cuda"):
+    """Frequencies of rotary positions: (freq float64 [rot_dim / 2] on device,
+    amplitude).  scaling: "plain", "linear", "base" or "ramp" (qlin.h says what
+    each does with factor, and "ramp" with original_len, fast and slow)."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling={scaling!r}: one of {', '.join(_ROPE_SCALINGS)}")
+    freq, amplitude = (ctypes.c_double * 128)(), ctypes.c_float()
+    _lib.check("qlin_rope_freqs", _lib.load().qlin_rope_freqs(
+        rot_dim, base, _ROPE_SCALINGS[scaling], factor, original_len, fast, slow, ctypes.addressof(freq),
+        ctypes.addressof(amplitude)))
+    return torch.tensor(freq[:rot_dim // 2], dtype=torch.float64, device=device), amplitude.value
+
+
+def _heads3(t, name, head_dim, index):
+    """fp16 [n, heads, head_dim], tokens any multiple of 8 elements apart: (n, heads, elements apart)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [T, heads, head_dim], got {tuple(t.shape)}")
+    heads = t.shape[1]
+    n, ld = _rows3(t, name, heads, head_dim, index)
+    return n, heads, ld
+
+
+def qlin_rope(q, k, position, freq, interleaved=False, inverse=False, amplitude=1.0, q_out=None, k_out=None):
+    """Turns the first 2 * len(freq) channels of each row of q fp16 [T, heads,
+    head_dim] and k fp16 [T, kv_heads, head_dim] (or None) by its position int32
+    [T] (negative: left as it was) times freq float64: channels (i, i + len(freq)),
+    or (2 i, 2 i + 1) if interleaved; backwards if inverse (the backward pass).
+    Tokens may lie any multiple of 8 elements apart.  q_out and k_out may be q and
+    k; by default new tensors are made, whose rows at negative positions are
+    whatever they were.  Returns (q_out, k_out)."""
+    lib, index = _lib.load(), _gpu_of(q, "q")
+    D = q.shape[-1]
+    T, heads, ld_q = _heads3(q, "q", D, index)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out: expected shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    ld_qo = _heads3(q_out, "q_out", D, index)[2]
+    kv_heads, ld_k, ld_ko, k_p, ko_p = 0, 0, 0, None, None
+    if k is not None:
+        Tk, kv_heads, ld_k = _heads3(k, "k", D, index)
+        if Tk != T:
+            raise ValueError(f"q holds {T} tokens, k {Tk}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.float16, device=k.device)
+        elif k_out.shape != k.shape:
+            raise ValueError(f"k_out: expected shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
+        ld_ko = _heads3(k_out, "k_out", D, index)[2]
+        k_p, ko_p = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    position_p = _same(position, "position", torch.int32, (T,), index)
+    if freq.dim() != 1:
+        raise ValueError(f"freq: expected [rot_dim / 2], got {tuple(freq.shape)}")
+    freq_p = _same(freq, "freq", torch.float64, freq.shape, index)
+    if T == 0:
+        return q_out, k_out
+    st = lib.qlin_rope(q.data_ptr(), ld_q, heads, k_p, ld_k, kv_heads, T, D, 2 * freq.shape[0], int(interleaved),
+                       position_p, freq_p, amplitude, int(inverse), q_out.data_ptr(), ld_qo, ko_p, ld_ko,
+                       torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check("qlin_rope", st)
+    return q_out, k_out
+
+
+def _space(work, need, index, like):
+    if not need:
+        return None
+    if work is None:
+        return torch.empty((need,), dtype=torch.uint8, device=like.device)
+    _same(work, "work", torch.uint8, work.shape, index)
+    if work.numel() < need:
+        raise ValueError(f"work: {work.numel()} bytes, needs {need}")
+    return work
+
+
+def _borders(cu_q, cu_k, index):
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError(f"cu_q: expected [B + 1], got {tuple(cu_q.shape)}")
+    B = cu_q.shape[0] - 1
+    cu_q_p = _same(cu_q, "cu_q", torch.int32, cu_q.shape, index)
+    return B, cu_q_p, cu_q_p if cu_k is None else _same(cu_k, "cu_k", torch.int32, (B + 1,), index)
+
+
+def _prompt_rows(q, k, v, index):
+    D = q.shape[-1]
+    Tq, heads, ld_q = _heads3(q, "q", D, index)
+    Tk, kv_heads, ld_k = _heads3(k, "k", D, index)
+    Tv, ld_v = _rows3(v, "v", kv_heads, D, index)
+    if Tv != Tk:
+        raise ValueError(f"k holds {Tk} tokens, v {Tv}")
+    return Tq, heads, ld_q, Tk, kv_heads, ld_k, ld_v, D
+
+
+def qlin_attn_prompt_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, causal=True, window=0) -> int:
+    return int(_lib.load().qlin_attn_prompt_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, int(causal), window))
+
+
+def qlin_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, out=None, lse=None, want_lse=False,
+                     work=None):
+    """Attention of packed prompts: q fp16 [Tq, heads, head_dim], k and v fp16
+    [Tk, kv_heads, head_dim] (tokens any multiple of 8 elements apart), sequence b
+    at cu_q[b] .. cu_q[b + 1] and cu_k[b] .. cu_k[b + 1] (int32 [B + 1]; None: as
+    the queries).  Causal: a query sees the keys up to its own position, counted
+    from the sequence's end, with a window that many of them.  scale defaults to
+    head_dim ** -0.5.  lse float32 [heads, Tq] is written if given or wanted.
+    work: a uint8 workspace of qlin_attn_prompt_work_bytes(..) bytes, or None to
+    allocate one.  Returns (out, lse); rows of no sequence are left as they were."""
+    lib, index = _lib.load(), _gpu_of(q, "q")
+    Tq, heads, ld_q, Tk, kv_heads, ld_k, ld_v, D = _prompt_rows(q, k, v, index)
+    B, cu_q_p, cu_k_p = _borders(cu_q, cu_k, index)
+    out = _given(out, "out", torch.float16, q.shape, index, q)
+    if lse is not None or want_lse:
+        lse = _given(lse, "lse", torch.float32, (heads, Tq), index, q)
+    if Tq == 0 or B == 0:
+        return out, lse
+    if scale is None:
+        scale = D ** -0.5
+    need = lib.qlin_attn_prompt_work_bytes(heads, kv_heads, D, B, Tq, Tk, int(causal), window)
+    work = _space(work, need, index, q)
+    st = lib.qlin_attn_prompt(q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k, v.data_ptr(), ld_v, kv_heads, D, cu_q_p,
+                              cu_k_p, B, Tq, Tk, scale, int(causal), window, out.data_ptr(), _ptr(lse),
+                              _ptr(work), torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check("qlin_attn_prompt", st)
+    return out, lse
+
+
+def qlin_attn_prompt_backward_work_bytes(heads, Tq) -> int:
+    return int(_lib.load().qlin_attn_prompt_backward_work_bytes(heads, Tq))
+
+
+def _grad(t, name, like, D, index):
+    """A gradient of like's shape, its tokens any multiple of 8 elements apart, or a new one; and the elements apart."""
+    if t is None:
+        t = torch.empty(like.shape, dtype=torch.float16, device=like.device)
+    elif t.shape != like.shape:
+        raise ValueError(f"{name}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return t, _heads3(t, name, D, index)[2]
+
+
+def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=None, causal=True, window=0, dq=None,
+                              dk=None, dv=None, work=None):
+    """Gradients (dq, dk, dv) of qlin_attn_prompt's out, from dout, shaped like it
+    (tokens any multiple of 8 elements apart), and that call's inputs and results.
+    dq, dk and dv may be slices of one tensor.  work: a uint8 workspace of
+    qlin_attn_prompt_backward_work_bytes(heads, Tq) bytes, or None to allocate
+    one.  Rows of no sequence are left as they were."""
+    lib, index = _lib.load(), _gpu_of(q, "q")
+    Tq, heads, ld_q, Tk, kv_heads, ld_k, ld_v, D = _prompt_rows(q, k, v, index)
+    B, cu_q_p, cu_k_p = _borders(cu_q, cu_k, index)
+    if dout.shape != q.shape:
+        raise ValueError(f"dout: expected shape {tuple(q.shape)}, got {tuple(dout.shape)}")
+    ld_do = _heads3(dout, "dout", D, index)[2]
+    out_p = _same(out, "out", torch.float16, q.shape, index)
+    lse_p = _same(lse, "lse", torch.float32, (heads, Tq), index)
+    (dq, ld_dq), (dk, ld_dk), (dv, ld_dv) = (_grad(t, n, x, D, index) for t, n, x in
+                                             ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    if B == 0 or (Tq == 0 and Tk == 0):
+        return dq, dk, dv
+    if scale is None:
+        scale = D ** -0.5
+    work = _space(work, lib.qlin_attn_prompt_backward_work_bytes(heads, Tq), index, q)
+    st = lib.qlin_attn_prompt_backward(dout.data_ptr(), ld_do, q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k,
+                                       v.data_ptr(), ld_v, kv_heads, D, out_p, lse_p, cu_q_p, cu_k_p, B, Tq, Tk, scale,
+                                       int(causal), window, dq.data_ptr(), ld_dq, dk.data_ptr(), ld_dk, dv.data_ptr(),
+                                       ld_dv, _ptr(work), torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check("qlin_attn_prompt_backward", st)
+    return dq, dk, dv
