@@ -37,6 +37,8 @@ struct PromptArgs {
 constexpr int kKeys = 64;
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
+static_assert(kRows == kTileRows, "");
+constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 
 // Weights are exp2(c s - m + kTop); m is the largest c s seen when it was last
 // set, and is set again where one passes it by kSlack: weights stay below 2^15,
@@ -56,17 +58,16 @@ __device__ __forceinline__ v4i finite_only(v4i x) {
 }
 
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptArgs a) {
   constexpr int KS = D / 16, DT = D / 32;
-  constexpr int kBytes = kKeys * D * 2;
+  constexpr int kBytes = Tile<D>::rows(kKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
-  slot = gridDim.x / a.heads - 1 - slot;  // causal rows at the end see the most: they begin first
   int64_t tile;
-  const int64_t b = find_tile<kRows>(a.s.cu_q, a.s.B, slot, tile);
+  const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const Seq s = sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
@@ -110,8 +111,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt_kernel(P
   const uint16_t* kb = a.k + s.k0 * a.ld_k + kvh * D;
   const uint16_t* vb = a.v + s.k0 * a.ld_v + kvh * D;
   TileLoad<D, kKeys, kWaves> kl, vl;
-  kl.init(a.ld_k, wave, lane);
-  vl.init(a.ld_v, wave, lane);
+  kl.init(a.ld_k, lane);
+  vl.init(a.ld_v, lane);
+  Operand<D> op;
+  op.init(lane);
   auto fetch = [&](int t) {
     uint8_t* to = lds + (t & 1) * 2 * kBytes;
     const int64_t at = kbeg + t * kKeys;
@@ -119,13 +122,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt_kernel(P
     vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
   };
 
-  // The lane's part of a transposing read: key lane / 4 of four, four channels.
-  const int key4 = (lane & 15) >> 2, ch = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  auto v_of = [&](const uint8_t* vt, int x, int d) {
-    const int r = 16 * x + 4 * half + key4, e = 32 * d + ch;
-    return join_halves(lds_transposed(vt + lds_at<D>(r, e >> 3) + 2 * (e & 7)),
-                       lds_transposed(vt + lds_at<D>(r + 8, e >> 3) + 2 * (e & 7)));
-  };
   // Some of the wave's, or of the workgroup's, queries do not see some of these keys.
   const int all_lo = low_of(row0 + kRows - 1), all_hi = top_of(row0);
   auto shared_cut = [&](int k0) { return k0 < all_lo || k0 + kKeys > all_hi; };
@@ -161,10 +157,8 @@ again:
 #pragma unroll
       for (int r = 0; r < 16; ++r) st[n][r] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const v8h kf = *reinterpret_cast<const v8h*>(kt + lds_at<D>(32 * n + col, 2 * ks + half));
-        st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], st[n], 0, 0, 0);
-      }
+      for (int ks = 0; ks < KS; ++ks)
+        st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, n, ks), qf[ks], st[n], 0, 0, 0);
     }
     if (cut(k0)) {
 #pragma unroll
@@ -209,7 +203,7 @@ again:
     for (int x = 0; x < 4; ++x)
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_of(vt, x, d), pf[x], o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, x, d), pf[x], o[d], 0, 0, 0);
   }
 
   // A weight of 0 does not keep a V that is not finite out of a sum.  Where a row

@@ -42,9 +42,11 @@ struct GradArgs {
   float* delta;    // [heads x Tq]
 };
 
-constexpr int kStep = 64;  // keys, or queries, of a tile (load64 takes their statistics)
+constexpr int kStep = 64;  // keys of a tile
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
+static_assert(kRows == kTileRows, "");
+constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 
 // p is held times 2^kTop, so that fp16 has weights down to 2^-28 to 2^-11 of
 // themselves.
@@ -110,26 +112,16 @@ __device__ __forceinline__ void store_rows(const v16f (&x)[D / 32], float f, uin
     }
 }
 
-// 16 rows (from r0 on) of a tile by 32 columns (from 32 d on) as the first operand
-// of a product over the rows, in the order in which a lane holds them.
 template <int D>
-__device__ __forceinline__ v8h transposed(const uint8_t* tile, int r0, int d, int lane) {
-  const int r = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2), e = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  return join_halves(lds_transposed(tile + lds_at<D>(r, e >> 3) + 2 * (e & 7)),
-                     lds_transposed(tile + lds_at<D>(r + 8, e >> 3) + 2 * (e & 7)));
-}
-
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel(GradArgs a) {
-  constexpr int KS = D / 16, DT = D / 32, kBytes = kStep * D * 2;
+__global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, kBytes = Tile<D>::rows(kStep);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
-  slot = gridDim.x / a.heads - 1 - slot;
   int64_t tile;
-  const int64_t b = find_tile<kRows>(a.s.cu_q, a.s.B, slot, tile);
+  const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const Seq s = sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
@@ -146,8 +138,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel
   const uint16_t* kb = a.k + s.k0 * a.ld_k + kvh * D;
   const uint16_t* vb = a.v + s.k0 * a.ld_v + kvh * D;
   TileLoad<D, kStep, kWaves> kl, vl;
-  kl.init(a.ld_k, wave, lane);
-  vl.init(a.ld_v, wave, lane);
+  kl.init(a.ld_k, lane);
+  vl.init(a.ld_v, lane);
+  Operand<D> op;
+  op.init(lane);
   auto fetch = [&](int t) {
     uint8_t* to = lds + (t & 1) * 2 * kBytes;
     const int64_t at = kbeg + t * kStep;
@@ -198,20 +192,23 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel
       v16f st = zeros(), dp = zeros();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const v8h*>(kt + lds_at<D>(32 * n + col, 2 * ks + half)), qf[ks], st, 0, 0, 0);
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, n, ks), qf[ks], st, 0, 0, 0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const v8h*>(vt + lds_at<D>(32 * n + col, 2 * ks + half)), df[ks], dp, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(vt, n, ks), df[ks], dp, 0, 0, 0);
       float top = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg));
         st[r] = p * (dp[r] - delta);
-        if (cut) st[r] = static_cast<uint32_t>(k0 + 32 * n + frag_row(r, lane) - lo) < span ? st[r] : 0.0f;
-        top = fmaxf(top, __builtin_fabsf(st[r]));
       }
+      if (cut) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          st[r] = static_cast<uint32_t>(k0 + 32 * n + frag_row(r, lane) - lo) < span ? st[r] : 0.0f;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(st[r]));
       if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
@@ -226,7 +223,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel
         const v8h ds = eight(st, x);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-          dq[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(kt, 32 * n + 16 * x, d, lane), ds, dq[d], 0, 0, 0);
+          dq[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(kt, 2 * n + x, d), ds, dq[d], 0, 0, 0);
       }
     }
   }
@@ -235,17 +232,21 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dq_kernel
 }
 
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kernel(GradArgs a) {
-  constexpr int KS = D / 16, DT = D / 32, kBytes = kStep * D * 2;
+__global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(GradArgs a) {
+  // Registers are short from 128 channels on: V's rows stay in LDS then.
+  constexpr bool kVInLds = D >= 128;
+  constexpr int kStep = kVInLds ? 32 : 64;  // queries of a tile
+  constexpr int KS = D / 16, DT = D / 32, kBytes = Tile<D>::rows(kStep);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
-  __shared__ __attribute__((aligned(1024))) float stats[2][2][kStep];  // -lse and delta of their rows
+  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];    // -lse and delta of their rows
+  __shared__ __attribute__((aligned(1024))) uint8_t v_lds[kVInLds ? Tile<D>::rows(kRows) : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int kv_heads = a.heads / a.group;
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const int64_t b = find_tile<kRows>(a.s.cu_k, a.s.B, slot, tile);
+  const int64_t b = nth_tile<true>(a.s, kv_heads, beside(D), a.causal, a.window, slot, tile);
   const Seq s = sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nk) return;
@@ -264,9 +265,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kerne
 
   const int64_t qw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_q, dw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_do;
   TileLoad<D, kStep, kWaves> ql, dl;
-  ql.init(a.ld_q, wave, lane);
-  dl.init(a.ld_do, wave, lane);
-  int f_head = kvh * a.group, f_tile = 0;  // the next tile to fetch
+  ql.init(a.ld_q, lane);
+  dl.init(a.ld_do, lane);
+  Operand<D> op;
+  op.init(lane);
+  // From the last queries to the first, so that the workgroups of a sequence, which
+  // begin at different queries, go over the same ones at a time.
+  int f_head = kvh * a.group, f_tile = per_head - 1;  // the next tile to fetch
   auto fetch = [&](int t) {
     uint8_t* to = lds + (t & 1) * 2 * kBytes;
     const int64_t at = f_tile * kStep;
@@ -275,10 +280,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kerne
     dl.load(a.dout + dw + at * a.ld_do + f_head * D, a.ld_do, rows, to + kBytes, wave);
     if (wave < 2) {
       const float* src = wave == 0 ? a.neg_lse : a.delta;
-      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows, stats[t & 1][wave], lane);
+      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows < kStep ? rows : kStep, stats[t & 1][wave], lane);
     }
-    if (++f_tile == per_head) {
-      f_tile = 0;
+    if (--f_tile < 0) {
+      f_tile = per_head - 1;
       ++f_head;
     }
   };
@@ -286,35 +291,40 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kerne
 
   const bool there = j < nk;
   const int64_t token = s.k0 + (there ? j : 0);
-  v8h kf[KS], vf[KS];
+  v8h kf[KS], vf[kVInLds ? 1 : KS];
   load_row<D>(a.k + token * a.ld_k + kvh * D + 8 * half, there, kf);
-  load_row<D>(a.v + token * a.ld_v + kvh * D + 8 * half, there, vf);
+  if constexpr (kVInLds) {
+    TileLoad<D, kRows, kWaves> vl;
+    vl.init(a.ld_v, lane);
+    vl.load(a.v + (s.k0 + static_cast<int64_t>(row0)) * a.ld_v + kvh * D, a.ld_v, nk - row0, v_lds, wave);
+  } else {
+    load_row<D>(a.v + token * a.ld_v + kvh * D + 8 * half, there, vf);
+  }
   v16f dk[DT], dv[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zeros();
   float power = 0.0f;  // of ds, the key's own
 
-  int c_tile = 0;
+  int c_tile = per_head;
   for (int t = 0; t < tiles; ++t) {
     tile_barrier();
     if (t + 1 < tiles) fetch(t + 1);
+    if (--c_tile < 0) c_tile = per_head - 1;
     const int i0 = qbeg + c_tile * kStep;
-    if (++c_tile == per_head) c_tile = 0;
     if (i0 >= last_hi || i0 + kStep <= first_lo) continue;
     const bool cut = i0 < first_hi || i0 + kStep > last_lo;
     const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* dt = qt + kBytes;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
+#pragma unroll 1
+    for (int n = 0; n < kStep / 32; ++n) {
       v16f st = zeros(), dp = zeros();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const v8h*>(qt + lds_at<D>(32 * n + col, 2 * ks + half)), kf[ks], st, 0, 0, 0);
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), kf[ks], st, 0, 0, 0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const v8h*>(dt + lds_at<D>(32 * n + col, 2 * ks + half)), vf[ks], dp, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), kVInLds ? op.rows(v_lds, wave, ks) : vf[kVInLds ? 0 : ks],
+                                                    dp, 0, 0, 0);
       float top = 0.0f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -324,13 +334,20 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kerne
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * g + e;
-          const bool seen = !cut || static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span;
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, nl[e]));
-          st[r] = seen ? p : 0.0f;
-          dp[r] = seen ? p * (dp[r] - de[e]) : 0.0f;
-          top = fmaxf(top, __builtin_fabsf(dp[r]));
+          st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, nl[e]));
+          dp[r] = st[r] * (dp[r] - de[e]);
         }
       }
+      if (cut) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool seen = static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span;
+          st[r] = seen ? st[r] : 0.0f;
+          dp[r] = seen ? dp[r] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(dp[r]));
       if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
@@ -345,8 +362,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void prompt_dkv_kerne
         const v8h p8 = eight(st, x), s8 = eight(dp, x);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          dv[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(dt, 32 * n + 16 * x, d, lane), p8, dv[d], 0, 0, 0);
-          dk[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(transposed<D>(qt, 32 * n + 16 * x, d, lane), s8, dk[d], 0, 0, 0);
+          dv[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8, dv[d], 0, 0, 0);
+          dk[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), s8, dk[d], 0, 0, 0);
         }
       }
     }

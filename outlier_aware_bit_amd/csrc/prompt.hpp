@@ -26,30 +26,6 @@ __device__ __forceinline__ int32_t clamp_i32(int32_t v, int32_t lo, int32_t hi) 
   return v < lo ? lo : v > hi ? hi : v;
 }
 
-// The sequence of the slot-th tile of ROWS rows, and which of its tiles that is.
-// Sequence b's tiles have the slots from cu[b] / ROWS + b on, which leaves room
-// for each (and a few slots without a tile): ceil(n / ROWS) <=
-// floor((cu + n) / ROWS) - floor(cu / ROWS) + 1.  A search with 64 probes at a
-// time, the same in every wave.
-template <int ROWS>
-__device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64_t slot, int64_t& tile) {
-  int64_t lo = 0, n = B;  // the last b in [lo, lo + n) whose slots begin at or before `slot`
-  const int lane = threadIdx.x & 63;
-  while (true) {
-    const int64_t step = (n + 63) / 64;
-    const int64_t b = lo + lane * step;
-    const bool at = b < lo + n && cu[b] / ROWS + b <= slot;
-    const int hits = __builtin_popcountll(__ballot(at));
-    const int64_t from = lo + (hits > 0 ? hits - 1 : 0) * step;
-    n = lo + n - from < step ? lo + n - from : step;
-    lo = from;
-    if (step == 1) break;
-  }
-  const int32_t b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));  // B < 2^31
-  tile = slot - (cu[b] / ROWS + b);
-  return b;
-}
-
 __device__ __forceinline__ Seq sequence(const Borders& s, int64_t b) {
   Seq r;
   r.q0 = clamp_i32(s.cu_q[b], 0, s.Tq);
@@ -57,6 +33,118 @@ __device__ __forceinline__ Seq sequence(const Borders& s, int64_t b) {
   r.k0 = clamp_i32(s.cu_k[b], 0, s.Tk);
   r.k1 = clamp_i32(s.cu_k[b + 1], r.k0, s.Tk);
   return r;
+}
+
+constexpr int kTileRows = 128;  // queries, or keys, of a workgroup
+
+// The slot-th tile of kTileRows rows: its sequence, and which of that one's tiles it
+// is (past the last one: no tile).  Sequence b's tiles have the slots from cu[b] / kTileRows + b on, which leaves room
+// for each (and a few slots without a tile): ceil(n / kTileRows) <=
+// floor((cu + n) / kTileRows) - floor(cu / kTileRows) + 1.  A search with 64 probes at a
+// time, the same in every wave.
+__device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64_t slot, int64_t& tile) {
+  int64_t lo = 0, n = B;  // the last b in [lo, lo + n) whose slots begin at or before `slot`
+  const int lane = threadIdx.x & 63;
+  while (true) {
+    const int64_t step = (n + 63) / 64;
+    const int64_t b = lo + lane * step;
+    const bool at = b < lo + n && cu[b] / kTileRows + b <= slot;
+    const int hits = __builtin_popcountll(__ballot(at));
+    const int64_t from = lo + (hits > 0 ? hits - 1 : 0) * step;
+    n = lo + n - from < step ? lo + n - from : step;
+    lo = from;
+    if (step == 1) break;
+  }
+  const int32_t b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));  // B < 2^31
+  tile = slot - (cu[b] / kTileRows + b);
+  return b;
+}
+
+
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// The tile of a workgroup that is the p-th of its head.  Tiles differ in work, in
+// causal attention from none to the whole sequence; workgroups begin in their
+// order and `beside` of them share a CU, so those with the most begin first, and
+// where two share one, the next 256 go the other way round: a CU's first has much
+// where its second has little.  Sixteen prompts of 3 - 4,001 tokens, 32 heads:
+// 930 us in the sequences' order, @ in this one; gradients of 4 x 2,048 tokens 827
+// and @.  With up to 64 sequences every wave finds the p-th by itself, from the
+// number of tiles with at least so many steps; with more, tiles go in the
+// sequences' order.
+//
+// KEYS: tiles of keys, and the work is the queries that see them.
+template <bool KEYS>
+__device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int beside, int causal, int window, int64_t p,
+                                            int64_t& tile) {
+  if (s.B > 64) return find_tile(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
+  const int lane = threadIdx.x & 63;
+  int n = 0, across = 0, shift = 0;  // tiles; steps of the sequence's last (keys: first) tile, nk - nq
+  if (lane < s.B) {
+    const Seq q = sequence(s, lane);
+    const int nq = q.q1 - q.q0, nk = q.k1 - q.k0;
+    n = ((KEYS ? nk : nq) + kTileRows - 1) / kTileRows;
+    across = KEYS ? nq : nk;
+    shift = nk - nq;
+  }
+  const int most = window > 0 && window + kTileRows < across ? window + kTileRows : across;
+  // Tiles of the lane's sequence that go over at least kTileRows u keys (queries).
+  auto at_least = [&](int u) {
+    const int w = u * kTileRows;
+    if (u == 0) return n;
+    if (w > most) return 0;
+    if (!causal) return n;
+    if (KEYS) return clamp_i32(((across - w + shift) >> 7) + 1, 0, n);
+    return n - clamp_i32(((w - shift + kTileRows - 1) >> 7) - 1, 0, n);
+  };
+  static_assert(kTileRows == 128, "the shifts above");
+  const int total = wave_total(n);
+  tile = -1;
+  if (p >= total) return 0;
+  int rank = static_cast<int>(p);
+  const int round = 256 / heads;  // tiles of 256 workgroups
+  if (beside == 2 && round > 0 && total > round && rank < 2 * round) {
+    const int two = total < 2 * round ? total : 2 * round, alone = 2 * round - two;
+    if (rank >= round)
+      rank = two - 1 - (rank - round);
+    else
+      rank = rank >= round - alone ? rank - (round - alone) : rank + alone;
+  }
+  int top = most;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const int v = __shfl_xor(top, o, 64);
+    top = v > top ? v : top;
+  }
+  int lo = 0, hi = __builtin_amdgcn_readfirstlane(top) / kTileRows + 1, past = 0;  // past: tiles of at least hi
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, m = wave_total(at_least(mid));
+    if (m > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      past = m;
+    }
+  }
+  const int from = at_least(lo), here = from - at_least(hi);
+  int before = here;  // of exactly lo, in the sequences before
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(before, o, 64);
+    if (lane >= o) before += v;
+  }
+  before -= here;
+  rank -= past;
+  const uint64_t hit = __ballot(here > 0 && before <= rank && rank < before + here);
+  const int b = __builtin_ctzll(hit);
+  // Causal tiles grow with their number, tiles of keys shrink.
+  const int first = !causal ? 0 : KEYS ? from - here : n - from;
+  tile = __builtin_amdgcn_readlane(first, b) + rank - __builtin_amdgcn_readlane(before, b);
+  return b;
 }
 
 // Workgroups are handed to the 8 XCDs in turn.  Heads that are a multiple of 8
@@ -68,23 +156,27 @@ __device__ __forceinline__ void head_and_slot(uint32_t id, uint32_t heads, uint3
   head = (heads & 7) == 0 ? (h & 7) * (heads >> 3) + (h >> 3) : h;
 }
 
-// Rows of D fp16 values lie in LDS as 16-byte chunks, chunk c of a row at c ^
-// swizzle(row): 16 neighbouring rows then have their chunk c in 16 different
-// places of the 256 bytes that the banks span, and so do four neighbouring
-// rows' runs of four chunks.
+// A tile of rows of D fp16 values in LDS.  What one wave's load brings, 1024 bytes,
+// is a block of 512 / D rows; in it the rows' runs of four 16-byte chunks lie row
+// after row, and blocks lie a little apart.  Then 16 neighbouring rows have their
+// chunk c in 16 different places of the 256 bytes that the banks span, four
+// neighbouring rows' runs of four chunks fill them too, and both addresses move by
+// constants from step to step, so that a lane needs one register for each.
 template <int D>
-__device__ __forceinline__ int swizzle(int row) {
-  if constexpr (D == 64) {
-    const int r = row >> 1;
-    return ((r & 1) << 2) | ((r >> 1) & 3);
-  } else {
-    return ((row & 3) << 2) | ((row >> 2) & 3);
+struct Tile {
+  static constexpr int kBlockRows = 512 / D;
+  static constexpr int kRun = 64 * kBlockRows;  // bytes from a row's four chunks to its next four
+  __device__ static constexpr int block(int b) {
+    return D == 64 ? 1056 * b : D == 128 ? 1040 * b : 2320 * (b >> 1) + 1152 * (b & 1);
   }
-}
-template <int D>
-__device__ __forceinline__ int lds_at(int row, int chunk) {  // in bytes
-  return row * (2 * D) + ((chunk ^ swizzle<D>(row)) << 4);
-}
+  // (64: rows r and r + 4 of a block are a multiple of 256 bytes apart.)
+  __device__ static constexpr int chunk_at(int r, int c) { return D == 64 ? (c & 3) ^ (r >> 2) : c & 3; }
+  __device__ static constexpr int at(int row, int c) {
+    const int r = row % kBlockRows;
+    return block(row / kBlockRows) + (c >> 2) * kRun + 64 * r + 16 * chunk_at(r, c);
+  }
+  __device__ static constexpr int rows(int n) { return block(n / kBlockRows); }  // n a multiple of 8
+};
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
@@ -106,26 +198,27 @@ __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, uin
 #endif
 }
 
-// Loads ROWS rows of D values, `ld` elements apart, into LDS; rows from `rows` on become zeros.  The lanes' source offsets do not
-// depend on the tile.  WAVES waves share the rows.
+// Loads ROWS rows of D values, `ld` elements apart, into LDS; rows from `rows` on
+// become zeros.  WAVES waves share the rows.
 template <int D, int ROWS, int WAVES>
 struct TileLoad {
-  static constexpr int kEach = ROWS * D * 2 / 1024 / WAVES;  // instructions of a wave, 1024 bytes each
+  static constexpr int kEach = ROWS * D * 2 / 1024 / WAVES;  // blocks of a wave
   static_assert(kEach * WAVES * 1024 == ROWS * D * 2, "");
-  uint32_t off[kEach];
+  uint32_t off;  // of the lane's chunk in its block's source
 
-  __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = (wave * kEach + i) * 64 + lane;  // chunk in LDS
-      const int row = at / (D / 8), pos = at % (D / 8);
-      off[i] = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * ld) + ((pos ^ swizzle<D>(row)) << 4);
-    }
+  __device__ __forceinline__ void init(int64_t ld, int lane) {
+    constexpr int R = Tile<D>::kBlockRows;
+    const int r = (lane >> 2) % R, c = 4 * ((lane >> 2) / R) + Tile<D>::chunk_at(r, lane);
+    off = static_cast<uint32_t>(r) * static_cast<uint32_t>(2 * ld) + 16 * c;
   }
   __device__ __forceinline__ void load(const uint16_t* base, int64_t ld, int rows, uint8_t* lds, int wave) const {
     const int32_t n = rows <= 0 ? 0 : static_cast<int32_t>((rows < ROWS ? rows - 1 : ROWS - 1) * (2 * ld) + 2 * D);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) load_to_lds<16>(base, n, off[i], lds + (wave * kEach + i) * 1024);
+    for (int i = 0; i < kEach; ++i) {
+      const int b = wave * kEach + i;
+      load_to_lds<16>(base, n, off + static_cast<uint32_t>(b) * static_cast<uint32_t>(2 * ld * Tile<D>::kBlockRows),
+                      lds + Tile<D>::block(b));
+    }
   }
 };
 // 64 fp32 values, those from `n` on as zeros.
@@ -143,9 +236,32 @@ __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0
 __device__ __forceinline__ v4h lds_transposed(const uint8_t* p) {
   return __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p));
 }
-__device__ __forceinline__ v8h join_halves(v4h a, v4h b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
+
+// A tile's rows as the first operand of a 32x32x16 product, from a lane's base
+// addresses: 32 rows by 16 columns, or, transposed, 32 columns by 16 rows, of
+// which a lane has rows {0-3, 8-11} (lanes 0 - 31) or {4-7, 12-15}, as it holds
+// the columns of a 32 x 32 result.
+template <int D>
+struct Operand {
+  int row;     // row lane & 31, chunk lane >> 5 of a step's two
+  int turned;  // row 4 (lane >> 5) + .., column 16 (lane >> 4 & 1) + ..
+
+  __device__ __forceinline__ void init(int lane) {
+    row = Tile<D>::at(lane & 31, lane >> 5);
+    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2), e = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    turned = Tile<D>::at(r, e >> 3) + 2 * (e & 7);
+  }
+  // Rows 32 n .., columns 16 ks ..
+  __device__ __forceinline__ v8h rows(const uint8_t* tile, int n, int ks) const {
+    return *reinterpret_cast<const v8h*>(tile + row + Tile<D>::rows(32 * n) + (ks >> 1) * Tile<D>::kRun + 32 * (ks & 1));
+  }
+  // Rows 16 x .., columns 32 d ..
+  __device__ __forceinline__ v8h columns(const uint8_t* tile, int x, int d) const {
+    const uint8_t* p = tile + turned + Tile<D>::rows(16 * x) + d * Tile<D>::kRun;
+    const v4h a = lds_transposed(p), b = lds_transposed(p + Tile<D>::rows(8));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
 // Two fp32 to fp16, to the nearest even.
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const v2f f = {a, b};
