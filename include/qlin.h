@@ -668,8 +668,8 @@ qlin_status qlin_kv_slots(const int32_t* lens, const int32_t* add, const int32_t
  * entries become -1; a call does not hand them out again itself.
  *   want      int32 [B] slots (a negative one counts as 0); B at most 65535
  *   page      slots per page, a power of two from 16 to 1024
- *   table     int32 [B x max_pages];  held int32 [B]: entries of each row in use,
- *             from the first on
+ *   table     int32 [B x max_pages], max_pages at most 2^20;  held int32 [B]:
+ *             entries of each row in use, from the first on
  *   ring      int32 [pages] in/out, with room for every page;  state int32 [2]:
  *             head, count
  *   table_out, held_out, state_out  the same shapes; each may be its input

@@ -7,39 +7,27 @@
 namespace qlin {
 namespace {
 
-// Exclusive sum over a workgroup's threads, and the total, of two values at a
-// time.  `lds` holds two values per wave; it may be used again after the call.
+// Exclusive sum over a workgroup's threads, and the total.
 template <int WAVES>
-__device__ __forceinline__ void block_scan(int64_t& x, int64_t& y, int64_t& sum_x, int64_t& sum_y, int64_t (*lds)[2]) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total, int64_t* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t x0 = x, y0 = y;
+  int64_t x = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(x, o, 64), v = __shfl_up(y, o, 64);
-    if (lane >= o) {
-      x += u;
-      y += v;
-    }
+    const int64_t u = __shfl_up(x, o, 64);
+    if (lane >= o) x += u;
   }
-  if (lane == 63) {
-    lds[wave][0] = x;
-    lds[wave][1] = y;
-  }
+  if (lane == 63) lds[wave] = x;
   __syncthreads();
-  x -= x0;
-  y -= y0;
-  sum_x = sum_y = 0;
+  x -= v;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
-    const int64_t u = lds[w][0], v = lds[w][1];
-    if (w < wave) {
-      x += u;
-      y += v;
-    }
-    sum_x += u;
-    sum_y += v;
+    const int64_t u = lds[w];
+    if (w < wave) x += u;
+    total += u;
   }
-  __syncthreads();
+  return x;
 }
 
 // ---------------------------------------------------------------- slots
@@ -65,7 +53,7 @@ __device__ __forceinline__ int32_t at_least_zero(int32_t v) { return v < 0 ? 0 :
 // in LDS where sequences begin among its tokens, and a running maximum over the
 // marks gives each token its sequence.
 __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
-  __shared__ int64_t sums[kSlotWaves][2];
+  __shared__ int64_t sums[kSlotWaves];
   __shared__ int32_t mark[kSlotTokens];   // the sequence that begins here, or -1
   __shared__ int32_t begin[kSlotTokens];  // its first token, from this workgroup's first
   __shared__ int32_t last[kSlotWaves];
@@ -75,9 +63,9 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
   const int64_t b0 = tid * each, b1 = b0 + each < a.B ? b0 + each : a.B;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mark[tid + i * kSlotThreads] = -1;
-  int64_t at = 0, none = 0, total, unused;
+  int64_t at = 0, total;
   for (int64_t b = b0; b < b1; ++b) at += at_least_zero(a.add[b]);
-  block_scan<kSlotWaves>(at, none, total, unused, sums);  // the marks are cleared behind its barriers
+  at = block_scan<kSlotWaves>(at, total, sums);  // the marks are cleared behind its barrier
   for (int64_t b = b0; b < b1; ++b) {
     const int64_t end = at + at_least_zero(a.add[b]);
     if (end > at && at < t0 + kSlotTokens && end > t0) {
@@ -159,85 +147,112 @@ struct PageArgs {
   int32_t* missing;
 };
 
-constexpr int kPageThreads = 1024;
-constexpr int kPageWaves = kPageThreads / 64;
-
-// A workgroup goes over the sequences 1024 at a time, one per thread, and leaves
+// A workgroup goes over the sequences THREADS at a time, one per thread, and leaves
 // in LDS how many pages each holds and will hold and where its changes begin in
 // the ring.  Then the changed entries are moved, each found by a search among
 // the sequences' sums, and, where the table is written elsewhere, the others are
 // copied.  Several workgroups take every so many entries each; each makes the
-// sums for itself.
-__global__ __launch_bounds__(kPageThreads) void kv_pages_kernel(PageArgs a) {
-  __shared__ int64_t sums[kPageWaves][2];
-  __shared__ int32_t held_of[kPageThreads], left_of[kPageThreads];
-  __shared__ int64_t grow_at[kPageThreads], give_at[kPageThreads];
-  __shared__ int64_t move_at[kPageThreads];
-  const int tid = threadIdx.x;
-  const int64_t head = static_cast<uint32_t>(a.state[0]) % static_cast<uint32_t>(a.pages);
-  int64_t count = at_least_zero(a.state[1]);
-  if (count > a.pages) count = a.pages;
-  int64_t asked = 0, given = 0, taken = 0, missing = 0;  // over the sequences so far
-  for (int64_t base = 0; base < a.B; base += kPageThreads) {
+// sums for itself.  A row has at most 2^20 entries, so that sums over 1,024 rows
+// fit 32 bits.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_pages_kernel(PageArgs a) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ uint32_t grows[WAVES];
+  __shared__ uint4 sums[WAVES];
+  __shared__ int32_t held_of[THREADS], left_of[THREADS];
+  __shared__ uint32_t grow_at[THREADS], give_at[THREADS], move_at[THREADS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t pages = static_cast<uint32_t>(a.pages), most = static_cast<uint32_t>(a.max_pages);
+  const uint32_t head = static_cast<uint32_t>(a.state[0]) % pages;
+  uint32_t count = at_least_zero(a.state[1]);
+  if (count > pages) count = pages;
+  uint32_t tail = head + count < pages ? head + count : head + count - pages;
+  int64_t asked = 0, given = 0, missing = 0;  // over the sequences so far
+  uint32_t taken = 0;
+  for (int64_t base = 0; base < a.B; base += THREADS) {
     const int64_t b = base + tid;
-    int32_t held = 0, left = 0;
-    int64_t need = 0, grow = 0;
+    int32_t held = 0;
+    uint32_t need = 0, grow = 0;
     bool fits = true;
     if (b < a.B) {
       held = at_least_zero(a.held[b]);
       if (held > a.max_pages) held = static_cast<int32_t>(a.max_pages);
-      need = (static_cast<int64_t>(at_least_zero(a.want[b])) + (1 << a.page_shift) - 1) >> a.page_shift;
-      fits = need <= a.max_pages;
-      grow = fits && need > held ? need - held : 0;
+      need = (static_cast<uint32_t>(at_least_zero(a.want[b])) + (1u << a.page_shift) - 1) >> a.page_shift;
+      fits = need <= most;
+      grow = fits && need > static_cast<uint32_t>(held) ? need - held : 0;
     }
-    int64_t ahead = grow, none = 0, all, unused;
-    block_scan<kPageWaves>(ahead, none, all, unused, sums);
+    uint32_t ahead = wave_scan(grow);
+    if (lane == 63) grows[wave] = ahead;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const uint32_t u = grows[w];
+      if (w < wave) ahead += u;
+      all += u;
+    }
+    ahead -= grow;
     const bool served = fits && (grow == 0 || asked + ahead + grow <= count);
-    left = served ? static_cast<int32_t>(need) : held;
-    int64_t back = held > left ? held - left : 0, lacks = served ? 0 : need - held, all_back, all_lacks;
-    const int64_t given_here = back;
-    block_scan<kPageWaves>(back, lacks, all_back, all_lacks, sums);
-    int64_t moved = served ? grow + given_here : 0, got = served ? grow : 0, all_moved, all_got;
-    block_scan<kPageWaves>(moved, got, all_moved, all_got, sums);
+    const int32_t left = served ? static_cast<int32_t>(need) : held;
+    const uint32_t back = held > left ? held - left : 0, got = served ? grow : 0, lacks = served ? 0 : need - held;
+    uint32_t backs = wave_scan(back), gots = wave_scan(got);
+    // Wants of 2^31 - 1 slots: up to 2^27 pages a row.
+    const uint32_t lacks_lo = wave_scan(lacks & 0xffffu), lacks_hi = wave_scan(lacks >> 16);
+    if (lane == 63) sums[wave] = make_uint4(backs, gots, lacks_lo, lacks_hi);
+    __syncthreads();
+    uint32_t all_back = 0, all_got = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const uint4 u = sums[w];
+      if (w < wave) {
+        backs += u.x;
+        gots += u.y;
+      }
+      all_back += u.x;
+      all_got += u.y;
+      missing += u.z + (static_cast<int64_t>(u.w) << 16);
+    }
+    backs -= back;
+    gots -= got;
     held_of[tid] = held;
     left_of[tid] = left;
-    grow_at[tid] = taken + got;
-    give_at[tid] = given + back;
-    move_at[tid] = moved;
+    grow_at[tid] = taken + gots;
+    give_at[tid] = backs;
+    move_at[tid] = gots + backs;
     __syncthreads();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kPageThreads;
-    const int64_t mine = static_cast<int64_t>(blockIdx.x) * kPageThreads + tid;
-    for (int64_t i = mine; i < all_moved; i += stride) {
+    const uint32_t stride = gridDim.x * THREADS, mine = blockIdx.x * THREADS + tid, moved = all_back + all_got;
+    const int32_t* table = a.table + base * a.max_pages;
+    int32_t* table_out = a.table_out + base * a.max_pages;
+    for (uint32_t i = mine; i < moved; i += stride) {
       int r = 0;  // the last sequence whose changes begin at or before i
 #pragma unroll
-      for (int o = kPageThreads / 2; o > 0; o >>= 1)
+      for (int o = THREADS / 2; o > 0; o >>= 1)
         if (move_at[r + o] <= i) r += o;
-      const int64_t n = i - move_at[r];
-      const int32_t h = held_of[r], l = left_of[r];
-      const int64_t row = (base + r) * a.max_pages;
+      const uint32_t n = i - move_at[r];
+      const uint32_t h = held_of[r], l = left_of[r], row = r * most;
       if (l > h) {
-        a.table_out[row + h + n] = a.ring[(head + grow_at[r] + n) % a.pages];
+        uint32_t from = head + grow_at[r] + n;  // below 2 pages
+        table_out[row + h + n] = a.ring[from < pages ? from : from - pages];
       } else {
-        a.ring[(head + count + give_at[r] + n) % a.pages] = a.table[row + l + n];
-        a.table_out[row + l + n] = -1;
+        uint32_t to = tail + give_at[r] + n;
+        if (to >= pages) to %= pages;
+        a.ring[to] = table[row + l + n];
+        table_out[row + l + n] = -1;
       }
     }
     if (a.table_out != a.table) {
-      const int64_t rows = a.B - base < kPageThreads ? a.B - base : kPageThreads;
-      const int64_t entries = rows * a.max_pages, from = base * a.max_pages;
-      for (int64_t f = mine; f < entries; f += 4 * stride) {
+      const uint32_t entries = static_cast<uint32_t>(a.B - base < THREADS ? a.B - base : THREADS) * most;
+      for (uint32_t f = mine; f < entries; f += 4 * stride) {
         int32_t id[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) id[j] = f + j * stride < entries ? a.table[from + f + j * stride] : 0;
+        for (int j = 0; j < 4; ++j) id[j] = f + j * stride < entries ? table[f + j * stride] : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t g = f + j * stride;
+          const uint32_t g = f + j * stride;
           if (g < entries) {
-            const int r = static_cast<int>(g >> 31 ? g / a.max_pages
-                                                   : static_cast<uint32_t>(g) / static_cast<uint32_t>(a.max_pages));
-            const int64_t e = g - r * a.max_pages;
-            const int32_t h = held_of[r], l = left_of[r];
-            if (e < (h < l ? h : l) || e >= (h < l ? l : h)) a.table_out[from + g] = id[j];
+            const uint32_t r = g / most, e = g - r * most;
+            const uint32_t h = held_of[r], l = left_of[r];
+            if (e < (h < l ? h : l) || e >= (h < l ? l : h)) table_out[g] = id[j];
           }
         }
       }
@@ -246,14 +261,14 @@ __global__ __launch_bounds__(kPageThreads) void kv_pages_kernel(PageArgs a) {
     asked += all;
     taken += all_got;
     given += all_back;
-    missing += all_lacks;
+    tail = (tail + all_back % pages) % pages;
     __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) {
-    int64_t now = count - taken + given;
-    if (now > a.pages) now = a.pages;
-    a.state_out[0] = static_cast<int32_t>((head + taken) % a.pages);
-    a.state_out[1] = static_cast<int32_t>(now);
+    const int64_t now = count - taken + given;
+    const uint32_t next = head + taken;  // at most 2 pages
+    a.state_out[0] = static_cast<int32_t>(next < pages ? next : next - pages);
+    a.state_out[1] = static_cast<int32_t>(now < a.pages ? now : a.pages);
     a.missing[0] = static_cast<int32_t>(missing < 0x7fffffff ? missing : 0x7fffffff);
   }
 }
@@ -299,8 +314,8 @@ extern "C" qlin_status qlin_kv_pages(const int32_t* want, int64_t B, int64_t max
                "page=%d: a power of two from 16 to 1024", page);
   QLIN_REQUIRE(B >= 0, QLIN_ERR_INVALID_ARG, "B=%lld is negative", (long long)B);
   QLIN_REQUIRE(B <= 65535, QLIN_ERR_SHAPE, "B=%lld: at most 65535", (long long)B);
-  QLIN_REQUIRE(max_pages >= 1 && max_pages <= (kMaxDim - 1) / page, QLIN_ERR_SHAPE,
-               "max_pages=%lld: at least 1, and fewer than 2^31 slots", (long long)max_pages);
+  QLIN_REQUIRE(max_pages >= 1 && max_pages <= (1 << 20) && max_pages <= (kMaxDim - 1) / page, QLIN_ERR_SHAPE,
+               "max_pages=%lld: from 1 to 2^20, and fewer than 2^31 slots", (long long)max_pages);
   QLIN_REQUIRE(pages >= 1 && pages < kMaxDim, QLIN_ERR_SHAPE, "pages=%lld: from 1 to 2^31 - 1", (long long)pages);
   QLIN_DIMS(B, max_pages);
   if (B > 0) {
@@ -320,12 +335,16 @@ extern "C" qlin_status qlin_kv_pages(const int32_t* want, int64_t B, int64_t max
   // Several workgroups where a table is written anew.  They read what others of
   // them write if held or state is updated in place: then, and where only changed
   // entries are written, one.
+  const bool few = B <= 256;  // sequences: one round of 256 threads
   int64_t blocks = 1;
   if (table_out != table && held_out != held && state_out != state) {
-    blocks = (B * max_pages) / (4 * kPageThreads);
+    blocks = (B * max_pages) / (few ? 4 * 256 : 4 * 1024);
     blocks = blocks < 1 ? 1 : blocks > 64 ? 64 : blocks;
   }
-  kv_pages_kernel<<<static_cast<unsigned>(blocks), kPageThreads, 0, as_stream(stream)>>>(a);
+  if (few)
+    kv_pages_kernel<256><<<static_cast<unsigned>(blocks), 256, 0, as_stream(stream)>>>(a);
+  else
+    kv_pages_kernel<1024><<<static_cast<unsigned>(blocks), 1024, 0, as_stream(stream)>>>(a);
   QLIN_LAUNCH_CHECK("kv_pages_kernel");
   return QLIN_OK;
 }

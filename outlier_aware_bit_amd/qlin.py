@@ -518,6 +518,7 @@ class KVCache:
 # short: one expression per tensor, and the full check, which names what is
 # wrong, where it does not hold.
 _current_device = torch._C._cuda_getDevice
+_raw_stream_of = torch._C._cuda_getCurrentRawStream
 
 
 def _elsewhere(t, name, index):
@@ -537,7 +538,7 @@ def _maybe(t, name, dtype, shape, index):
 def _raw_stream(cache):
     if _current_device() != cache.index:  # where a launch goes
         raise ValueError(f"the cache is on cuda:{cache.index}, the current device is cuda:{_current_device()}")
-    return torch._C._cuda_getCurrentRawStream(cache.index)
+    return _raw_stream_of(cache.index)
 
 
 def _rows3(t, name, heads, head_dim, index):
@@ -717,9 +718,9 @@ def qlin_kv_evict(cache, table, lens, max_len, budget, recent, mass, pos, mass_o
 # ---------------------------------------------------------------- around the decoding step
 def _gpu_of(t, name):
     """The index of t's GPU, which has to be the current one: that is where a launch goes."""
-    if t is None or not t.is_cuda:
+    index = -1 if t is None else t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    index = t.get_device()
     if _current_device() != index:
         raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
     return index
@@ -754,13 +755,18 @@ def qlin_kv_slots(lens, add, T, first=None, cu=None, row=None, slot=None, positi
     first_p = None if first is None else _same(first, "first", i32, (B,), index)
     if T < 0:
         raise ValueError(f"T={T} is negative")
-    cu = _given(cu, "cu", i32, (B + 1,), index, lens)
-    row, slot, position = (_given(t, n, i32, (T,), index, lens)
-                           for t, n in ((row, "row"), (slot, "slot"), (position, "position")))
-    lens_out = _given(lens_out, "lens_out", i32, (B,), index, lens)
-    st = lib.qlin_kv_slots(lens_p or None, add_p or None, first_p or None, B, T, cu.data_ptr(), row.data_ptr() or None,
-                           slot.data_ptr() or None, position.data_ptr() or None, lens_out.data_ptr() or None,
-                           torch._C._cuda_getCurrentRawStream(index))
+    if cu is None and row is None and slot is None and position is None and lens_out is None:
+        # One allocation, each array on 16 bytes.
+        cu, _, row, _, slot, _, position, _, lens_out = torch.empty(
+            (B + 1 + (3 - B & 3) + 3 * (T + (-T & 3)) + B,), dtype=i32, device=lens.device).split_with_sizes(
+                (B + 1, 3 - B & 3, T, -T & 3, T, -T & 3, T, -T & 3, B))
+    else:
+        cu = _given(cu, "cu", i32, (B + 1,), index, lens)
+        row, slot, position = (_given(t, n, i32, (T,), index, lens)
+                               for t, n in ((row, "row"), (slot, "slot"), (position, "position")))
+        lens_out = _given(lens_out, "lens_out", i32, (B,), index, lens)
+    st = lib.qlin_kv_slots(lens_p, add_p, first_p, B, T, cu.data_ptr(), row.data_ptr(), slot.data_ptr(),
+                           position.data_ptr(), lens_out.data_ptr(), _raw_stream_of(index))
     if st:
         _lib.check("qlin_kv_slots", st)
     return cu, row, slot, position, lens_out
@@ -777,19 +783,26 @@ def qlin_kv_pages(want, page, table, held, ring, state, table_out=None, held_out
     i32 = torch.int32
     if table.dim() != 2 or want.dim() != 1 or ring.dim() != 1:
         raise ValueError("expected want [B], table [B, max_pages] and ring [pages]")
-    B, most = table.shape
-    want_p = _same(want, "want", i32, (B,), index)
-    table_p, held_p = _same(table, "table", i32, (B, most), index), _same(held, "held", i32, (B,), index)
-    ring_p, state_p = _same(ring, "ring", i32, ring.shape, index), _same(state, "state", i32, (2,), index)
-    table_out, held_out, state_out = (old if new is None else new for old, new in
-                                      ((table, table_out), (held, held_out), (state, state_out)))
-    _same(table_out, "table_out", i32, (B, most), index)
-    _same(held_out, "held_out", i32, (B,), index)
-    _same(state_out, "state_out", i32, (2,), index)
+    B, most = shape = table.shape
+    rows, two = (B,), (2,)
+    table_p, held_p = _same(table, "table", i32, shape, index), _same(held, "held", i32, rows, index)
+    state_p = _same(state, "state", i32, two, index)
+    if table_out is None:
+        table_out, table_out_p = table, table_p
+    else:
+        table_out_p = _same(table_out, "table_out", i32, shape, index)
+    if held_out is None:
+        held_out, held_out_p = held, held_p
+    else:
+        held_out_p = _same(held_out, "held_out", i32, rows, index)
+    if state_out is None:
+        state_out, state_out_p = state, state_p
+    else:
+        state_out_p = _same(state_out, "state_out", i32, two, index)
     missing = _given(missing, "missing", i32, (1,), index, want)
-    st = lib.qlin_kv_pages(want_p or None, B, most, page, table_p or None, held_p or None, ring_p, ring.shape[0],
-                           state_p, table_out.data_ptr() or None, held_out.data_ptr() or None, state_out.data_ptr(),
-                           missing.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+    st = lib.qlin_kv_pages(_same(want, "want", i32, rows, index), B, most, page, table_p, held_p,
+                           _same(ring, "ring", i32, ring.shape, index), ring.shape[0], state_p, table_out_p, held_out_p,
+                           state_out_p, missing.data_ptr(), _raw_stream_of(index))
     if st:
         _lib.check("qlin_kv_pages", st)
     return table_out, held_out, state_out, missing
@@ -815,11 +828,18 @@ def qlin_rope_freqs(rot_dim, base=10000.0, scaling="plain", factor=1.0, original
 
 def _heads3(t, name, head_dim, index):
     """fp16 [n, heads, head_dim], tokens any multiple of 8 elements apart: (n, heads, elements apart)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [T, heads, head_dim], got {tuple(t.shape)}")
-    heads = t.shape[1]
-    n, ld = _rows3(t, name, heads, head_dim, index)
-    return n, heads, ld
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: expected [T, heads, head_dim], got {tuple(shape)}")
+    n, ld = _rows3(t, name, shape[1], head_dim, index)
+    return n, shape[1], ld
+
+
+def _shaped(t, name, shape, D, index):
+    """Elements between the tokens of t, which has to have this shape."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _heads3(t, name, D, index)[2]
 
 
 def qlin_rope(q, k, position, freq, interleaved=False, inverse=False, amplitude=1.0, q_out=None, k_out=None):
@@ -834,32 +854,30 @@ def qlin_rope(q, k, position, freq, interleaved=False, inverse=False, amplitude=
     D = q.shape[-1]
     T, heads, ld_q = _heads3(q, "q", D, index)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"q_out: expected shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
-    ld_qo = _heads3(q_out, "q_out", D, index)[2]
+        q_out, ld_qo = torch.empty((T, heads, D), dtype=torch.float16, device=q.device), heads * D
+    else:
+        ld_qo = _shaped(q_out, "q_out", q.shape, D, index)
     kv_heads, ld_k, ld_ko, k_p, ko_p = 0, 0, 0, None, None
     if k is not None:
         Tk, kv_heads, ld_k = _heads3(k, "k", D, index)
         if Tk != T:
             raise ValueError(f"q holds {T} tokens, k {Tk}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.float16, device=k.device)
-        elif k_out.shape != k.shape:
-            raise ValueError(f"k_out: expected shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
-        ld_ko = _heads3(k_out, "k_out", D, index)[2]
+            k_out, ld_ko = torch.empty((T, kv_heads, D), dtype=torch.float16, device=q.device), kv_heads * D
+        else:
+            ld_ko = _shaped(k_out, "k_out", k.shape, D, index)
         k_p, ko_p = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out needs k")
     position_p = _same(position, "position", torch.int32, (T,), index)
     if freq.dim() != 1:
         raise ValueError(f"freq: expected [rot_dim / 2], got {tuple(freq.shape)}")
-    freq_p = _same(freq, "freq", torch.float64, freq.shape, index)
+    pairs = freq.shape
+    freq_p = _same(freq, "freq", torch.float64, pairs, index)
     if T == 0:
         return q_out, k_out
-    st = lib.qlin_rope(q.data_ptr(), ld_q, heads, k_p, ld_k, kv_heads, T, D, 2 * freq.shape[0], int(interleaved),
-                       position_p, freq_p, amplitude, int(inverse), q_out.data_ptr(), ld_qo, ko_p, ld_ko,
-                       torch._C._cuda_getCurrentRawStream(index))
+    st = lib.qlin_rope(q.data_ptr(), ld_q, heads, k_p, ld_k, kv_heads, T, D, 2 * pairs[0], bool(interleaved), position_p,
+                       freq_p, amplitude, bool(inverse), q_out.data_ptr(), ld_qo, ko_p, ld_ko, _raw_stream_of(index))
     if st:
         _lib.check("qlin_rope", st)
     return q_out, k_out
@@ -922,7 +940,7 @@ def qlin_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0
     work = _space(work, need, index, q)
     st = lib.qlin_attn_prompt(q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k, v.data_ptr(), ld_v, kv_heads, D, cu_q_p,
                               cu_k_p, B, Tq, Tk, scale, int(causal), window, out.data_ptr(), _ptr(lse),
-                              _ptr(work), torch._C._cuda_getCurrentRawStream(index))
+                              _ptr(work), _raw_stream_of(index))
     if st:
         _lib.check("qlin_attn_prompt", st)
     return out, lse
@@ -935,10 +953,8 @@ def qlin_attn_prompt_backward_work_bytes(heads, Tq) -> int:
 def _grad(t, name, like, D, index):
     """A gradient of like's shape, its tokens any multiple of 8 elements apart, or a new one; and the elements apart."""
     if t is None:
-        t = torch.empty(like.shape, dtype=torch.float16, device=like.device)
-    elif t.shape != like.shape:
-        raise ValueError(f"{name}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    return t, _heads3(t, name, D, index)[2]
+        return torch.empty(like.shape, dtype=torch.float16, device=like.device), like.shape[1] * D
+    return t, _shaped(t, name, like.shape, D, index)
 
 
 def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=None, causal=True, window=0, dq=None,
@@ -966,7 +982,7 @@ def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=No
     st = lib.qlin_attn_prompt_backward(dout.data_ptr(), ld_do, q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k,
                                        v.data_ptr(), ld_v, kv_heads, D, out_p, lse_p, cu_q_p, cu_k_p, B, Tq, Tk, scale,
                                        int(causal), window, dq.data_ptr(), ld_dq, dk.data_ptr(), ld_dk, dv.data_ptr(),
-                                       ld_dv, _ptr(work), torch._C._cuda_getCurrentRawStream(index))
+                                       ld_dv, _ptr(work), _raw_stream_of(index))
     if st:
         _lib.check("qlin_attn_prompt_backward", st)
     return dq, dk, dv
