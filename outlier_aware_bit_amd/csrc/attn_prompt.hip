@@ -94,20 +94,6 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptAr
     tiles = to - from;
   }
 
-  // Q^T as the second operand: a lane holds 8 channels of its query per step.
-  v8h qf[KS];
-  {
-    const bool there = i < nq;
-    const uint16_t* q = a.q + (s.q0 + (there ? i : 0)) * a.ld_q + head * D + 8 * half;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      v4i w = *reinterpret_cast<const v4i*>(q + 16 * ks);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = there ? w[j] ^ a.flip : 0;
-      qf[ks] = __builtin_bit_cast(v8h, w);
-    }
-  }
-
   const uint16_t* kb = a.k + s.k0 * a.ld_k + kvh * D;
   const uint16_t* vb = a.v + s.k0 * a.ld_v + kvh * D;
   TileLoad<D, kKeys, kWaves> kl, vl;
@@ -121,6 +107,21 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptAr
     kl.load(kb + at * a.ld_k, a.ld_k, nk - static_cast<int>(at), to, wave);
     vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
   };
+  if (tiles > 0) fetch(0);
+
+  // Q^T as the second operand: a lane holds 8 channels of its query per step.
+  v8h qf[KS];
+  {
+    const bool there = i < nq;
+    const uint16_t* q = a.q + (s.q0 + (there ? i : 0)) * a.ld_q + head * D + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      v4i w = *reinterpret_cast<const v4i*>(q + 16 * ks);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = there ? w[j] ^ a.flip : 0;
+      qf[ks] = __builtin_bit_cast(v8h, w);
+    }
+  }
 
   // Some of the wave's, or of the workgroup's, queries do not see some of these keys.
   const int all_lo = low_of(row0 + kRows - 1), all_hi = top_of(row0);
@@ -138,7 +139,6 @@ again:
     for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   m = kNoRef;
   l = 0.0f;
-  if (tiles > 0) fetch(0);
   for (int t = 0; t < tiles; ++t) {
     tile_barrier();  // tile t has arrived; the tile before it is used up
     if (t + 1 < tiles) fetch(t + 1);
@@ -217,7 +217,10 @@ again:
 #pragma unroll
       for (int r = 0; r < 16; ++r) any = __builtin_fmaf(o[d][r], 0.0f, any);
     careful = __syncthreads_or(any != 0.0f);
-    if (careful) goto again;
+    if (careful) {
+      if (tiles > 0) fetch(0);
+      goto again;
+    }
   } else {
     for (int t = 0; t < tiles; ++t) {
       const int k0 = kbeg + t * kKeys;

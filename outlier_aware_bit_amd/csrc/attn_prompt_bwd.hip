@@ -38,8 +38,8 @@ struct GradArgs {
   uint16_t* dk;
   uint16_t* dv;
   int64_t ld_dq, ld_dk, ld_dv;
-  float* neg_lse;  // [heads x Tq]: kTop - lse log2(e)
-  float* delta;    // [heads x Tq]
+  float* neg_lse;      // [heads x Tq]: kTop - lse log2(e)
+  float* minus_delta;  // [heads x Tq]
 };
 
 constexpr int kStep = 64;  // keys of a tile
@@ -171,14 +171,18 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
     neg = lse == -INFINITY || !there ? -INFINITY : __builtin_fmaf(-kLog2e, lse, kTop);
     if (there && half == 0) {
       a.neg_lse[at] = neg;
-      a.delta[at] = delta;
+      a.minus_delta[at] = -delta;
     }
   }
 
   v16f dq[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) dq[d] = zeros();
-  float power = 0.0f;  // of ds, the query's own
+  v16f less;  // dP's products begin at -delta
+#pragma unroll
+  for (int r = 0; r < 16; ++r) less[r] = -delta;
+  float power = 1.0f, ref = neg;  // of ds, the query's own; the exponent with it
+  bool unset = true;
   for (int t = 0; t < tiles; ++t) {
     tile_barrier();
     if (t + 1 < tiles) fetch(t + 1);
@@ -189,35 +193,35 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
     const uint8_t* vt = kt + kBytes;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      v16f st = zeros(), dp = zeros();
+      v16f st = zeros(), dp = less;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, n, ks), qf[ks], st, 0, 0, 0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(vt, n, ks), df[ks], dp, 0, 0, 0);
-      float top = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg));
-        st[r] = p * (dp[r] - delta);
-      }
+      for (int r = 0; r < 16; ++r) st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, ref)) * dp[r];
       if (cut) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           st[r] = static_cast<uint32_t>(k0 + 32 * n + frag_row(r, lane) - lo) < span ? st[r] : 0.0f;
       }
+      float top = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(st[r]));
-      if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
+      if (__any(top > kCeil || (unset && top > 0.0f))) {
+        // Each query by itself: its bits do not depend on its neighbours'.
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
-        const float next = now ? power_for(top) : power;
-        times(dq, power == 0.0f ? 1.0f : next / power);
-        power = next;
-      }
+        const bool now = top > kCeil || (unset && top > 0.0f);
+        const float by = now ? power_for(top) : 1.0f;
+        times(dq, by);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) st[r] *= power;
+        for (int r = 0; r < 16; ++r) st[r] *= by;
+        unset = unset && !now;
+        power *= by;
+        ref += static_cast<float>(static_cast<int>(__builtin_bit_cast(uint32_t, by) >> 23) - 127);  // log2
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const v8h ds = eight(st, x);
@@ -227,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
       }
     }
   }
-  const float f = power == 0.0f ? 0.0f : a.scale * 0x1p-14f / power;
+  const float f = a.scale * 0x1p-14f / power;
   store_rows<D>(dq, f, a.dq + (s.q0 + static_cast<int64_t>(i)) * a.ld_dq + head * D, half, there);
 }
 
@@ -238,7 +242,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
   constexpr int kStep = kVInLds ? 32 : 64;  // queries of a tile
   constexpr int KS = D / 16, DT = D / 32, kBytes = Tile<D>::rows(kStep);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
-  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];    // -lse and delta of their rows
+  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];    // of their rows: kTop - lse, -delta
   __shared__ __attribute__((aligned(1024))) uint8_t v_lds[kVInLds ? Tile<D>::rows(kRows) : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
     ql.load(a.q + qw + at * a.ld_q + f_head * D, a.ld_q, rows, to, wave);
     dl.load(a.dout + dw + at * a.ld_do + f_head * D, a.ld_do, rows, to + kBytes, wave);
     if (wave < 2) {
-      const float* src = wave == 0 ? a.neg_lse : a.delta;
+      const float* src = wave == 0 ? a.neg_lse : a.minus_delta;
       load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows < kStep ? rows : kStep, stats[t & 1][wave], lane);
     }
     if (--f_tile < 0) {
@@ -317,7 +321,13 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
     const uint8_t* dt = qt + kBytes;
 #pragma unroll 1
     for (int n = 0; n < kStep / 32; ++n) {
-      v16f st = zeros(), dp = zeros();
+      v16f st = zeros(), dp;  // dP's products begin at -delta
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v4f del = *reinterpret_cast<const v4f*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dp[4 * g + e] = del[e];
+      }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), kf[ks], st, 0, 0, 0);
@@ -328,14 +338,12 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
       float top = 0.0f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float4 neg = *reinterpret_cast<const float4*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
-        const float4 del = *reinterpret_cast<const float4*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
-        const float nl[4] = {neg.x, neg.y, neg.z, neg.w}, de[4] = {del.x, del.y, del.z, del.w};
+        const v4f neg = *reinterpret_cast<const v4f*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * g + e;
-          st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, nl[e]));
-          dp[r] = st[r] * (dp[r] - de[e]);
+          st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg[e]));
+          dp[r] *= st[r];
         }
       }
       if (cut) {
@@ -437,7 +445,7 @@ extern "C" qlin_status qlin_attn_prompt_backward(
   a.c = scale * kLog2e, a.scale = scale, a.causal = causal, a.window = prompt_window(window);
   a.dq = dq, a.dk = dk, a.dv = dv, a.ld_dq = ld_dq, a.ld_dk = ld_dk, a.ld_dv = ld_dv;
   a.neg_lse = static_cast<float*>(work);
-  a.delta = a.neg_lse + grad_work(heads, Tq) / 8;
+  a.minus_delta = a.neg_lse + grad_work(heads, Tq) / 8;
   hipStream_t st = as_stream(stream);
   return head_dim == 64 ? launch<64>(a, st) : head_dim == 128 ? launch<128>(a, st) : launch<256>(a, st);
 }

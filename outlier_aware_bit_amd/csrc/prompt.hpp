@@ -2,7 +2,7 @@
 // the packed sequences' borders, tiles of rows in LDS, host-side checks.
 #pragma once
 
-#include "common.hpp"
+#include "kv.hpp"
 
 namespace qlin {
 
@@ -62,9 +62,7 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64
 
 
 __device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return __builtin_amdgcn_readfirstlane(v);
+  return __builtin_amdgcn_readlane(static_cast<int>(wave_scan(static_cast<uint32_t>(v))), 63);
 }
 
 // The tile of a workgroup that is the p-th of its head.  Tiles differ in work, in
@@ -114,13 +112,7 @@ __device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int bes
     else
       rank = rank >= round - alone ? rank - (round - alone) : rank + alone;
   }
-  int top = most;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const int v = __shfl_xor(top, o, 64);
-    top = v > top ? v : top;
-  }
-  int lo = 0, hi = __builtin_amdgcn_readfirstlane(top) / kTileRows + 1, past = 0;  // past: tiles of at least hi
+  int lo = 0, hi = (KEYS ? s.Tq : s.Tk) / kTileRows + 1, past = 0;  // past: tiles of at least hi
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2, m = wave_total(at_least(mid));
     if (m > rank) {
@@ -131,13 +123,7 @@ __device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int bes
     }
   }
   const int from = at_least(lo), here = from - at_least(hi);
-  int before = here;  // of exactly lo, in the sequences before
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(before, o, 64);
-    if (lane >= o) before += v;
-  }
-  before -= here;
+  const int before = static_cast<int>(wave_scan(static_cast<uint32_t>(here))) - here;  // of exactly lo, in the sequences before
   rank -= past;
   const uint64_t hit = __ballot(here > 0 && before <= rank && rank < before + here);
   const int b = __builtin_ctzll(hit);
