@@ -68,7 +68,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptAr
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
   const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = sequence(a.s, b);
+  const Seq s = the_sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows;

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
   const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = sequence(a.s, b);
+  const Seq s = the_sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows, i0 = row0 + 32 * wave, i = i0 + col;
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
   const int64_t b = nth_tile<true>(a.s, kv_heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = sequence(a.s, b);
+  const Seq s = the_sequence(a.s, b);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;

@@ -56,7 +56,7 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64
     if (step == 1) break;
   }
   const int32_t b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));  // B < 2^31
-  tile = slot - (cu[b] / kTileRows + b);
+  tile = slot - (__builtin_amdgcn_readfirstlane(cu[b]) / kTileRows + b);
   return b;
 }
 
@@ -126,11 +126,21 @@ __device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int bes
   const int before = static_cast<int>(wave_scan(static_cast<uint32_t>(here))) - here;  // of exactly lo, in the sequences before
   rank -= past;
   const uint64_t hit = __ballot(here > 0 && before <= rank && rank < before + here);
-  const int b = __builtin_ctzll(hit);
+  const int b = __builtin_amdgcn_readfirstlane(static_cast<int>(__builtin_ctzll(hit)));
   // Causal tiles grow with their number, tiles of keys shrink.
   const int first = !causal ? 0 : KEYS ? from - here : n - from;
   tile = __builtin_amdgcn_readlane(first, b) + rank - __builtin_amdgcn_readlane(before, b);
   return b;
+}
+
+// The same for a sequence that is the same in every lane, in scalar registers.
+__device__ __forceinline__ Seq the_sequence(const Borders& s, int64_t b) {
+  Seq r = sequence(s, b);
+  r.q0 = __builtin_amdgcn_readfirstlane(r.q0);
+  r.q1 = __builtin_amdgcn_readfirstlane(r.q1);
+  r.k0 = __builtin_amdgcn_readfirstlane(r.k0);
+  r.k1 = __builtin_amdgcn_readfirstlane(r.k1);
+  return r;
 }
 
 // Workgroups are handed to the 8 XCDs in turn.  Heads that are a multiple of 8
