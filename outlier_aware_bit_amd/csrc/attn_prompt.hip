@@ -67,8 +67,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptAr
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = the_sequence(a.s, b);
+  const Seq s = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows;
@@ -160,6 +159,10 @@ again:
       for (int ks = 0; ks < KS; ++ks)
         st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, n, ks), qf[ks], st[n], 0, 0, 0);
     }
+    if constexpr (D == 128) {
+      reads_ahead<2 * KS, 1, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (cut(k0)) {
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -204,6 +207,7 @@ again:
 #pragma unroll
       for (int d = 0; d < DT; ++d)
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, x, d), pf[x], o[d], 0, 0, 0);
+    reads_ahead<4 * DT, 2, 4>();
   }
 
   // A weight of 0 does not keep a V that is not finite out of a sum.  Where a row

@@ -121,8 +121,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const int64_t b = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = the_sequence(a.s, b);
+  const Seq s = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows, i0 = row0 + 32 * wave, i = i0 + col;
@@ -235,26 +234,33 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   store_rows<D>(dq, f, a.dq + (s.q0 + static_cast<int64_t>(i)) * a.ld_dq + head * D, half, there);
 }
 
+// Waves work in pairs, each pair on 32 keys: the first has K and makes P and dV,
+// the second has V and makes dP, dS and dK; P goes from the one to the other
+// through LDS in fp32.  Registers then hold one operand and one sum a wave, and a
+// workgroup has two waves for a SIMD by itself, so that a long one is not alone
+// with half of the GPU's rate.
+constexpr int kPairs = 4;
+static_assert(32 * kPairs == kTileRows, "");
+
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(GradArgs a) {
-  // Registers are short from 128 channels on: V's rows stay in LDS then.
-  constexpr bool kVInLds = D >= 128;
-  constexpr int kStep = kVInLds ? 32 : 64;  // queries of a tile
-  constexpr int KS = D / 16, DT = D / 32, kBytes = Tile<D>::rows(kStep);
+__global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kernel(GradArgs a) {
+  constexpr int kStep = D == 256 ? 32 : 64;  // queries of a tile
+  constexpr int KS = D / 16, DT = D / 32, NB = kStep / 32, kBytes = Tile<D>::rows(kStep);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
   __shared__ __attribute__((aligned(1024))) float stats[2][2][64];    // of their rows: kTop - lse, -delta
-  __shared__ __attribute__((aligned(1024))) uint8_t v_lds[kVInLds ? Tile<D>::rows(kRows) : 16];
+  __shared__ v4f weights[kPairs][NB][4][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pair = wave >> 1;
+  const bool second = ((wave ^ (wave >> 2)) & 1) != 0;  // a SIMD has waves i and i + 4: one of each
   const int col = lane & 31, half = lane >> 5;
   const int kv_heads = a.heads / a.group;
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const int64_t b = nth_tile<true>(a.s, kv_heads, beside(D), a.causal, a.window, slot, tile);
-  const Seq s = the_sequence(a.s, b);
+  const Seq s = nth_tile<true>(a.s, kv_heads, D == 64 ? 2 : 1, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nk) return;
-  const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;
+  const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * pair, j = j0 + col;
   // Queries [first, last) see a key.
   auto first_of = [&](int r) { return a.causal ? clamp_i32(r - shift, 0, nq) : 0; };
   auto last_of = [&](int r) {
@@ -268,7 +274,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
   const int tiles = per_head * a.group;
 
   const int64_t qw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_q, dw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_do;
-  TileLoad<D, kStep, kWaves> ql, dl;
+  TileLoad<D, kStep, 2 * kPairs> ql, dl;
   ql.init(a.ld_q, lane);
   dl.init(a.ld_do, lane);
   Operand<D> op;
@@ -284,7 +290,8 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
     dl.load(a.dout + dw + at * a.ld_do + f_head * D, a.ld_do, rows, to + kBytes, wave);
     if (wave < 2) {
       const float* src = wave == 0 ? a.neg_lse : a.minus_delta;
-      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows < kStep ? rows : kStep, stats[t & 1][wave], lane);
+      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows < kStep ? rows : kStep,
+             stats[t & 1][wave], lane);
     }
     if (--f_tile < 0) {
       f_tile = per_head - 1;
@@ -295,91 +302,134 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dkv_kernel(Grad
 
   const bool there = j < nk;
   const int64_t token = s.k0 + (there ? j : 0);
-  v8h kf[KS], vf[kVInLds ? 1 : KS];
-  load_row<D>(a.k + token * a.ld_k + kvh * D + 8 * half, there, kf);
-  if constexpr (kVInLds) {
-    TileLoad<D, kRows, kWaves> vl;
-    vl.init(a.ld_v, lane);
-    vl.load(a.v + (s.k0 + static_cast<int64_t>(row0)) * a.ld_v + kvh * D, a.ld_v, nk - row0, v_lds, wave);
-  } else {
-    load_row<D>(a.v + token * a.ld_v + kvh * D + 8 * half, there, vf);
-  }
-  v16f dk[DT], dv[DT];
+  v8h own[KS];  // K's row, or V's
+  load_row<D>((second ? a.v + token * a.ld_v : a.k + token * a.ld_k) + kvh * D + 8 * half, there, own);
+  v16f sum[DT];  // dV, or dK
 #pragma unroll
-  for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zeros();
-  float power = 0.0f;  // of ds, the key's own
+  for (int d = 0; d < DT; ++d) sum[d] = zeros();
+  const int64_t row = s.k0 + static_cast<int64_t>(j);
+  auto first_query = [&](int t) { return qbeg + (per_head - 1 - t % per_head) * kStep; };
+  auto skipped = [&](int i0) { return i0 >= last_hi || i0 + kStep <= first_lo; };
 
-  int c_tile = per_head;
+  if (!second) {
+    for (int t = 0; t < tiles; ++t) {
+      tile_barrier();
+      if (t + 1 < tiles) fetch(t + 1);
+      const int i0 = first_query(t);
+      const bool skip = skipped(i0);
+      const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
+      const uint8_t* dt = qt + kBytes;
+      v8h p8[NB][2];
+      if (!skip) {
+        v16f st[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          st[n] = zeros();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), own[ks], st[n], 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v4f neg = *reinterpret_cast<const v4f*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st[n][4 * g + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][4 * g + e], a.c, neg[e]));
+          }
+        if (i0 < first_hi || i0 + kStep > last_lo) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              st[n][r] = static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span ? st[n][r] : 0.0f;
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            weights[pair][n][g][lane] = v4f{st[n][4 * g], st[n][4 * g + 1], st[n][4 * g + 2], st[n][4 * g + 3]};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) p8[n][x] = eight(st[n], x);
+        }
+      }
+      lds_barrier();
+      if (skip) continue;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8[n][x], sum[d], 0, 0, 0);
+    }
+    store_rows<D>(sum, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
+    return;
+  }
+
+  float power = 1.0f;  // of ds, the key's own
+  bool unset = true;
   for (int t = 0; t < tiles; ++t) {
     tile_barrier();
     if (t + 1 < tiles) fetch(t + 1);
-    if (--c_tile < 0) c_tile = per_head - 1;
-    const int i0 = qbeg + c_tile * kStep;
-    if (i0 >= last_hi || i0 + kStep <= first_lo) continue;
-    const bool cut = i0 < first_hi || i0 + kStep > last_lo;
+    const int i0 = first_query(t);
+    const bool skip = skipped(i0);
     const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* dt = qt + kBytes;
-#pragma unroll 1
-    for (int n = 0; n < kStep / 32; ++n) {
-      v16f st = zeros(), dp;  // dP's products begin at -delta
+    v16f dp[NB];
+    if (!skip) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const v4f del = *reinterpret_cast<const v4f*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dp[4 * g + e] = del[e];
-      }
+        for (int g = 0; g < 4; ++g) {  // dP's products begin at -delta
+          const v4f del = *reinterpret_cast<const v4f*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), kf[ks], st, 0, 0, 0);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), kVInLds ? op.rows(v_lds, wave, ks) : vf[kVInLds ? 0 : ks],
-                                                    dp, 0, 0, 0);
-      float top = 0.0f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const v4f neg = *reinterpret_cast<const v4f*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * g + e;
-          st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg[e]));
-          dp[r] *= st[r];
+          for (int e = 0; e < 4; ++e) dp[n][4 * g + e] = del[e];
         }
-      }
-      if (cut) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool seen = static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span;
-          st[r] = seen ? st[r] : 0.0f;
-          dp[r] = seen ? dp[r] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(dp[r]));
-      if (__any(top * power > kCeil || (power == 0.0f && top > 0.0f))) {
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const bool now = top * power > kCeil || (power == 0.0f && top > 0.0f);
-        const float next = now ? power_for(top) : power;
-        times(dk, power == 0.0f ? 1.0f : next / power);
-        power = next;
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] *= power;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const v8h p8 = eight(st, x), s8 = eight(dp, x);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          dv[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8, dv[d], 0, 0, 0);
-          dk[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), s8, dk[d], 0, 0, 0);
-        }
+        for (int ks = 0; ks < KS; ++ks)
+          dp[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), own[ks], dp[n], 0, 0, 0);
       }
     }
+    lds_barrier();
+    if (skip) continue;
+    float top = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v4f p = weights[pair][n][g][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dp[n][4 * g + e] *= p[e] * power;
+          top = fmaxf(top, __builtin_fabsf(dp[n][4 * g + e]));
+        }
+      }
+    if (__any(top > kCeil || (unset && top > 0.0f))) {
+      // Each key by itself: its bits do not depend on its neighbours'.
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const bool now = top > kCeil || (unset && top > 0.0f);
+      const float by = now ? power_for(top) : 1.0f;
+      times(sum, by);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[n][r] *= by;
+      unset = unset && !now;
+      power *= by;
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const v8h ds = eight(dp[n], x);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), ds, sum[d], 0, 0, 0);
+      }
   }
-  const float f = power == 0.0f ? 0.0f : a.scale * 0x1p-14f / power;
-  const int64_t row = s.k0 + static_cast<int64_t>(j);
-  store_rows<D>(dk, f, a.dk + row * a.ld_dk + kvh * D, half, there);
-  store_rows<D>(dv, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
+  store_rows<D>(sum, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
 }
 
 template <int D>
@@ -391,7 +441,7 @@ qlin_status launch(const GradArgs& a, hipStream_t st) {
   }
   if (a.s.Tk > 0) {
     const int64_t wgs = (a.s.Tk / kRows + a.s.B) * (a.heads / a.group);
-    prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 64 * kWaves, 0, st>>>(a);
+    prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 128 * kPairs, 0, st>>>(a);
     QLIN_LAUNCH_CHECK("prompt_dkv_kernel");
   }
   return QLIN_OK;

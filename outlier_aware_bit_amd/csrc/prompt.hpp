@@ -61,6 +61,12 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64
 }
 
 
+// That of one lane, in scalar registers.
+__device__ __forceinline__ Seq lane_sequence(const Seq& r, int lane) {
+  return Seq{__builtin_amdgcn_readlane(r.q0, lane), __builtin_amdgcn_readlane(r.q1, lane),
+             __builtin_amdgcn_readlane(r.k0, lane), __builtin_amdgcn_readlane(r.k1, lane)};
+}
+
 __device__ __forceinline__ int wave_total(int v) {
   return __builtin_amdgcn_readlane(static_cast<int>(wave_scan(static_cast<uint32_t>(v))), 63);
 }
@@ -77,18 +83,18 @@ __device__ __forceinline__ int wave_total(int v) {
 //
 // KEYS: tiles of keys, and the work is the queries that see them.
 template <bool KEYS>
-__device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int beside, int causal, int window, int64_t p,
-                                            int64_t& tile) {
-  if (s.B > 64) return find_tile(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
-  const int lane = threadIdx.x & 63;
-  int n = 0, across = 0, shift = 0;  // tiles; steps of the sequence's last (keys: first) tile, nk - nq
-  if (lane < s.B) {
-    const Seq q = sequence(s, lane);
-    const int nq = q.q1 - q.q0, nk = q.k1 - q.k0;
-    n = ((KEYS ? nk : nq) + kTileRows - 1) / kTileRows;
-    across = KEYS ? nq : nk;
-    shift = nk - nq;
+__device__ __forceinline__ Seq nth_tile(const Borders& s, int heads, int beside, int causal, int window, int64_t p,
+                                        int64_t& tile) {
+  if (s.B > 64) {
+    const int64_t b = find_tile(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
+    return lane_sequence(sequence(s, b), 0);
   }
+  const int lane = threadIdx.x & 63;
+  Seq q = {0, 0, 0, 0};
+  if (lane < s.B) q = sequence(s, lane);
+  const int nq = q.q1 - q.q0, nk = q.k1 - q.k0, shift = nk - nq;
+  const int n = ((KEYS ? nk : nq) + kTileRows - 1) / kTileRows;  // tiles
+  const int across = KEYS ? nq : nk;
   const int most = window > 0 && window + kTileRows < across ? window + kTileRows : across;
   // Tiles of the lane's sequence that go over at least kTileRows u keys (queries).
   auto at_least = [&](int u) {
@@ -102,7 +108,7 @@ __device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int bes
   static_assert(kTileRows == 128, "the shifts above");
   const int total = wave_total(n);
   tile = -1;
-  if (p >= total) return 0;
+  if (p >= total) return lane_sequence(q, 0);
   int rank = static_cast<int>(p);
   const int round = 256 / heads;  // tiles of 256 workgroups
   if (beside == 2 && round > 0 && total > round && rank < 2 * round) {
@@ -130,17 +136,7 @@ __device__ __forceinline__ int64_t nth_tile(const Borders& s, int heads, int bes
   // Causal tiles grow with their number, tiles of keys shrink.
   const int first = !causal ? 0 : KEYS ? from - here : n - from;
   tile = __builtin_amdgcn_readlane(first, b) + rank - __builtin_amdgcn_readlane(before, b);
-  return b;
-}
-
-// The same for a sequence that is the same in every lane, in scalar registers.
-__device__ __forceinline__ Seq the_sequence(const Borders& s, int64_t b) {
-  Seq r = sequence(s, b);
-  r.q0 = __builtin_amdgcn_readfirstlane(r.q0);
-  r.q1 = __builtin_amdgcn_readfirstlane(r.q1);
-  r.k0 = __builtin_amdgcn_readfirstlane(r.k0);
-  r.k1 = __builtin_amdgcn_readfirstlane(r.k1);
-  return r;
+  return lane_sequence(q, b);
 }
 
 // Workgroups are handed to the 8 XCDs in turn.  Heads that are a multiple of 8
@@ -258,6 +254,22 @@ struct Operand {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
+// The order of the products before it in their block, and of the reads from LDS
+// that feed them, EACH to a product: reads go AHEAD products before their own.
+// Left to itself the compiler reuses a few registers, and a wave waits for LDS
+// before every few products.
+template <int PRODUCTS, int EACH, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+  constexpr int kReads = 0x100, kProducts = 0x008;
+  __builtin_amdgcn_sched_group_barrier(kReads, AHEAD * EACH, 0);
+#pragma unroll
+  for (int i = 0; i < PRODUCTS - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProducts, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kReads, EACH, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(kProducts, AHEAD, 0);
+}
+
 // Two fp32 to fp16, to the nearest even.
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const v2f f = {a, b};
