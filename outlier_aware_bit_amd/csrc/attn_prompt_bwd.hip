@@ -64,6 +64,17 @@ __device__ __forceinline__ float power_for(float x) {
   return __builtin_bit_cast(float, static_cast<uint32_t>(p < 1 ? 1 : p > 254 ? 254 : p) << 23);
 }
 
+// A lane's ds has grown past fp16, or is the first: the power of two to bring it,
+// and what was added up, to.  Each lane by itself, so that its bits do not depend
+// on its neighbours'.
+__device__ __forceinline__ bool needs_power(float top, bool unset) { return top > kCeil || (unset && top > 0.0f); }
+__device__ __forceinline__ float next_power(float top, bool& unset) {
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  if (!needs_power(top, unset)) return 1.0f;
+  unset = false;
+  return power_for(top);
+}
+
 __device__ __forceinline__ v16f zeros() {
   v16f x;
 #pragma unroll
@@ -209,17 +220,13 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
       float top = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(st[r]));
-      if (__any(top > kCeil || (unset && top > 0.0f))) {
-        // Each query by itself: its bits do not depend on its neighbours'.
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const bool now = top > kCeil || (unset && top > 0.0f);
-        const float by = now ? power_for(top) : 1.0f;
-        times(dq, by);
+      if (__any(needs_power(top, unset))) {
+        const float f = next_power(top, unset);
+        times(dq, f);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) st[r] *= by;
-        unset = unset && !now;
-        power *= by;
-        ref += static_cast<float>(static_cast<int>(__builtin_bit_cast(uint32_t, by) >> 23) - 127);  // log2
+        for (int r = 0; r < 16; ++r) st[r] *= f;
+        power *= f;
+        ref += static_cast<float>(static_cast<int>(__builtin_bit_cast(uint32_t, f) >> 23) - 127);  // log2
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -234,20 +241,208 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   store_rows<D>(dq, f, a.dq + (s.q0 + static_cast<int64_t>(i)) * a.ld_dq + head * D, half, there);
 }
 
-// Waves work in pairs, each pair on 32 keys: the first has K and makes P and dV,
-// the second has V and makes dP, dS and dK; P goes from the one to the other
-// through LDS in fp32.  Registers then hold one operand and one sum a wave, and a
-// workgroup has two waves for a SIMD by itself, so that a long one is not alone
-// with half of the GPU's rate.
+// The queries that see a workgroup's keys, in tiles of STEP, for every query head
+// of the keys' own: from the last queries to the first, so that the workgroups
+// of a sequence, which begin at different queries, go over the same ones at a
+// time.  WAVES waves load them.
+template <int D, int STEP, int WAVES>
+struct Queries {
+  TileLoad<D, STEP, WAVES> ql, dl;
+  int begin, end, per_head, tiles;
+  int head, next;  // of the next tile to fetch
+
+  __device__ __forceinline__ void init(const GradArgs& a, int kvh, int first, int last, int nq, int lane) {
+    ql.init(a.ld_q, lane);
+    dl.init(a.ld_do, lane);
+    begin = first;
+    end = nq;
+    per_head = last > first ? (last - first + STEP - 1) / STEP : 0;
+    tiles = per_head * a.group;
+    head = kvh * a.group;
+    next = per_head - 1;
+  }
+  __device__ __forceinline__ int first_query(int t) const { return begin + (per_head - 1 - t % per_head) * STEP; }
+  // The next tile's rows, and kTop - lse and -delta of each.
+  __device__ __forceinline__ void fetch(const GradArgs& a, const Seq& s, uint8_t* q, uint8_t* dout, float (*stats)[64],
+                                        int wave, int lane) {
+    const int64_t at = begin + next * STEP, token = s.q0 + at;
+    const int rows = end - static_cast<int>(at);
+    ql.load(a.q + token * a.ld_q + head * D, a.ld_q, rows, q, wave);
+    dl.load(a.dout + token * a.ld_do + head * D, a.ld_do, rows, dout, wave);
+    if (wave < 2) {
+      const float* src = wave == 0 ? a.neg_lse : a.minus_delta;
+      load64(src + static_cast<int64_t>(head) * a.s.Tq + token, rows < STEP ? rows : STEP, stats[wave], lane);
+    }
+    if (--next < 0) {
+      next = per_head - 1;
+      ++head;
+    }
+  }
+};
+
+// Queries [first, last) of a sequence see key j.
+struct Seen {
+  int nq, shift, causal, window;
+  __device__ __forceinline__ int first(int j) const { return causal ? clamp_i32(j - shift, 0, nq) : 0; }
+  __device__ __forceinline__ int last(int j) const {
+    return window > 0 && j - shift < nq - window ? clamp_i32(j - shift + window, 0, nq) : nq;
+  }
+};
+
+// Keys j0 .. j0 + 31 of a wave, one to a lane and the lane 32 further on.
+struct KeyRange {
+  int first;      // the lane's key is seen by the queries [first, first + span)
+  uint32_t span;
+  int first_lo, first_hi, last_lo, last_hi;  // over the wave's keys
+
+  __device__ __forceinline__ void init(const Seen& q, int j0, int col) {
+    first = q.first(j0 + col);
+    const int last = q.last(j0 + col);
+    span = last > first ? last - first : 0;
+    first_lo = q.first(j0), first_hi = q.first(j0 + 31), last_lo = q.last(j0), last_hi = q.last(j0 + 31);
+  }
+  // None of the queries i0 .. i0 + n - 1 sees any of the keys; some does not see all.
+  __device__ __forceinline__ bool skipped(int i0, int n) const { return i0 >= last_hi || i0 + n <= first_lo; }
+  __device__ __forceinline__ bool cut(int i0, int n) const { return i0 < first_hi || i0 + n > last_lo; }
+  __device__ __forceinline__ bool seen(int i) const { return static_cast<uint32_t>(i - first) < span; }
+};
+
+// -delta, or kTop - lse, of the rows of a 32 x 32 result.
+__device__ __forceinline__ v4f four_rows(const float* stats, int n, int g, int half) {
+  return *reinterpret_cast<const v4f*>(stats + 32 * n + 8 * g + 4 * half);
+}
+__device__ __forceinline__ v16f sixteen_rows(const float* stats, int n, int half) {
+  v16f x;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const v4f f = four_rows(stats, n, g, half);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * g + e] = f[e];
+  }
+  return x;
+}
+
+// 64 channels: a wave makes P, dV, dS and dK of its 32 keys.  (In pairs, as below,
+// four sequences of 2,048 take 350 us where this takes 333, twelve texts of 60 -
+// 3,001 in a window of 1,000 take 690 where this takes 644, dq in both.)
+__global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a) {
+  constexpr int D = 64, kStep = 64;  // queries of a tile
+  constexpr int KS = D / 16, DT = D / 32, kBytes = Tile<D>::rows(kStep);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
+  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int kv_heads = a.heads / a.group;
+  uint32_t kvh, slot;
+  head_and_slot(blockIdx.x, kv_heads, kvh, slot);
+  int64_t tile;
+  const Seq s = nth_tile<true>(a.s, kv_heads, 2, a.causal, a.window, slot, tile);
+  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
+  if (tile < 0 || tile * kRows >= nk) return;
+  const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;
+  const Seen by{nq, nk - nq, a.causal, a.window};
+  KeyRange keys;
+  keys.init(by, j0, col);
+  Queries<D, kStep, kWaves> queries;
+  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
+  auto fetch = [&](int t) {
+    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+    queries.fetch(a, s, to, to + kBytes, stats[t & 1], wave, lane);
+  };
+  if (queries.tiles > 0) fetch(0);
+  Operand<D> op;
+  op.init(lane);
+  const bool there = j < nk;
+  const int64_t token = s.k0 + (there ? j : 0);
+  v8h kf[KS], vf[KS];
+  load_row<D>(a.k + token * a.ld_k + kvh * D + 8 * half, there, kf);
+  load_row<D>(a.v + token * a.ld_v + kvh * D + 8 * half, there, vf);
+  v16f dk[DT], dv[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zeros();
+  float power = 1.0f;  // of ds, the key's own
+  bool unset = true;
+
+  for (int t = 0; t < queries.tiles; ++t) {
+    tile_barrier();
+    if (t + 1 < queries.tiles) fetch(t + 1);
+    const int i0 = queries.first_query(t);
+    if (keys.skipped(i0, kStep)) continue;
+    const bool cut = keys.cut(i0, kStep);
+    const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
+    const uint8_t* dt = qt + kBytes;
+    // (Both halves at once need three more registers than two waves a SIMD have use
+    // for: 350 and 629 us on the two cases above.)
+#pragma unroll 1
+    for (int n = 0; n < kStep / 32; ++n) {
+      v16f st = zeros(), dp = sixteen_rows(stats[t & 1][1], n, half);  // dP's products begin at -delta
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), kf[ks], st, 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), vf[ks], dp, 0, 0, 0);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v4f neg = four_rows(stats[t & 1][0], n, g, half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * g + e;
+          st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, neg[e]));
+          dp[r] *= st[r] * power;
+        }
+      }
+      if (cut) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool seen = keys.seen(i0 + 32 * n + frag_row(r, lane));
+          st[r] = seen ? st[r] : 0.0f;
+          dp[r] = seen ? dp[r] : 0.0f;
+        }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(dp[r]));
+      if (__any(needs_power(top, unset))) {
+        const float f = next_power(top, unset);
+        times(dk, f);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] *= f;
+        power *= f;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const v8h p8 = eight(st, x), s8 = eight(dp, x);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          dv[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8, dv[d], 0, 0, 0);
+          dk[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), s8, dk[d], 0, 0, 0);
+        }
+      }
+    }
+  }
+  const int64_t row = s.k0 + static_cast<int64_t>(j);
+  store_rows<D>(dk, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
+  store_rows<D>(dv, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
+}
+
+// 128 channels and more: waves work in pairs, each pair on 32 keys.  The first has
+// K and makes P and dV, the second has V and makes dP, dS and dK; P goes from the
+// one to the other through LDS in fp32.  Registers then hold one operand and one
+// sum a wave, and a workgroup has two waves for a SIMD by itself, so that a long
+// one is not alone with half of the GPU's rate.  (A wave for all of it, as above,
+// has V in LDS with 128 channels, and four sequences of 2,048 take 584 us where
+// this takes 556; with 256 it spills, and four of 1,024 take 822 against 330.  The
+// second waves a tile behind the first, one barrier a tile instead of two: 563.)
 constexpr int kPairs = 4;
 static_assert(32 * kPairs == kTileRows, "");
 
 template <int D>
-__global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kernel(GradArgs a) {
+__global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a) {
   constexpr int kStep = D == 256 ? 32 : 64;  // queries of a tile
   constexpr int KS = D / 16, DT = D / 32, NB = kStep / 32, kBytes = Tile<D>::rows(kStep);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of Q, two of dO
-  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];    // of their rows: kTop - lse, -delta
+  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];
   __shared__ v4f weights[kPairs][NB][4][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pair = wave >> 1;
@@ -257,49 +452,22 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const Seq s = nth_tile<true>(a.s, kv_heads, D == 64 ? 2 : 1, a.causal, a.window, slot, tile);
-  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
+  const Seq s = nth_tile<true>(a.s, kv_heads, 1, a.causal, a.window, slot, tile);
+  const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * pair, j = j0 + col;
-  // Queries [first, last) see a key.
-  auto first_of = [&](int r) { return a.causal ? clamp_i32(r - shift, 0, nq) : 0; };
-  auto last_of = [&](int r) {
-    return a.window > 0 && r - shift < nq - a.window ? clamp_i32(r - shift + a.window, 0, nq) : nq;
-  };
-  const int first = first_of(j), last = last_of(j);
-  const uint32_t span = last > first ? last - first : 0;
-  const int first_lo = first_of(j0), first_hi = first_of(j0 + 31), last_lo = last_of(j0), last_hi = last_of(j0 + 31);
-  const int qbeg = first_of(row0), qend = last_of(row0 + kRows - 1);
-  const int per_head = qend > qbeg ? (qend - qbeg + kStep - 1) / kStep : 0;
-  const int tiles = per_head * a.group;
-
-  const int64_t qw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_q, dw = (s.q0 + static_cast<int64_t>(qbeg)) * a.ld_do;
-  TileLoad<D, kStep, 2 * kPairs> ql, dl;
-  ql.init(a.ld_q, lane);
-  dl.init(a.ld_do, lane);
-  Operand<D> op;
-  op.init(lane);
-  // From the last queries to the first, so that the workgroups of a sequence, which
-  // begin at different queries, go over the same ones at a time.
-  int f_head = kvh * a.group, f_tile = per_head - 1;  // the next tile to fetch
+  const Seen by{nq, nk - nq, a.causal, a.window};
+  KeyRange keys;
+  keys.init(by, j0, col);
+  Queries<D, kStep, 2 * kPairs> queries;
+  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
   auto fetch = [&](int t) {
     uint8_t* to = lds + (t & 1) * 2 * kBytes;
-    const int64_t at = f_tile * kStep;
-    const int rows = nq - qbeg - static_cast<int>(at);
-    ql.load(a.q + qw + at * a.ld_q + f_head * D, a.ld_q, rows, to, wave);
-    dl.load(a.dout + dw + at * a.ld_do + f_head * D, a.ld_do, rows, to + kBytes, wave);
-    if (wave < 2) {
-      const float* src = wave == 0 ? a.neg_lse : a.minus_delta;
-      load64(src + static_cast<int64_t>(f_head) * a.s.Tq + s.q0 + qbeg + at, rows < kStep ? rows : kStep,
-             stats[t & 1][wave], lane);
-    }
-    if (--f_tile < 0) {
-      f_tile = per_head - 1;
-      ++f_head;
-    }
+    queries.fetch(a, s, to, to + kBytes, stats[t & 1], wave, lane);
   };
-  if (tiles > 0) fetch(0);
-
+  if (queries.tiles > 0) fetch(0);
+  Operand<D> op;
+  op.init(lane);
   const bool there = j < nk;
   const int64_t token = s.k0 + (there ? j : 0);
   v8h own[KS];  // K's row, or V's
@@ -308,15 +476,13 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
 #pragma unroll
   for (int d = 0; d < DT; ++d) sum[d] = zeros();
   const int64_t row = s.k0 + static_cast<int64_t>(j);
-  auto first_query = [&](int t) { return qbeg + (per_head - 1 - t % per_head) * kStep; };
-  auto skipped = [&](int i0) { return i0 >= last_hi || i0 + kStep <= first_lo; };
 
   if (!second) {
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = 0; t < queries.tiles; ++t) {
       tile_barrier();
-      if (t + 1 < tiles) fetch(t + 1);
-      const int i0 = first_query(t);
-      const bool skip = skipped(i0);
+      if (t + 1 < queries.tiles) fetch(t + 1);
+      const int i0 = queries.first_query(t);
+      const bool skip = keys.skipped(i0, kStep);
       const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
       const uint8_t* dt = qt + kBytes;
       v8h p8[NB][2];
@@ -333,17 +499,16 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const v4f neg = *reinterpret_cast<const v4f*>(&stats[t & 1][0][32 * n + 8 * g + 4 * half]);
+            const v4f neg = four_rows(stats[t & 1][0], n, g, half);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               st[n][4 * g + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][4 * g + e], a.c, neg[e]));
           }
-        if (i0 < first_hi || i0 + kStep > last_lo) {
+        if (keys.cut(i0, kStep)) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              st[n][r] = static_cast<uint32_t>(i0 + 32 * n + frag_row(r, lane) - first) < span ? st[n][r] : 0.0f;
+            for (int r = 0; r < 16; ++r) st[n][r] = keys.seen(i0 + 32 * n + frag_row(r, lane)) ? st[n][r] : 0.0f;
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -354,7 +519,7 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
           for (int x = 0; x < 2; ++x) p8[n][x] = eight(st[n], x);
         }
       }
-      lds_barrier();
+      lds_barrier();  // P has arrived
       if (skip) continue;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
@@ -370,29 +535,24 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
 
   float power = 1.0f;  // of ds, the key's own
   bool unset = true;
-  for (int t = 0; t < tiles; ++t) {
+  for (int t = 0; t < queries.tiles; ++t) {
     tile_barrier();
-    if (t + 1 < tiles) fetch(t + 1);
-    const int i0 = first_query(t);
-    const bool skip = skipped(i0);
+    if (t + 1 < queries.tiles) fetch(t + 1);
+    const int i0 = queries.first_query(t);
+    const bool skip = keys.skipped(i0, kStep);
     const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* dt = qt + kBytes;
     v16f dp[NB];
     if (!skip) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {  // dP's products begin at -delta
-          const v4f del = *reinterpret_cast<const v4f*>(&stats[t & 1][1][32 * n + 8 * g + 4 * half]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dp[n][4 * g + e] = del[e];
-        }
+        dp[n] = sixteen_rows(stats[t & 1][1], n, half);  // its products begin at -delta
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
           dp[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), own[ks], dp[n], 0, 0, 0);
       }
     }
-    lds_barrier();
+    lds_barrier();  // P has arrived
     if (skip) continue;
     float top = 0.0f;
 #pragma unroll
@@ -406,18 +566,14 @@ __global__ __launch_bounds__(128 * kPairs, D == 64 ? 4 : 2) void prompt_dkv_kern
           top = fmaxf(top, __builtin_fabsf(dp[n][4 * g + e]));
         }
       }
-    if (__any(top > kCeil || (unset && top > 0.0f))) {
-      // Each key by itself: its bits do not depend on its neighbours'.
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const bool now = top > kCeil || (unset && top > 0.0f);
-      const float by = now ? power_for(top) : 1.0f;
-      times(sum, by);
+    if (__any(needs_power(top, unset))) {
+      const float f = next_power(top, unset);
+      times(sum, f);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) dp[n][r] *= by;
-      unset = unset && !now;
-      power *= by;
+        for (int r = 0; r < 16; ++r) dp[n][r] *= f;
+      power *= f;
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n)
@@ -441,7 +597,10 @@ qlin_status launch(const GradArgs& a, hipStream_t st) {
   }
   if (a.s.Tk > 0) {
     const int64_t wgs = (a.s.Tk / kRows + a.s.B) * (a.heads / a.group);
-    prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 128 * kPairs, 0, st>>>(a);
+    if constexpr (D == 64)
+      prompt_dkv64_kernel<<<static_cast<unsigned>(wgs), 64 * kWaves, 0, st>>>(a);
+    else
+      prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 128 * kPairs, 0, st>>>(a);
     QLIN_LAUNCH_CHECK("prompt_dkv_kernel");
   }
   return QLIN_OK;

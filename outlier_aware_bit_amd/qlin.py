@@ -757,9 +757,13 @@ def qlin_kv_slots(lens, add, T, first=None, cu=None, row=None, slot=None, positi
         raise ValueError(f"T={T} is negative")
     if cu is None and row is None and slot is None and position is None and lens_out is None:
         # One allocation, each array on 16 bytes.
-        cu, _, row, _, slot, _, position, _, lens_out = torch.empty(
-            (B + 1 + (3 - B & 3) + 3 * (T + (-T & 3)) + B,), dtype=i32, device=lens.device).split_with_sizes(
-                (B + 1, 3 - B & 3, T, -T & 3, T, -T & 3, T, -T & 3, B))
+        T4, B4 = T + 3 & -4, B + 3 & -4
+        row, slot, position, lens_out, cu = torch.empty((3 * T4 + B4 + B + 1,), dtype=i32, device=lens.device) \
+            .split_with_sizes((T4, T4, T4, B4, B + 1))
+        if T4 != T:
+            row, slot, position = row[:T], slot[:T], position[:T]
+        if B4 != B:
+            lens_out = lens_out[:B]
     else:
         cu = _given(cu, "cu", i32, (B + 1,), index, lens)
         row, slot, position = (_given(t, n, i32, (T,), index, lens)
@@ -854,7 +858,7 @@ def qlin_rope(q, k, position, freq, interleaved=False, inverse=False, amplitude=
     D = q.shape[-1]
     T, heads, ld_q = _heads3(q, "q", D, index)
     if q_out is None:
-        q_out, ld_qo = torch.empty((T, heads, D), dtype=torch.float16, device=q.device), heads * D
+        q_out, ld_qo = torch.empty_like(q, memory_format=torch.contiguous_format), heads * D
     else:
         ld_qo = _shaped(q_out, "q_out", q.shape, D, index)
     kv_heads, ld_k, ld_ko, k_p, ko_p = 0, 0, 0, None, None
@@ -863,7 +867,7 @@ def qlin_rope(q, k, position, freq, interleaved=False, inverse=False, amplitude=
         if Tk != T:
             raise ValueError(f"q holds {T} tokens, k {Tk}")
         if k_out is None:
-            k_out, ld_ko = torch.empty((T, kv_heads, D), dtype=torch.float16, device=q.device), kv_heads * D
+            k_out, ld_ko = torch.empty_like(k, memory_format=torch.contiguous_format), kv_heads * D
         else:
             ld_ko = _shaped(k_out, "k_out", k.shape, D, index)
         k_p, ko_p = k.data_ptr(), k_out.data_ptr()
@@ -953,7 +957,7 @@ def qlin_attn_prompt_backward_work_bytes(heads, Tq) -> int:
 def _grad(t, name, like, D, index):
     """A gradient of like's shape, its tokens any multiple of 8 elements apart, or a new one; and the elements apart."""
     if t is None:
-        return torch.empty(like.shape, dtype=torch.float16, device=like.device), like.shape[1] * D
+        return torch.empty_like(like, memory_format=torch.contiguous_format), like.shape[1] * D
     return t, _shaped(t, name, like.shape, D, index)
 
 
