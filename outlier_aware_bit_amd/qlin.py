@@ -8,6 +8,7 @@ kernels; nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -920,6 +921,12 @@ def qlin_attn_prompt_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, causal=Tru
     return int(_lib.load().qlin_attn_prompt_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, int(causal), window))
 
 
+@functools.lru_cache(maxsize=4096)
+def _prompt_need(*sizes):
+    """The workspace of a call of these sizes: a number that follows from them alone."""
+    return _lib.load().qlin_attn_prompt_work_bytes(*sizes)
+
+
 def qlin_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, out=None, lse=None, want_lse=False,
                      work=None):
     """Attention of packed prompts: q fp16 [Tq, heads, head_dim], k and v fp16
@@ -933,18 +940,24 @@ def qlin_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0
     lib, index = _lib.load(), _gpu_of(q, "q")
     Tq, heads, ld_q, Tk, kv_heads, ld_k, ld_v, D = _prompt_rows(q, k, v, index)
     B, cu_q_p, cu_k_p = _borders(cu_q, cu_k, index)
-    out = _given(out, "out", torch.float16, q.shape, index, q)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _same(out, "out", torch.float16, q.shape, index)
     if lse is not None or want_lse:
         lse = _given(lse, "lse", torch.float32, (heads, Tq), index, q)
     if Tq == 0 or B == 0:
         return out, lse
     if scale is None:
         scale = D ** -0.5
-    need = lib.qlin_attn_prompt_work_bytes(heads, kv_heads, D, B, Tq, Tk, int(causal), window)
-    work = _space(work, need, index, q)
+    causal = bool(causal)
+    need = _prompt_need(heads, kv_heads, D, B, Tq, Tk, causal, window)
+    if need:
+        work = _space(work, need, index, q)
     st = lib.qlin_attn_prompt(q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k, v.data_ptr(), ld_v, kv_heads, D, cu_q_p,
-                              cu_k_p, B, Tq, Tk, scale, int(causal), window, out.data_ptr(), _ptr(lse),
-                              _ptr(work), _raw_stream_of(index))
+                              cu_k_p, B, Tq, Tk, scale, causal, window, out.data_ptr(),
+                              None if lse is None else lse.data_ptr(), work.data_ptr() if need else None,
+                              _raw_stream_of(index))
     if st:
         _lib.check("qlin_attn_prompt", st)
     return out, lse
