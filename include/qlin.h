@@ -746,10 +746,11 @@ qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads, const uint
  *             multiple of kv_heads, query head j reads kv head
  *             j / (heads / kv_heads); head_dim 64, 128 or 256
  *   cu_q, cu_k  int32 [B + 1] (device), not decreasing; may be one array.  B at
- *             most 65535.  Borders past Tq or Tk are taken to be there
+ *             most 65535, tokens at most 2^30, (T / 128 + B) * heads below 2^23.
+ *             Borders past Tq or Tk are taken to be there
  *   causal    0 or not;  window  0 (none), or with causal the keys a query sees
- *   out       fp16 [Tq x heads x head_dim], contiguous; rows of no sequence are
- *             left as they were
+ *   out       fp16 [Tq x heads x head_dim], contiguous, not an input; rows of no
+ *             sequence are left as they were
  *   lse       fp32 [heads x Tq] or NULL
  *   work      device workspace of qlin_attn_prompt_work_bytes(..) bytes, 16-byte
  *             aligned (NULL if that is 0); its contents on entry do not matter.
@@ -783,8 +784,8 @@ size_t qlin_attn_prompt_work_bytes(int32_t heads, int32_t kv_heads, int32_t head
  *   q, k, v, cu_q, cu_k, scale, causal, window   as in the forward call, and out
  *             (contiguous) and lse as it wrote them
  *   dq, dk, dv  fp16, shaped as q, k and v, ld_dq, ld_dk and ld_dv elements
- *             between tokens (slices of one gradient of the projection will do);
- *             rows of no sequence are left as they were
+ *             between tokens (slices of one gradient of the projection will do, but
+ *             no inputs); rows of no sequence are left as they were
  *   work      device workspace of qlin_attn_prompt_backward_work_bytes(heads, Tq)
  *             bytes, 16-byte aligned; its contents on entry do not matter.  Calls
  *             that overlap must not share it.

@@ -362,6 +362,7 @@ extern "C" qlin_status qlin_attn_prompt(const uint16_t* q, int64_t ld_q, int32_t
   QLIN_PTR(out);
   QLIN_OPT_PTR(lse);
   QLIN_OPT_PTR(work);
+  QLIN_REQUIRE(out != q && out != k && out != v, QLIN_ERR_INVALID_ARG, "out must not be q, k or v");
   PromptArgs a{q,   k,   v, ld_q, ld_k, ld_v, heads, heads / kv_heads, {cu_q, cu_k, B, (int32_t)Tq, (int32_t)Tk}, 0.0f, 0,
                causal, prompt_window(window), out, lse, 1, nullptr, nullptr};
   a.splits = prompt_splits(heads, head_dim, B, Tq, Tk, window);

@@ -646,6 +646,11 @@ extern "C" qlin_status qlin_attn_prompt_backward(
   }
   QLIN_PTR(cu_q);
   QLIN_PTR(cu_k);
+  for (const uint16_t* g : {dq, dk, dv})
+    QLIN_REQUIRE(g == nullptr || (g != dout && g != q && g != k && g != v && g != out), QLIN_ERR_INVALID_ARG,
+                 "dq, dk and dv must not be inputs: these are read after gradients were written");
+  QLIN_REQUIRE((dk == nullptr || (dk != dq && dk != dv)) && (dv == nullptr || dv != dq), QLIN_ERR_INVALID_ARG,
+               "dq, dk and dv must be apart");
   GradArgs a{};
   a.dout = dout, a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
   a.ld_do = ld_dout, a.ld_q = ld_q, a.ld_k = ld_k, a.ld_v = ld_v;

@@ -294,13 +294,15 @@ __device__ __forceinline__ v8h pack8(float a, float b, float c, float d, float e
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 inline int32_t prompt_window(int32_t window) { return window < kMaxTokens ? window : static_cast<int32_t>(kMaxTokens); }
 
-// What both passes require of their sizes (a grid's workgroups stay below 2^31).
+// What both passes require of their sizes.  A grid of up to 512 threads a workgroup
+// stays below 2^32 threads.
 inline bool prompt_heads_ok(int32_t heads, int32_t kv_heads) {
   return kv_heads >= 1 && heads >= 1 && heads <= 65535 && heads % kv_heads == 0;
 }
 inline bool prompt_sizes_ok(int32_t heads, int64_t B, int64_t Tq, int64_t Tk) {
-  return B <= 65535 && Tq <= kMaxTokens && Tk <= kMaxTokens && (Tq / 32 + B) * heads < kMaxDim &&
-         (Tk / 32 + B) * heads < kMaxDim;
+  const int64_t most = int64_t(1) << 23;
+  return B <= 65535 && Tq <= kMaxTokens && Tk <= kMaxTokens && (Tq / kTileRows + B) * heads < most &&
+         (Tk / kTileRows + B) * heads < most;
 }
 inline bool prompt_shape_ok(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk,
                             int32_t causal, int32_t window) {
@@ -317,7 +319,7 @@ inline bool prompt_shape_ok(int32_t heads, int32_t kv_heads, int32_t head_dim, i
     QLIN_REQUIRE((B) >= 0 && (Tq) >= 0 && (Tk) >= 0, QLIN_ERR_INVALID_ARG, "B=%lld, Tq=%lld, Tk=%lld: negative", \
                  (long long)(B), (long long)(Tq), (long long)(Tk));                                            \
     QLIN_REQUIRE(::qlin::prompt_sizes_ok((heads), (B), (Tq), (Tk)), QLIN_ERR_SHAPE,                            \
-                 "B=%lld, Tq=%lld, Tk=%lld: at most 65535 sequences and 2^30 tokens, fewer than 2^31 tiles",        \
+                 "B=%lld, Tq=%lld, Tk=%lld: at most 65535 sequences and 2^30 tokens, (T / 128 + B) * heads below 2^23",        \
                  (long long)(B), (long long)(Tq), (long long)(Tk));                                            \
     QLIN_REQUIRE((scale) - (scale) == 0.0f, QLIN_ERR_INVALID_ARG, "scale is not finite");                      \
     QLIN_REQUIRE((window) >= 0 && ((window) == 0 || (causal)), QLIN_ERR_INVALID_ARG,                           \

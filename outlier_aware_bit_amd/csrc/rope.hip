@@ -216,7 +216,7 @@ extern "C" qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads,
                    all,         T,               chunk_shift,   rot_dim / 16,   split_shift,
                    position,    freq,            amplitude,     inverse ? -1.0f : 1.0f};
   const int64_t blocks = ((T << (chunk_shift + split_shift)) + kRopeThreads - 1) / kRopeThreads;
-  const unsigned grid = static_cast<unsigned>(blocks < (1 << 24) ? blocks : (1 << 24));
+  const unsigned grid = static_cast<unsigned>(blocks < (1 << 22) ? blocks : (1 << 22));  // below 2^32 threads
   if (interleaved)
     rope_kernel<true><<<grid, kRopeThreads, 0, as_stream(stream)>>>(a);
   else

@@ -299,3 +299,36 @@ def test_empty_calls():
     none = torch.empty(2, 0, device="cuda")
     dq, dk, dv = q.qlin_attn_prompt_backward(e, e, y, y, e, none, cu, five)
     assert torch.all(dk == 0.0) and torch.all(dv == 0.0) and dq.shape == (0, 2, 64)
+
+
+def test_offsets_past_32_bits():
+    # Tokens 2^22 elements apart: 700 of them pass 2^31 elements, in every tensor that may be strided.
+    import torch
+    from outlier_aware_bit_amd import qlin as q
+    log("prompt attention, offsets past 2^31")
+    c = Packed(19, [500, 200], [500, 200], 2, 1, 64)
+    ld, T = 1 << 22, 700
+    room = torch.empty((T, ld), dtype=torch.float16, device="cuda")
+    at = [0]
+
+    def far(x):
+        n = x.shape[1] * x.shape[2]
+        view = room[:, at[0]:at[0] + n].unflatten(1, x.shape[1:])
+        at[0] += n
+        view.copy_(dev(x) if isinstance(x, np.ndarray) else x)
+        return view
+
+    x = [far(t) for t in (c.q, c.k, c.v)]
+    out, lse = q.qlin_attn_prompt(*x, dev(c.cu_q), want_lse=True)
+    want, tol, want_lse, lse_tol = c.forward()
+    within(host(out), want, tol, "out")
+    within(host(lse), want_lse, lse_tol, "lse")
+    grads = [far(torch.zeros(t.shape, dtype=torch.float16, device="cuda")) for t in x]
+    q.qlin_attn_prompt_backward(far(c.dout), *x, out, lse, dev(c.cu_q), dq=grads[0], dk=grads[1], dv=grads[2])
+    for name, g, w, t in zip(("dq", "dk", "dv"), grads, *c.backward()):
+        within(host(g), w, t, name)
+    freq, _ = q.qlin_rope_freqs(64)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    near = q.qlin_rope(x[0].contiguous(), x[1].contiguous(), pos, freq)
+    got = q.qlin_rope(x[0], x[1], pos, freq, q_out=x[0], k_out=x[1])
+    assert all(torch.equal(a, b) for a, b in zip(near, got))

@@ -22,13 +22,13 @@ def rope(q=A, ld_q=512, heads=4, k=A, ld_k=256, kv_heads=2, T=3, D=128, rot=128,
 
 
 def attend(q=A, ld_q=512, heads=4, k=A, ld_k=256, v=A, ld_v=256, kv_heads=2, D=128, cu_q=A, cu_k=A, B=2, Tq=40, Tk=50,
-           scale=1.0, causal=1, window=0, out=A, lse=None, work=None):
+           scale=1.0, causal=1, window=0, out=4 * A, lse=None, work=None):
     return _lib.load().qlin_attn_prompt(q, ld_q, heads, k, ld_k, v, ld_v, kv_heads, D, cu_q, cu_k, B, Tq, Tk, scale,
                                         causal, window, out, lse, work, None)
 
 
 def learn(dout=A, ld_do=512, q=A, ld_q=512, heads=4, k=A, ld_k=256, v=A, ld_v=256, kv_heads=2, D=128, out=A, lse=A,
-          cu_q=A, cu_k=A, B=2, Tq=40, Tk=50, scale=1.0, causal=1, window=0, dq=A, ld_dq=512, dk=A, ld_dk=256, dv=A,
+          cu_q=A, cu_k=A, B=2, Tq=40, Tk=50, scale=1.0, causal=1, window=0, dq=5 * A, ld_dq=512, dk=6 * A, ld_dk=256, dv=7 * A,
           ld_dv=256, work=A):
     return _lib.load().qlin_attn_prompt_backward(dout, ld_do, q, ld_q, heads, k, ld_k, v, ld_v, kv_heads, D, out, lse,
                                                  cu_q, cu_k, B, Tq, Tk, scale, causal, window, dq, ld_dq, dk, ld_dk,
@@ -60,7 +60,7 @@ def test_rope(kw, status):
 BOTH = [(dict(D=96), U), (dict(D=32), U), (dict(heads=3), S), (dict(heads=0), S), (dict(kv_heads=0), S),
         (dict(kv_heads=-2, heads=-4), S), (dict(heads=131072, kv_heads=1), S), (dict(B=-1), I), (dict(Tq=-1), I),
         (dict(Tk=-1), I), (dict(B=65536), S), (dict(Tq=(1 << 30) + 1), S), (dict(Tk=1 << 31), S),
-        (dict(Tq=1 << 30, heads=128, ld_q=16384), S), (dict(scale=float("nan")), I), (dict(scale=float("inf")), I),
+        (dict(Tq=1 << 30, heads=128, ld_q=16384), S), (dict(B=65535, heads=130, ld_q=16640), S), (dict(scale=float("nan")), I), (dict(scale=float("inf")), I),
         (dict(window=-1), I), (dict(window=5, causal=0), I), (dict(ld_q=504), S), (dict(ld_q=516), S),
         (dict(ld_k=0), S), (dict(ld_v=260), S), (dict(ld_v=(1 << 22) + 8), S), (dict(q=None), I), (dict(k=None), I),
         (dict(v=MIS), AL), (dict(out=None), I), (dict(out=MIS), AL), (dict(cu_q=None), I), (dict(cu_k=MIS), AL),
@@ -68,7 +68,8 @@ BOTH = [(dict(D=96), U), (dict(D=32), U), (dict(heads=3), S), (dict(heads=0), S)
 
 
 @pytest.mark.parametrize("kw,status", BOTH + [(dict(lse=MIS), AL), (dict(work=MIS), AL), (dict(Tq=0, q=None), OK),
-                                              (dict(Tq=40, Tk=100000), I)])  # a long axis needs a workspace
+                                              (dict(Tq=40, Tk=100000), I),  # a long axis needs a workspace
+                                              (dict(out=A), I), (dict(q=2 * A, k=2 * A, out=2 * A), I)])
 def test_attention(kw, status):
     assert attend(**kw) == status, _lib.load().qlin_last_error()
 
@@ -76,7 +77,8 @@ def test_attention(kw, status):
 @pytest.mark.parametrize("kw,status", BOTH + [
     (dict(dout=None), I), (dict(lse=None), I), (dict(lse=MIS), AL), (dict(dq=None), I), (dict(dk=MIS), AL),
     (dict(dv=None), I), (dict(work=None), I), (dict(work=MIS), AL), (dict(ld_do=256), S), (dict(ld_dq=508), S),
-    (dict(ld_dk=8), S), (dict(ld_dv=(1 << 23)), S), (dict(Tq=0, Tk=0, q=None, k=None), OK)])
+    (dict(ld_dk=8), S), (dict(ld_dv=(1 << 23)), S), (dict(Tq=0, Tk=0, q=None, k=None), OK), (dict(dq=A), I),
+    (dict(dk=A), I), (dict(dv=A), I), (dict(dk=5 * A), I), (dict(dv=5 * A), I), (dict(dv=6 * A), I)])
 def test_gradients(kw, status):
     assert learn(**kw) == status, _lib.load().qlin_last_error()
 
