@@ -758,13 +758,12 @@ def qlin_kv_slots(lens, add, T, first=None, cu=None, row=None, slot=None, positi
         raise ValueError(f"T={T} is negative")
     if cu is None and row is None and slot is None and position is None and lens_out is None:
         # One allocation, each array on 16 bytes.
-        T4, B4 = T + 3 & -4, B + 3 & -4
-        row, slot, position, lens_out, cu = torch.empty((3 * T4 + B4 + B + 1,), dtype=i32, device=lens.device) \
-            .split_with_sizes((T4, T4, T4, B4, B + 1))
-        if T4 != T:
-            row, slot, position = row[:T], slot[:T], position[:T]
-        if B4 != B:
-            lens_out = lens_out[:B]
+        t4, b4 = -T & 3, -B & 3
+        room = torch.empty((3 * (T + t4) + B + b4 + B + 1,), dtype=i32, device=lens.device)
+        if t4 or b4:
+            row, _, slot, _, position, _, lens_out, _, cu = room.split_with_sizes((T, t4, T, t4, T, t4, B, b4, B + 1))
+        else:
+            row, slot, position, lens_out, cu = room.split_with_sizes((T, T, T, B, B + 1))
     else:
         cu = _given(cu, "cu", i32, (B + 1,), index, lens)
         row, slot, position = (_given(t, n, i32, (T,), index, lens)
