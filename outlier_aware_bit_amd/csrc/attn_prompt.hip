@@ -1,7 +1,7 @@
 // Attention over whole prompts (qlin_attn_prompt).
 //
-// Per workgroup 128 queries of one head, 32 of them to a wave; the keys in tiles
-// of 64.  On 32x32x16 fp16 matrix instructions
+// Per workgroup 128 queries of one head (256 with 256 channels), 32 of them to a
+// wave; the keys in tiles of 64.  On 32x32x16 fp16 matrix instructions
 //   S^T = K Q^T (keys x queries),  P = exp2(c S - m),  O^T = V^T P^T (D x queries)
 // so that a lane holds one query in both products: the softmax's maximum and
 // sum are taken down a lane's registers and across one exchange, the rescaling
@@ -34,11 +34,14 @@ struct PromptArgs {
   float2* part_ml;  // [splits x heads x Tq]: reference exponent and sum
 };
 
-constexpr int kKeys = 64;
-constexpr int kWaves = 4;
-constexpr int kRows = 32 * kWaves;
-static_assert(kRows == kTileRows, "");
-constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
+// With 256 channels LDS has room for one workgroup a CU: eight waves, so that two
+// share a SIMD as elsewhere, and one block of 32 keys at a time, so that their
+// registers suffice.
+constexpr int waves(int D) { return D == 256 ? 8 : 4; }
+constexpr int rows(int D) { return 32 * waves(D); }
+constexpr int keys(int D) { return D == 128 ? 32 : 64; }
+constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU, at least
+constexpr int waves_a_simd(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
 // Weights are exp2(c s - m + kTop); m is the largest c s seen when it was last
 // set, and is set again where one passes it by kSlack: weights stay below 2^15,
@@ -58,8 +61,9 @@ __device__ __forceinline__ v4i finite_only(v4i x) {
 }
 
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptArgs a) {
-  constexpr int KS = D / 16, DT = D / 32;
+__global__ __launch_bounds__(64 * waves(D), waves_a_simd(D)) void prompt_kernel(PromptArgs a) {
+  constexpr int KS = D / 16, DT = D / 32, kWaves = waves(D), kRows = rows(D);
+  constexpr int kKeys = keys(D), NB = D == 64 ? 2 : 1;  // of a tile; blocks of 32 at a time
   constexpr int kBytes = Tile<D>::rows(kKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -67,7 +71,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_kernel(PromptAr
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const Seq s = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows;
@@ -150,64 +154,67 @@ again:
     if (skipped(k0)) continue;
     const uint8_t* kt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* vt = kt + kBytes;
-    v16f st[2];
+#pragma unroll 1
+    for (int b = 0; b < kKeys / 32; b += NB) {
+      v16f st[NB];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) st[n][r] = 0.0f;
+        for (int r = 0; r < 16; ++r) st[n][r] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, n, ks), qf[ks], st[n], 0, 0, 0);
-    }
-    if constexpr (D == 128) {
-      reads_ahead<2 * KS, 1, 4>();
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (cut(k0)) {
+        for (int ks = 0; ks < KS; ++ks)
+          st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, b + n, ks), qf[ks], st[n], 0, 0, 0);
+      }
+      if constexpr (D >= 128) {
+        reads_ahead<NB * KS, 1, D == 256 ? 2 : 4>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (cut(k0)) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const uint32_t j = k0 + 32 * (b + n) + frag_row(r, lane) - lo;
+            st[n][r] = j < span ? st[n][r] : -INFINITY;
+          }
+      }
+      float top = st[0][0];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, st[n][r]);
+      top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.c;
+      if (__any(top > m + kSlack)) {
+        // Each query by itself: its bits do not depend on its neighbours'.
+        const float now = top > m + kSlack ? top : m, f = __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] *= f;
+      }
+      const float ref = kTop - m;
+      v8h pf[2 * NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const uint32_t j = k0 + 32 * n + frag_row(r, lane) - lo;
-          st[n][r] = j < span ? st[n][r] : -INFINITY;
+          st[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][r], a.c, ref));
+          l += st[n][r];
         }
-    }
-    float top = st[0][0];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, st[n][r]);
-    top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.c;
-    if (__any(top > m + kSlack)) {
-      // Each query by itself: its bits do not depend on its neighbours'.
-      const float now = top > m + kSlack ? top : m, f = __builtin_amdgcn_exp2f(m - now);
-      m = now;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] *= f;
-    }
-    const float ref = kTop - m;
-    v8h pf[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        st[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][r], a.c, ref));
-        l += st[n][r];
+        for (int x = 0; x < 2; ++x)
+          pf[2 * n + x] = pack8(st[n][8 * x], st[n][8 * x + 1], st[n][8 * x + 2], st[n][8 * x + 3], st[n][8 * x + 4],
+                                st[n][8 * x + 5], st[n][8 * x + 6], st[n][8 * x + 7]);
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        pf[2 * n + x] = pack8(st[n][8 * x], st[n][8 * x + 1], st[n][8 * x + 2], st[n][8 * x + 3], st[n][8 * x + 4],
-                              st[n][8 * x + 5], st[n][8 * x + 6], st[n][8 * x + 7]);
+      for (int x = 0; x < 2 * NB; ++x)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, 2 * b + x, d), pf[x], o[d], 0, 0, 0);
+      reads_ahead<2 * NB * DT, 2, D == 256 ? 1 : D == 128 ? 3 : 4>();
     }
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, x, d), pf[x], o[d], 0, 0, 0);
-    reads_ahead<4 * DT, 2, 4>();
   }
 
   // A weight of 0 does not keep a V that is not finite out of a sum.  Where a row
@@ -312,14 +319,14 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
     a.lse[at] = l == 0.0f ? -INFINITY : (m - kTop + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// How many workgroups share a row's keys: as many as fill the GPU, each with
-// eight tiles or more of an average sequence.
+// How many workgroups share a row's keys: as many as fill the GPU, each with 512
+// keys or more of an average sequence.
 int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
-  const int64_t groups = (Tq / kRows + B) * heads, room = head_dim == 256 ? 256 : 512;
-  int64_t keys = Tk / B;
-  if (window > 0 && window + kRows < keys) keys = window + kRows;
+  const int64_t groups = (Tq / rows(head_dim) + B) * heads, room = 256 * beside(head_dim);
+  int64_t each = Tk / B;
+  if (window > 0 && window + rows(head_dim) < each) each = window + rows(head_dim);
   int64_t n = room / groups;
-  if (n > keys / (8 * kKeys)) n = keys / (8 * kKeys);
+  if (n > each / 512) n = each / 512;
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 size_t prompt_work(int64_t rows, int32_t head_dim, int splits) {
@@ -328,9 +335,9 @@ size_t prompt_work(int64_t rows, int32_t head_dim, int splits) {
 
 template <int D>
 void launch(const PromptArgs& a, hipStream_t st) {
-  const int64_t slots = a.s.Tq / kRows + a.s.B;
+  const int64_t slots = a.s.Tq / rows(D) + a.s.B;
   const dim3 grid(static_cast<unsigned>(slots * a.heads), static_cast<unsigned>(a.splits));
-  prompt_kernel<D><<<grid, 64 * kWaves, 0, st>>>(a);
+  prompt_kernel<D><<<grid, 64 * waves(D), 0, st>>>(a);
   if (a.splits > 1) {
     const int64_t threads = static_cast<int64_t>(a.heads) * a.s.Tq * (D / 8);
     prompt_join_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a, D == 64 ? 6 : D == 128 ? 7 : 8);

@@ -45,7 +45,6 @@ struct GradArgs {
 constexpr int kStep = 64;  // keys of a tile
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
-static_assert(kRows == kTileRows, "");
 constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 
 // p is held times 2^kTop, so that fp16 has weights down to 2^-28 to 2^-11 of
@@ -132,7 +131,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const Seq s = nth_tile<false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows, i0 = row0 + 32 * wave, i = i0 + col;
@@ -336,7 +335,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const Seq s = nth_tile<true>(a.s, kv_heads, 2, a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, true>(a.s, kv_heads, 2, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;
@@ -435,7 +434,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
 // this takes 556; with 256 it spills, and four of 1,024 take 822 against 330.  The
 // second waves a tile behind the first, one barrier a tile instead of two: 563.)
 constexpr int kPairs = 4;
-static_assert(32 * kPairs == kTileRows, "");
+static_assert(32 * kPairs == kRows, "");
 
 template <int D>
 __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a) {
@@ -452,7 +451,7 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const Seq s = nth_tile<true>(a.s, kv_heads, 1, a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, true>(a.s, kv_heads, 1, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * pair, j = j0 + col;

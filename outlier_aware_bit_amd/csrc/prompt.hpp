@@ -35,20 +35,19 @@ __device__ __forceinline__ Seq sequence(const Borders& s, int64_t b) {
   return r;
 }
 
-constexpr int kTileRows = 128;  // queries, or keys, of a workgroup
-
-// The slot-th tile of kTileRows rows: its sequence, and which of that one's tiles it
-// is (past the last one: no tile).  Sequence b's tiles have the slots from cu[b] / kTileRows + b on, which leaves room
-// for each (and a few slots without a tile): ceil(n / kTileRows) <=
-// floor((cu + n) / kTileRows) - floor(cu / kTileRows) + 1.  A search with 64 probes at a
+// The slot-th tile of ROWS rows (queries, or keys, of a workgroup): its sequence, and which of that one's tiles it
+// is (past the last one: no tile).  Sequence b's tiles have the slots from cu[b] / ROWS + b on, which leaves room
+// for each (and a few slots without a tile): ceil(n / ROWS) <=
+// floor((cu + n) / ROWS) - floor(cu / ROWS) + 1.  A search with 64 probes at a
 // time, the same in every wave.
+template <int ROWS>
 __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64_t slot, int64_t& tile) {
   int64_t lo = 0, n = B;  // the last b in [lo, lo + n) whose slots begin at or before `slot`
   const int lane = threadIdx.x & 63;
   while (true) {
     const int64_t step = (n + 63) / 64;
     const int64_t b = lo + lane * step;
-    const bool at = b < lo + n && cu[b] / kTileRows + b <= slot;
+    const bool at = b < lo + n && cu[b] / ROWS + b <= slot;
     const int hits = __builtin_popcountll(__ballot(at));
     const int64_t from = lo + (hits > 0 ? hits - 1 : 0) * step;
     n = lo + n - from < step ? lo + n - from : step;
@@ -56,7 +55,7 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64
     if (step == 1) break;
   }
   const int32_t b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));  // B < 2^31
-  tile = slot - (__builtin_amdgcn_readfirstlane(cu[b]) / kTileRows + b);
+  tile = slot - (__builtin_amdgcn_readfirstlane(cu[b]) / ROWS + b);
   return b;
 }
 
@@ -82,30 +81,31 @@ __device__ __forceinline__ int wave_total(int v) {
 // sequences' order.
 //
 // KEYS: tiles of keys, and the work is the queries that see them.
-template <bool KEYS>
+template <int ROWS, bool KEYS>
 __device__ __forceinline__ Seq nth_tile(const Borders& s, int heads, int beside, int causal, int window, int64_t p,
                                         int64_t& tile) {
   if (s.B > 64) {
-    const int64_t b = find_tile(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
+    const int64_t b = find_tile<ROWS>(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
     return lane_sequence(sequence(s, b), 0);
   }
+  constexpr int kShift = ROWS == 256 ? 8 : 7;
+  static_assert(ROWS == 1 << kShift, "");
   const int lane = threadIdx.x & 63;
   Seq q = {0, 0, 0, 0};
   if (lane < s.B) q = sequence(s, lane);
   const int nq = q.q1 - q.q0, nk = q.k1 - q.k0, shift = nk - nq;
-  const int n = ((KEYS ? nk : nq) + kTileRows - 1) / kTileRows;  // tiles
+  const int n = ((KEYS ? nk : nq) + ROWS - 1) / ROWS;  // tiles
   const int across = KEYS ? nq : nk;
-  const int most = window > 0 && window + kTileRows < across ? window + kTileRows : across;
-  // Tiles of the lane's sequence that go over at least kTileRows u keys (queries).
+  const int most = window > 0 && window + ROWS < across ? window + ROWS : across;
+  // Tiles of the lane's sequence that go over at least ROWS u keys (queries).
   auto at_least = [&](int u) {
-    const int w = u * kTileRows;
+    const int w = u * ROWS;
     if (u == 0) return n;
     if (w > most) return 0;
     if (!causal) return n;
-    if (KEYS) return clamp_i32(((across - w + shift) >> 7) + 1, 0, n);
-    return n - clamp_i32(((w - shift + kTileRows - 1) >> 7) - 1, 0, n);
+    if (KEYS) return clamp_i32(((across - w + shift) >> kShift) + 1, 0, n);
+    return n - clamp_i32(((w - shift + ROWS - 1) >> kShift) - 1, 0, n);
   };
-  static_assert(kTileRows == 128, "the shifts above");
   const int total = wave_total(n);
   tile = -1;
   if (p >= total) return lane_sequence(q, 0);
@@ -118,7 +118,7 @@ __device__ __forceinline__ Seq nth_tile(const Borders& s, int heads, int beside,
     else
       rank = rank >= round - alone ? rank - (round - alone) : rank + alone;
   }
-  int lo = 0, hi = (KEYS ? s.Tq : s.Tk) / kTileRows + 1, past = 0;  // past: tiles of at least hi
+  int lo = 0, hi = (KEYS ? s.Tq : s.Tk) / ROWS + 1, past = 0;  // past: tiles of at least hi
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2, m = wave_total(at_least(mid));
     if (m > rank) {
@@ -301,8 +301,7 @@ inline bool prompt_heads_ok(int32_t heads, int32_t kv_heads) {
 }
 inline bool prompt_sizes_ok(int32_t heads, int64_t B, int64_t Tq, int64_t Tk) {
   const int64_t most = int64_t(1) << 23;
-  return B <= 65535 && Tq <= kMaxTokens && Tk <= kMaxTokens && (Tq / kTileRows + B) * heads < most &&
-         (Tk / kTileRows + B) * heads < most;
+  return B <= 65535 && Tq <= kMaxTokens && Tk <= kMaxTokens && (Tq / 128 + B) * heads < most && (Tk / 128 + B) * heads < most;
 }
 inline bool prompt_shape_ok(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk,
                             int32_t causal, int32_t window) {
