@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64 * waves(D), waves_a_simd(D)) void prompt_kernel(
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const Seq s = nth_tile<kRows, false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, false>(a.s, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows;

@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   uint32_t head, slot;
   head_and_slot(blockIdx.x, a.heads, head, slot);
   int64_t tile;
-  const Seq s = nth_tile<kRows, false>(a.s, a.heads, beside(D), a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, false>(a.s, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0, shift = nk - nq;
   if (tile < 0 || tile * kRows >= nq) return;
   const int row0 = static_cast<int>(tile) * kRows, i0 = row0 + 32 * wave, i = i0 + col;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const Seq s = nth_tile<kRows, true>(a.s, kv_heads, 2, a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, true>(a.s, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * wave, j = j0 + col;
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   uint32_t kvh, slot;
   head_and_slot(blockIdx.x, kv_heads, kvh, slot);
   int64_t tile;
-  const Seq s = nth_tile<kRows, true>(a.s, kv_heads, 1, a.causal, a.window, slot, tile);
+  const Seq s = nth_tile<kRows, true>(a.s, a.causal, a.window, slot, tile);
   const int nq = s.q1 - s.q0, nk = s.k1 - s.k0;
   if (tile < 0 || tile * kRows >= nk) return;
   const int row0 = static_cast<int>(tile) * kRows, j0 = row0 + 32 * pair, j = j0 + col;

@@ -59,7 +59,6 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* cu, int64_t B, int64
   return b;
 }
 
-
 // That of one lane, in scalar registers.
 __device__ __forceinline__ Seq lane_sequence(const Seq& r, int lane) {
   return Seq{__builtin_amdgcn_readlane(r.q0, lane), __builtin_amdgcn_readlane(r.q1, lane),
@@ -70,20 +69,18 @@ __device__ __forceinline__ int wave_total(int v) {
   return __builtin_amdgcn_readlane(static_cast<int>(wave_scan(static_cast<uint32_t>(v))), 63);
 }
 
-// The tile of a workgroup that is the p-th of its head.  Tiles differ in work, in
-// causal attention from none to the whole sequence; workgroups begin in their
-// order and `beside` of them share a CU, so those with the most begin first, and
-// where two share one, the next 256 go the other way round: a CU's first has much
-// where its second has little.  Sixteen prompts of 3 - 4,001 tokens, 32 heads:
-// 930 us in the sequences' order, @ in this one; gradients of 4 x 2,048 tokens 827
-// and @.  With up to 64 sequences every wave finds the p-th by itself, from the
-// number of tiles with at least so many steps; with more, tiles go in the
+// The tile of a workgroup that is the p-th of its head, and its sequence.  Tiles
+// differ in work, in causal attention from none to the whole sequence, and
+// workgroups begin in their order: those with the most first.  In the sequences'
+// order sixteen prompts of 3 - 4,001 tokens take 930 us where they take 900 in
+// this one, and gradients of 4 x 2,048 tokens 827 and 720 (both as the kernels
+// were then).  With up to 64 sequences every wave finds the p-th by itself, from
+// the number of tiles with at least so many steps; with more, tiles go in the
 // sequences' order.
 //
 // KEYS: tiles of keys, and the work is the queries that see them.
 template <int ROWS, bool KEYS>
-__device__ __forceinline__ Seq nth_tile(const Borders& s, int heads, int beside, int causal, int window, int64_t p,
-                                        int64_t& tile) {
+__device__ __forceinline__ Seq nth_tile(const Borders& s, int causal, int window, int64_t p, int64_t& tile) {
   if (s.B > 64) {
     const int64_t b = find_tile<ROWS>(KEYS ? s.cu_k : s.cu_q, s.B, p, tile);
     return lane_sequence(sequence(s, b), 0);
@@ -110,14 +107,6 @@ __device__ __forceinline__ Seq nth_tile(const Borders& s, int heads, int beside,
   tile = -1;
   if (p >= total) return lane_sequence(q, 0);
   int rank = static_cast<int>(p);
-  const int round = 256 / heads;  // tiles of 256 workgroups
-  if (beside == 2 && round > 0 && total > round && rank < 2 * round) {
-    const int two = total < 2 * round ? total : 2 * round, alone = 2 * round - two;
-    if (rank >= round)
-      rank = two - 1 - (rank - round);
-    else
-      rank = rank >= round - alone ? rank - (round - alone) : rank + alone;
-  }
   int lo = 0, hi = (KEYS ? s.Tq : s.Tk) / ROWS + 1, past = 0;  // past: tiles of at least hi
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2, m = wave_total(at_least(mid));
