@@ -207,11 +207,14 @@ extern "C" qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads,
   QLIN_PTR(q_out);
   QLIN_OPT_PTR(k_out);
   const int chunk_shift = head_dim == 64 ? 2 : head_dim == 128 ? 3 : 4, all = heads + kv_heads;
-  // A thread per unit and head where tokens are few; eight threads share a unit's
-  // heads where they are many.
+  // A thread per unit and head where tokens are few, down to eight threads for a
+  // unit's heads while 512 workgroups are left: its angles are worked out once for
+  // each.  32 + 8 heads of 128, in us: one token 2.8, and 4.2 with eight; 1,024
+  // tokens 6.6, and 8.6 with a thread per head, 7.2 with eight; 32,768 tokens 129,
+  // and 184 with a thread per head, 137 with four.
   int split_shift = 0;
   while ((1 << split_shift) < all) ++split_shift;
-  while (split_shift > 3 && T << (chunk_shift + split_shift - 1) >= 256 * 2048) --split_shift;
+  while (split_shift > 3 && T << (chunk_shift + split_shift - 1) >= 256 * 512) --split_shift;
   const RopeArgs a{{q, k},      {q_out, k_out},  {ld_q, ld_k},  {ld_qo, ld_ko}, heads,
                    all,         T,               chunk_shift,   rot_dim / 16,   split_shift,
                    position,    freq,            amplitude,     inverse ? -1.0f : 1.0f};
