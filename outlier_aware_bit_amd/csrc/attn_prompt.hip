@@ -40,8 +40,8 @@ struct PromptArgs {
 constexpr int waves(int D) { return D == 256 ? 8 : 4; }
 constexpr int rows(int D) { return 32 * waves(D); }
 constexpr int keys(int D) { return D == 128 ? 32 : 64; }
-constexpr int beside(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU, at least
 constexpr int waves_a_simd(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+constexpr int beside(int D) { return 4 * waves_a_simd(D) / waves(D); }  // workgroups of a CU
 
 // Weights are exp2(c s - m + kTop); m is the largest c s seen when it was last
 // set, and is set again where one passes it by kSlack: weights stay below 2^15,
@@ -104,13 +104,12 @@ __global__ __launch_bounds__(64 * waves(D), waves_a_simd(D)) void prompt_kernel(
   vl.init(a.ld_v, lane);
   Operand<D> op;
   op.init(lane);
-  auto fetch = [&](int t) {
-    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+  auto fetch = [&](int t, uint8_t* to, const uint16_t* kb, const uint16_t* vb) {
     const int64_t at = kbeg + t * kKeys;
     kl.load(kb + at * a.ld_k, a.ld_k, nk - static_cast<int>(at), to, wave);
     vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
   };
-  if (tiles > 0) fetch(0);
+  if (tiles > 0) fetch(0, lds, kb, vb);
 
   // Q^T as the second operand: a lane holds 8 channels of its query per step.
   v8h qf[KS];
@@ -142,17 +141,12 @@ again:
     for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   m = kNoRef;
   l = 0.0f;
-  for (int t = 0; t < tiles; ++t) {
-    tile_barrier();  // tile t has arrived; the tile before it is used up
-    if (t + 1 < tiles) fetch(t + 1);
+  // Parameters apart from each other: see tile_barrier.
+  auto step = [&](int t, const uint8_t* __restrict__ kt, uint8_t* __restrict__ next, const uint16_t* __restrict__ kb,
+                  const uint16_t* __restrict__ vb) __attribute__((always_inline)) {
+    if (t + 1 < tiles) fetch(t + 1, next, kb, vb);
     const int k0 = kbeg + t * kKeys;
-    if (careful && shared_cut(k0)) {
-      v4i* v = reinterpret_cast<v4i*>(lds + (t & 1) * 2 * kBytes + kBytes);
-      for (int x = tid; x < kBytes / 16; x += 64 * kWaves) v[x] = finite_only(v[x]);
-      tile_barrier();
-    }
-    if (skipped(k0)) continue;
-    const uint8_t* kt = lds + (t & 1) * 2 * kBytes;
+    if (skipped(k0)) return;
     const uint8_t* vt = kt + kBytes;
 #pragma unroll 1
     for (int b = 0; b < kKeys / 32; b += NB) {
@@ -183,7 +177,7 @@ again:
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, st[n][r]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.c;
+      top = larger_half(top) * a.c;
       if (__any(top > m + kSlack)) {
         // Each query by itself: its bits do not depend on its neighbours'.
         const float now = top > m + kSlack ? top : m, f = __builtin_amdgcn_exp2f(m - now);
@@ -213,8 +207,19 @@ again:
 #pragma unroll
         for (int d = 0; d < DT; ++d)
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, 2 * b + x, d), pf[x], o[d], 0, 0, 0);
-      reads_ahead<2 * NB * DT, 2, D == 256 ? 1 : D == 128 ? 3 : 4>();
+      if constexpr (D >= 128) reads_ahead<2 * NB * DT, 2, D == 256 ? 1 : 3>();
     }
+  };
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();  // tile t has arrived; the tile before it is used up
+    uint8_t* kt = lds + (t & 1) * 2 * kBytes;
+    uint8_t* next = lds + (~t & 1) * 2 * kBytes;
+    if (careful && shared_cut(kbeg + t * kKeys)) {
+      v4i* v = reinterpret_cast<v4i*>(kt + kBytes);
+      for (int x = tid; x < kBytes / 16; x += 64 * kWaves) v[x] = finite_only(v[x]);
+      tile_barrier();
+    }
+    step(t, kt, next, kb, vb);
   }
 
   // A weight of 0 does not keep a V that is not finite out of a sum.  Where a row
@@ -229,7 +234,7 @@ again:
       for (int r = 0; r < 16; ++r) any = __builtin_fmaf(o[d][r], 0.0f, any);
     careful = __syncthreads_or(any != 0.0f);
     if (careful) {
-      if (tiles > 0) fetch(0);
+      if (tiles > 0) fetch(0, lds, kb, vb);
       goto again;
     }
   } else {
@@ -319,8 +324,12 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
     a.lse[at] = l == 0.0f ? -INFINITY : (m - kTop + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// How many workgroups share a row's keys: as many as fill the GPU, each with 512
-// keys or more of an average sequence.
+// How many workgroups share a row's keys: as many as the GPU runs at once, each with
+// 512 keys or more of an average sequence.  500 queries after 15,000 keys, 32 heads
+// of 128 and of 64: 159 and 96 us, and 163 and 99 with two workgroups to a CU only;
+// 16 heads of 256: 158, and 783 undivided.  From 256 keys on, 2 x 40 queries after
+// 4,000 take 32 us where they take 34, and 512 after 512 take 34 instead of 33; from
+// 1,024 on, 51 and 30.
 int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
   const int64_t groups = (Tq / rows(head_dim) + B) * heads, room = 256 * beside(head_dim);
   int64_t each = Tk / B;

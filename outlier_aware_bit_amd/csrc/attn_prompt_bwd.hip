@@ -151,13 +151,12 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   vl.init(a.ld_v, lane);
   Operand<D> op;
   op.init(lane);
-  auto fetch = [&](int t) {
-    uint8_t* to = lds + (t & 1) * 2 * kBytes;
+  auto fetch = [&](int t, uint8_t* to, const uint16_t* kb, const uint16_t* vb) {
     const int64_t at = kbeg + t * kStep;
     kl.load(kb + at * a.ld_k, a.ld_k, nk - static_cast<int>(at), to, wave);
     vl.load(vb + at * a.ld_v, a.ld_v, nk - static_cast<int>(at), to + kBytes, wave);
   };
-  if (tiles > 0) fetch(0);
+  if (tiles > 0) fetch(0, lds, kb, vb);
 
   const bool there = i < nq;
   const int64_t token = s.q0 + (there ? i : 0);
@@ -192,13 +191,13 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
   for (int r = 0; r < 16; ++r) less[r] = -delta;
   float power = 1.0f, ref = neg;  // of ds, the query's own; the exponent with it
   bool unset = true;
-  for (int t = 0; t < tiles; ++t) {
-    tile_barrier();
-    if (t + 1 < tiles) fetch(t + 1);
+  // Parameters apart from each other: see tile_barrier.
+  auto step = [&](int t, const uint8_t* __restrict__ kt, uint8_t* __restrict__ next, const uint16_t* __restrict__ kb,
+                  const uint16_t* __restrict__ vb) __attribute__((always_inline)) {
+    if (t + 1 < tiles) fetch(t + 1, next, kb, vb);
     const int k0 = kbeg + t * kStep;
-    if (k0 >= hi_last || k0 + kStep <= lo_first) continue;
+    if (k0 >= hi_last || k0 + kStep <= lo_first) return;
     const bool cut = k0 < lo_last || k0 + kStep > hi_first;
-    const uint8_t* kt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* vt = kt + kBytes;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -235,6 +234,10 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
           dq[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(kt, 2 * n + x, d), ds, dq[d], 0, 0, 0);
       }
     }
+  };
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();
+    step(t, lds + (t & 1) * 2 * kBytes, lds + (~t & 1) * 2 * kBytes, kb, vb);
   }
   const float f = a.scale * 0x1p-14f / power;
   store_rows<D>(dq, f, a.dq + (s.q0 + static_cast<int64_t>(i)) * a.ld_dq + head * D, half, there);
@@ -262,14 +265,15 @@ struct Queries {
   }
   __device__ __forceinline__ int first_query(int t) const { return begin + (per_head - 1 - t % per_head) * STEP; }
   // The next tile's rows, and kTop - lse and -delta of each.
-  __device__ __forceinline__ void fetch(const GradArgs& a, const Seq& s, uint8_t* q, uint8_t* dout, float (*stats)[64],
-                                        int wave, int lane) {
+  __device__ __forceinline__ void fetch(const GradArgs& a, const Seq& s, uint8_t* to, float (*stats)[64], const uint16_t* q,
+                                        const uint16_t* dout, const float* neg_lse, const float* minus_delta, int wave,
+                                        int lane) {
     const int64_t at = begin + next * STEP, token = s.q0 + at;
     const int rows = end - static_cast<int>(at);
-    ql.load(a.q + token * a.ld_q + head * D, a.ld_q, rows, q, wave);
-    dl.load(a.dout + token * a.ld_do + head * D, a.ld_do, rows, dout, wave);
+    ql.load(q + token * a.ld_q + head * D, a.ld_q, rows, to, wave);
+    dl.load(dout + token * a.ld_do + head * D, a.ld_do, rows, to + Tile<D>::rows(STEP), wave);
     if (wave < 2) {
-      const float* src = wave == 0 ? a.neg_lse : a.minus_delta;
+      const float* src = wave == 0 ? neg_lse : minus_delta;
       load64(src + static_cast<int64_t>(head) * a.s.Tq + token, rows < STEP ? rows : STEP, stats[wave], lane);
     }
     if (--next < 0) {
@@ -344,11 +348,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
   keys.init(by, j0, col);
   Queries<D, kStep, kWaves> queries;
   queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
-  auto fetch = [&](int t) {
-    uint8_t* to = lds + (t & 1) * 2 * kBytes;
-    queries.fetch(a, s, to, to + kBytes, stats[t & 1], wave, lane);
-  };
-  if (queries.tiles > 0) fetch(0);
+  if (queries.tiles > 0)
+    queries.fetch(a, s, lds, stats[0], a.q, a.dout, a.neg_lse, a.minus_delta, wave, lane);
   Operand<D> op;
   op.init(lane);
   const bool there = j < nk;
@@ -362,19 +363,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
   float power = 1.0f;  // of ds, the key's own
   bool unset = true;
 
-  for (int t = 0; t < queries.tiles; ++t) {
-    tile_barrier();
-    if (t + 1 < queries.tiles) fetch(t + 1);
+  auto step = [&](int t, const uint8_t* __restrict__ qt, const float (*__restrict__ now)[64], uint8_t* __restrict__ next,
+                  float (*__restrict__ next_stats)[64], const uint16_t* __restrict__ q, const uint16_t* __restrict__ dout,
+                  const float* __restrict__ neg_lse, const float* __restrict__ minus_delta) __attribute__((always_inline)) {
+    if (t + 1 < queries.tiles) queries.fetch(a, s, next, next_stats, q, dout, neg_lse, minus_delta, wave, lane);
     const int i0 = queries.first_query(t);
-    if (keys.skipped(i0, kStep)) continue;
+    if (keys.skipped(i0, kStep)) return;
     const bool cut = keys.cut(i0, kStep);
-    const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* dt = qt + kBytes;
     // (Both halves at once need three more registers than two waves a SIMD have use
     // for: 350 and 629 us on the two cases above.)
 #pragma unroll 1
     for (int n = 0; n < kStep / 32; ++n) {
-      v16f st = zeros(), dp = sixteen_rows(stats[t & 1][1], n, half);  // dP's products begin at -delta
+      v16f st = zeros(), dp = sixteen_rows(now[1], n, half);  // dP's products begin at -delta
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(qt, n, ks), kf[ks], st, 0, 0, 0);
@@ -383,7 +384,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
         dp = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), vf[ks], dp, 0, 0, 0);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const v4f neg = four_rows(stats[t & 1][0], n, g, half);
+        const v4f neg = four_rows(now[0], n, g, half);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * g + e;
@@ -419,6 +420,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
         }
       }
     }
+  };
+  for (int t = 0; t < queries.tiles; ++t) {
+    tile_barrier();
+    step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
+         a.minus_delta);
   }
   const int64_t row = s.k0 + static_cast<int64_t>(j);
   store_rows<D>(dk, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
@@ -460,11 +466,8 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   keys.init(by, j0, col);
   Queries<D, kStep, 2 * kPairs> queries;
   queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
-  auto fetch = [&](int t) {
-    uint8_t* to = lds + (t & 1) * 2 * kBytes;
-    queries.fetch(a, s, to, to + kBytes, stats[t & 1], wave, lane);
-  };
-  if (queries.tiles > 0) fetch(0);
+  if (queries.tiles > 0)
+    queries.fetch(a, s, lds, stats[0], a.q, a.dout, a.neg_lse, a.minus_delta, wave, lane);
   Operand<D> op;
   op.init(lane);
   const bool there = j < nk;
@@ -477,12 +480,12 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   const int64_t row = s.k0 + static_cast<int64_t>(j);
 
   if (!second) {
-    for (int t = 0; t < queries.tiles; ++t) {
-      tile_barrier();
-      if (t + 1 < queries.tiles) fetch(t + 1);
+    auto step = [&](int t, const uint8_t* __restrict__ qt, const float (*__restrict__ now)[64], uint8_t* __restrict__ next,
+                    float (*__restrict__ next_stats)[64], const uint16_t* __restrict__ q, const uint16_t* __restrict__ dout,
+                    const float* __restrict__ neg_lse, const float* __restrict__ minus_delta) __attribute__((always_inline)) {
+      if (t + 1 < queries.tiles) queries.fetch(a, s, next, next_stats, q, dout, neg_lse, minus_delta, wave, lane);
       const int i0 = queries.first_query(t);
       const bool skip = keys.skipped(i0, kStep);
-      const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
       const uint8_t* dt = qt + kBytes;
       v8h p8[NB][2];
       if (!skip) {
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const v4f neg = four_rows(stats[t & 1][0], n, g, half);
+            const v4f neg = four_rows(now[0], n, g, half);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               st[n][4 * g + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][4 * g + e], a.c, neg[e]));
@@ -519,7 +522,7 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
         }
       }
       lds_barrier();  // P has arrived
-      if (skip) continue;
+      if (skip) return;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -527,6 +530,11 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
 #pragma unroll
           for (int d = 0; d < DT; ++d)
             sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8[n][x], sum[d], 0, 0, 0);
+    };
+    for (int t = 0; t < queries.tiles; ++t) {
+      tile_barrier();
+      step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
+           a.minus_delta);
     }
     store_rows<D>(sum, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
     return;
@@ -534,25 +542,25 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
 
   float power = 1.0f;  // of ds, the key's own
   bool unset = true;
-  for (int t = 0; t < queries.tiles; ++t) {
-    tile_barrier();
-    if (t + 1 < queries.tiles) fetch(t + 1);
+  auto step = [&](int t, const uint8_t* __restrict__ qt, const float (*__restrict__ now)[64], uint8_t* __restrict__ next,
+                  float (*__restrict__ next_stats)[64], const uint16_t* __restrict__ q, const uint16_t* __restrict__ dout,
+                  const float* __restrict__ neg_lse, const float* __restrict__ minus_delta) __attribute__((always_inline)) {
+    if (t + 1 < queries.tiles) queries.fetch(a, s, next, next_stats, q, dout, neg_lse, minus_delta, wave, lane);
     const int i0 = queries.first_query(t);
     const bool skip = keys.skipped(i0, kStep);
-    const uint8_t* qt = lds + (t & 1) * 2 * kBytes;
     const uint8_t* dt = qt + kBytes;
     v16f dp[NB];
     if (!skip) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        dp[n] = sixteen_rows(stats[t & 1][1], n, half);  // its products begin at -delta
+        dp[n] = sixteen_rows(now[1], n, half);  // its products begin at -delta
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
           dp[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(dt, n, ks), own[ks], dp[n], 0, 0, 0);
       }
     }
     lds_barrier();  // P has arrived
-    if (skip) continue;
+    if (skip) return;
     float top = 0.0f;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
@@ -583,6 +591,11 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
         for (int d = 0; d < DT; ++d)
           sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), ds, sum[d], 0, 0, 0);
       }
+  };
+  for (int t = 0; t < queries.tiles; ++t) {
+    tile_barrier();
+    step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
+         a.minus_delta);
   }
   store_rows<D>(sum, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
 }
