@@ -63,7 +63,7 @@ __device__ __forceinline__ v4i finite_only(v4i x) {
 template <int D>
 __global__ __launch_bounds__(64 * waves(D), waves_a_simd(D)) void prompt_kernel(PromptArgs a) {
   constexpr int KS = D / 16, DT = D / 32, kWaves = waves(D), kRows = rows(D);
-  constexpr int kKeys = keys(D), NB = D == 64 ? 2 : 1;  // of a tile; blocks of 32 at a time
+  constexpr int kKeys = keys(D);  // of a tile, 32 at a time
   constexpr int kBytes = Tile<D>::rows(kKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes];  // two tiles of K, two of V
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,34 +149,27 @@ again:
     if (skipped(k0)) return;
     const uint8_t* vt = kt + kBytes;
 #pragma unroll 1
-    for (int b = 0; b < kKeys / 32; b += NB) {
-      v16f st[NB];
+    for (int b = 0; b < kKeys / 32; ++b) {
+      v16f st;
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int r = 0; r < 16; ++r) st[r] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) st[n][r] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          st[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, b + n, ks), qf[ks], st[n], 0, 0, 0);
-      }
+      for (int ks = 0; ks < KS; ++ks)
+        st = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.rows(kt, b, ks), qf[ks], st, 0, 0, 0);
       if constexpr (D >= 128) {
-        reads_ahead<NB * KS, 1, D == 256 ? 2 : 4>();
+        reads_ahead<KS, 1, D == 256 ? 2 : 4>();
         __builtin_amdgcn_sched_barrier(0);
       }
       if (cut(k0)) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const uint32_t j = k0 + 32 * (b + n) + frag_row(r, lane) - lo;
-            st[n][r] = j < span ? st[n][r] : -INFINITY;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const uint32_t j = k0 + 32 * b + frag_row(r, lane) - lo;
+          st[r] = j < span ? st[r] : -INFINITY;
+        }
       }
-      float top = st[0][0];
+      float top = st[0];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, st[n][r]);
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, st[r]);
       top = larger_half(top) * a.c;
       if (__any(top > m + kSlack)) {
         // Each query by itself: its bits do not depend on its neighbours'.
@@ -189,25 +182,20 @@ again:
           for (int r = 0; r < 16; ++r) o[d][r] *= f;
       }
       const float ref = kTop - m;
-      v8h pf[2 * NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          st[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][r], a.c, ref));
-          l += st[n][r];
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          pf[2 * n + x] = pack8(st[n][8 * x], st[n][8 * x + 1], st[n][8 * x + 2], st[n][8 * x + 3], st[n][8 * x + 4],
-                                st[n][8 * x + 5], st[n][8 * x + 6], st[n][8 * x + 7]);
+      for (int r = 0; r < 16; ++r) {
+        st[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[r], a.c, ref));
+        l += st[r];
       }
 #pragma unroll
-      for (int x = 0; x < 2 * NB; ++x)
+      for (int x = 0; x < 2; ++x) {
+        const v8h p = pack8(st[8 * x], st[8 * x + 1], st[8 * x + 2], st[8 * x + 3], st[8 * x + 4], st[8 * x + 5],
+                            st[8 * x + 6], st[8 * x + 7]);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, 2 * b + x, d), pf[x], o[d], 0, 0, 0);
-      if constexpr (D >= 128) reads_ahead<2 * NB * DT, 2, D == 256 ? 1 : 3>();
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(vt, 2 * b + x, d), p, o[d], 0, 0, 0);
+      }
+      if constexpr (D >= 128) reads_ahead<2 * DT, 2, D == 256 ? 1 : 3>();
     }
   };
   for (int t = 0; t < tiles; ++t) {
