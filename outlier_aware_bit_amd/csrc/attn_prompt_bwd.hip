@@ -371,8 +371,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
     if (keys.skipped(i0, kStep)) return;
     const bool cut = keys.cut(i0, kStep);
     const uint8_t* dt = qt + kBytes;
-    // (Both halves at once need three more registers than two waves a SIMD have use
-    // for: 350 and 629 us on the two cases above.)
+    // (Both halves at once take 228 registers, for two waves a SIMD instead of three:
+    // 328 us where this takes 346, and 638 where it takes 628, on the cases above.)
 #pragma unroll 1
     for (int n = 0; n < kStep / 32; ++n) {
       v16f st = zeros(), dp = sixteen_rows(now[1], n, half);  // dP's products begin at -delta
@@ -480,6 +480,9 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   const int64_t row = s.k0 + static_cast<int64_t>(j);
 
   if (!second) {
+    // The other waits for its P.  (Four sequences of 2,048 with 128 channels, dq too,
+    // 516 us instead of 532; of 1,024 with 256, 308 and 325.)
+    __builtin_amdgcn_s_setprio(1);
     auto step = [&](int t, const uint8_t* __restrict__ qt, const float (*__restrict__ now)[64], uint8_t* __restrict__ next,
                     float (*__restrict__ next_stats)[64], const uint16_t* __restrict__ q, const uint16_t* __restrict__ dout,
                     const float* __restrict__ neg_lse, const float* __restrict__ minus_delta) __attribute__((always_inline)) {
