@@ -748,6 +748,7 @@ qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads, const uint
  *   cu_q, cu_k  int32 [B + 1] (device), not decreasing; may be one array.  B at
  *             most 65535, tokens at most 2^30, (T / 128 + B) * heads below 2^23.
  *             Borders past Tq or Tk are taken to be there
+ *   scale     from -2^40 to 2^40
  *   causal    0 or not;  window  0 (none), or with causal the keys a query sees
  *   out       fp16 [Tq x heads x head_dim], contiguous, not an input; rows of no
  *             sequence are left as they were
@@ -776,7 +777,7 @@ size_t qlin_attn_prompt_work_bytes(int32_t heads, int32_t kv_heads, int32_t head
  * and ds enter their products as fp16, to 2^-11 of themselves, ds times a power
  * of two that follows its size (2^-25 of the largest of the row, for dk of the
  * rows before, is still a normal number), so gradients of any size keep their
- * bits.  A key that no query sees, and a query that sees no key, has zeros.  A
+ * bits; p is made again from lse, to 2^-23 |lse| of itself.  A key that no query sees, and a query that sees no key, has zeros.  A
  * value that is not finite makes its own sequence's gradients so, wherever it
  * stands there, and no other's.  The same call gives the same bits.
  *   dout      fp16 [Tq x heads x head_dim], ld_dout elements between tokens; the

@@ -324,15 +324,17 @@ inline bool prompt_shape_ok(int32_t heads, int32_t kv_heads, int32_t head_dim, i
     QLIN_REQUIRE(::qlin::prompt_sizes_ok((heads), (B), (Tq), (Tk)), QLIN_ERR_SHAPE,                            \
                  "B=%lld, Tq=%lld, Tk=%lld: at most 65535 sequences and 2^30 tokens, (T / 128 + B) * heads below 2^23",        \
                  (long long)(B), (long long)(Tq), (long long)(Tk));                                            \
-    QLIN_REQUIRE((scale) - (scale) == 0.0f, QLIN_ERR_INVALID_ARG, "scale is not finite");                      \
+    QLIN_REQUIRE((scale) >= -0x1p40f && (scale) <= 0x1p40f, QLIN_ERR_INVALID_ARG,                              \
+                 "scale=%g: from -2^40 to 2^40", static_cast<double>(scale));                                  \
     QLIN_REQUIRE((window) >= 0 && ((window) == 0 || (causal)), QLIN_ERR_INVALID_ARG,                           \
                  "window=%d: not negative, and for causal attention only", (window));                          \
     QLIN_DIMS(Tq, static_cast<int64_t>(heads) * (head_dim));                                                   \
     QLIN_DIMS(Tk, static_cast<int64_t>(kv_heads) * (head_dim));                                                \
   } while (0)
 
-// |scale| log2(e); never 0, so that a hidden key's -inf stays what it is (logits
-// are below 2^41: this makes them nothing).
+// |scale| log2(e); never 0, so that a hidden key's -inf stays what it is (products
+// of q and k are at most 2^40: this makes them nothing; and with the largest scale
+// logits stay far from the end of fp32).
 inline float prompt_scale(float scale) {
   const float c = (scale < 0.0f ? -scale : scale) * kLog2e;
   return c > 1.0e-30f ? c : 1.0e-30f;

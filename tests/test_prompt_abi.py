@@ -61,6 +61,7 @@ BOTH = [(dict(D=96), U), (dict(D=32), U), (dict(heads=3), S), (dict(heads=0), S)
         (dict(kv_heads=-2, heads=-4), S), (dict(heads=131072, kv_heads=1), S), (dict(B=-1), I), (dict(Tq=-1), I),
         (dict(Tk=-1), I), (dict(B=65536), S), (dict(Tq=(1 << 30) + 1), S), (dict(Tk=1 << 31), S),
         (dict(Tq=1 << 30, heads=128, ld_q=16384), S), (dict(B=65535, heads=130, ld_q=16640), S), (dict(scale=float("nan")), I), (dict(scale=float("inf")), I),
+        (dict(scale=2.0 ** 41), I), (dict(scale=-2.0 ** 41), I),
         (dict(window=-1), I), (dict(window=5, causal=0), I), (dict(ld_q=504), S), (dict(ld_q=516), S),
         (dict(ld_k=0), S), (dict(ld_v=260), S), (dict(ld_v=(1 << 22) + 8), S), (dict(q=None), I), (dict(k=None), I),
         (dict(v=MIS), AL), (dict(out=None), I), (dict(out=MIS), AL), (dict(cu_q=None), I), (dict(cu_k=MIS), AL),
