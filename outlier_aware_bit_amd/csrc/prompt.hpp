@@ -254,7 +254,8 @@ struct Operand {
 // The order of the products before it in their block, and of the reads from LDS
 // that feed them, EACH to a product: reads go AHEAD products before their own.
 // Left to itself the compiler reuses a few registers, and a wave waits for LDS
-// before every few products.
+// before every few products: 4 x 2,048 tokens, forward, 164 us where this takes 159
+// with 128 channels, 158 and 154 with 256, no difference with 64.
 template <int PRODUCTS, int EACH, int AHEAD>
 __device__ __forceinline__ void reads_ahead() {
   constexpr int kReads = 0x100, kProducts = 0x008;
