@@ -718,7 +718,8 @@ qlin_status qlin_rope_freqs(int32_t rot_dim, double base, int32_t scaling, doubl
  *   freq      float64 [rot_dim / 2] (qlin_rope_freqs, or any other)
  *   inverse   non-zero: by -a, which with the same amplitude is the backward pass
  *   q_out, k_out  fp16, ld_qo and ld_ko elements between tokens; each either its
- *             input (then with the same stride) or apart from both inputs
+ *             input (then with the same stride) or apart from both inputs; not
+ *             one array
  */
 qlin_status qlin_rope(const uint16_t* q, int64_t ld_q, int32_t heads, const uint16_t* k, int64_t ld_k,
                       int32_t kv_heads, int64_t T, int32_t head_dim, int32_t rot_dim,

@@ -52,7 +52,8 @@ def pages(want=A, B=2, max_pages=4, page=16, table=A, held=2 * A, ring=A, n=8, s
     (dict(amplitude=float("nan")), I), (dict(k=None), I), (dict(k_out=None), I), (dict(kv_heads=0), I),
     (dict(q_out=A, ld_qo=520), S), (dict(k_out=A, ld_ko=264), S), (dict(q=None), I), (dict(q_out=None), I),
     (dict(position=None), I), (dict(freq=None), I), (dict(q=MIS), AL), (dict(k_out=MIS), AL), (dict(position=MIS), AL),
-    (dict(freq=MIS), AL), (dict(T=0, q=None, q_out=None), OK)])
+    (dict(freq=MIS), AL), (dict(T=0, q=None, q_out=None), OK), (dict(q=3 * A, q_out=A, k_out=4 * A), I),
+    (dict(k=3 * A, k_out=A), I), (dict(k=3 * A), I)])
 def test_rope(kw, status):
     assert rope(**kw) == status, _lib.load().qlin_last_error()
 
