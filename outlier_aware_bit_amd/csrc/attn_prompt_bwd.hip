@@ -380,9 +380,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
     if (keys.skipped(i0, kStep)) return;
     const bool cut = keys.cut(i0, kStep);
     const uint8_t* dt = qt + kBytes;
-    // (Both halves at once take 228 registers, for two waves a SIMD instead of three:
-    // 328 us where this takes 346, and 638 where it takes 628, on the cases above.)
-#pragma unroll 1
+    // Both halves at once: 228 registers and two waves a SIMD, where 165 would let
+    // three run, but the one's products go beside the other's exponentials.  339 us on
+    // the first of the cases above, and 355 with one half at a time; one sequence of
+    // 8,192 with 16 heads 647 and 677; the twelve texts 662 and 652, without a window
+    // 880 and 893.
+#pragma unroll
     for (int n = 0; n < kStep / 32; ++n) {
       v16f st = zeros(), dp = sixteen_rows(now[1], n, half);  // dP's products begin at -delta
 #pragma unroll
