@@ -788,10 +788,10 @@ size_t qlin_attn_prompt_work_bytes(int32_t heads, int32_t kv_heads, int32_t head
  *   dq, dk, dv  fp16, shaped as q, k and v, ld_dq, ld_dk and ld_dv elements
  *             between tokens (slices of one gradient of the projection will do, but
  *             no inputs); rows of no sequence are left as they were
- *   work      device workspace of qlin_attn_prompt_backward_work_bytes(heads, Tq)
- *             bytes, 16-byte aligned; its contents on entry do not matter.  Calls
- *             that overlap must not share it.
- * Two launches.
+ *   work      device workspace of qlin_attn_prompt_backward_work_bytes(..) bytes,
+ *             16-byte aligned; its contents on entry do not matter.  Calls that
+ *             overlap must not share it.
+ * Two launches, and a third where few workgroups would have all queries of a key.
  */
 qlin_status qlin_attn_prompt_backward(
     const uint16_t* dout, int64_t ld_dout, const uint16_t* q, int64_t ld_q, int32_t heads,
@@ -802,7 +802,9 @@ qlin_status qlin_attn_prompt_backward(
     int64_t ld_dv, void* work, void* stream);
 
 /* Bytes of the qlin_attn_prompt_backward workspace (0 for invalid arguments). Host only. */
-size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int64_t Tq);
+size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                            int64_t B, int64_t Tq, int64_t Tk, int32_t causal,
+                                            int32_t window);
 
 #ifdef __cplusplus
 }

@@ -61,7 +61,7 @@ SIGNATURES = {
     "qlin_attn_prompt_work_bytes": (C.c_size_t, [i32, i32, i32, i64, i64, i64, i32, i32]),
     "qlin_attn_prompt_backward": (i32, [p, i64, p, i64, i32, p, i64, p, i64, i32, i32, p, p, p, p, i64, i64, i64, f32,
                                         i32, i32, p, i64, p, i64, p, i64, p, p]),
-    "qlin_attn_prompt_backward_work_bytes": (C.c_size_t, [i32, i64]),
+    "qlin_attn_prompt_backward_work_bytes": (C.c_size_t, [i32, i32, i32, i64, i64, i64, i32, i32]),
     "qlin_quaff_backward": (i32, [p, i64, i64, i64, p, p, p, p, p, i32, p, p, p, p, p, p, p]),
 }
 

@@ -344,7 +344,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
 int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
   const int64_t groups = (Tq / rows(head_dim) + B) * heads, room = 256 * beside(head_dim);
   int64_t each = Tk / B;
-  if (window > 0 && window + rows(head_dim) < each) each = window + rows(head_dim);
+  if (window > 0 && int64_t{window} + rows(head_dim) < each) each = window + rows(head_dim);
   int64_t n = room / groups;
   if (n > each / 512) n = each / 512;
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);

@@ -47,6 +47,8 @@ struct GradArgs {
   int64_t ld_dq, ld_dk, ld_dv;
   float* neg_lse;      // [heads x Tq]: kTop - lse log2(e)
   float* minus_delta;  // [heads x Tq]
+  int32_t splits;  // workgroups that share a key tile's queries
+  float* parts;    // [splits x 2 x Tk x kv_heads x D], with splits > 1: dk's and dv's
 };
 
 constexpr int kStep = 64;  // keys of a tile
@@ -127,6 +129,18 @@ __device__ __forceinline__ void store_rows(const v16f (&x)[D / 32], float f, uin
       const v4i w = {static_cast<int>(y[0]), static_cast<int>(z[0]), static_cast<int>(y[1]), static_cast<int>(z[1])};
       if (there) *reinterpret_cast<v4i*>(row + 32 * d + 8 * g + 8 * half) = w;
     }
+}
+
+// The same in fp32.
+template <int D>
+__device__ __forceinline__ void store_part(const v16f (&x)[D / 32], float f, float* row, int half, bool there) {
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (there)
+        *reinterpret_cast<float4*>(row + 32 * d + 8 * g + 4 * half) =
+            make_float4(x[d][4 * g] * f, x[d][4 * g + 1] * f, x[d][4 * g + 2] * f, x[d][4 * g + 3] * f);
 }
 
 // (Tiles of 32 keys cost 2 - 4 % with 128 channels; reads ordered ahead of their
@@ -259,18 +273,26 @@ __global__ __launch_bounds__(64 * kWaves, beside(D)) void prompt_dq_kernel(GradA
 template <int D, int STEP, int WAVES>
 struct Queries {
   TileLoad<D, STEP, WAVES> ql, dl;
-  int begin, end, per_head, tiles;
-  int head, next;  // of the next tile to fetch
+  int begin, end, per_head;
+  int from, tiles;  // the workgroup's own: tiles [from, tiles) of all heads'
+  int head, next;   // of the next tile to fetch
 
-  __device__ __forceinline__ void init(const GradArgs& a, int kvh, int first, int last, int nq, int lane) {
+  __device__ __forceinline__ void init(const GradArgs& a, int kvh, int first, int last, int nq, int split, int lane) {
     ql.init(a.ld_q, lane);
     dl.init(a.ld_do, lane);
     begin = first;
     end = nq;
     per_head = last > first ? (last - first + STEP - 1) / STEP : 0;
+    from = 0;
     tiles = per_head * a.group;
     head = kvh * a.group;
     next = per_head - 1;
+    if (a.splits > 1 && tiles > 0) {
+      from = static_cast<int>(static_cast<int64_t>(tiles) * split / a.splits);
+      tiles = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / a.splits);
+      head += from / per_head;
+      next -= from % per_head;
+    }
   }
   __device__ __forceinline__ int first_query(int t) const { return begin + (per_head - 1 - t % per_head) * STEP; }
   // The next tile's rows, and kTop - lse and -delta of each.
@@ -334,6 +356,12 @@ __device__ __forceinline__ v16f sixteen_rows(const float* stats, int n, int half
   return x;
 }
 
+// A key's place in its workgroup's part of dk (0) or dv (1).
+__device__ __forceinline__ float* part_row(const GradArgs& a, int which, int64_t row, int kvh, int D) {
+  const int64_t width = static_cast<int64_t>(a.heads / a.group) * D;
+  return a.parts + ((static_cast<int64_t>(blockIdx.y) * 2 + which) * a.s.Tk + row) * width + kvh * D;
+}
+
 // 64 channels: a wave makes P, dV, dS and dK of its 32 keys.  (In pairs, as below,
 // four sequences of 2,048 take 350 us where this takes 333, twelve texts of 60 -
 // 3,001 in a window of 1,000 take 690 where this takes 644, dq in both.)
@@ -356,9 +384,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
   KeyRange keys;
   keys.init(by, j0, col);
   Queries<D, kStep, kWaves> queries;
-  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
-  if (queries.tiles > 0)
-    queries.fetch(a, s, lds, stats[0], a.q, a.dout, a.neg_lse, a.minus_delta, wave, lane);
+  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, blockIdx.y, lane);
+  if (queries.from < queries.tiles)
+    queries.fetch(a, s, lds + (queries.from & 1) * 2 * kBytes, stats[queries.from & 1], a.q, a.dout, a.neg_lse,
+                  a.minus_delta, wave, lane);
   Operand<D> op;
   op.init(lane);
   const bool there = j < nk;
@@ -433,12 +462,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv64_kernel(GradArgs a
       }
     }
   };
-  for (int t = 0; t < queries.tiles; ++t) {
+  for (int t = queries.from; t < queries.tiles; ++t) {
     tile_barrier();
     step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
          a.minus_delta);
   }
   const int64_t row = s.k0 + static_cast<int64_t>(j);
+  if (a.splits > 1) {
+    store_part<D>(dk, a.scale * 0x1p-14f / power, part_row(a, 0, row, kvh, D), half, there);
+    store_part<D>(dv, 0x1p-14f, part_row(a, 1, row, kvh, D), half, there);
+    return;
+  }
   store_rows<D>(dk, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
   store_rows<D>(dv, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
 }
@@ -477,9 +511,10 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
   KeyRange keys;
   keys.init(by, j0, col);
   Queries<D, kStep, 2 * kPairs> queries;
-  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, lane);
-  if (queries.tiles > 0)
-    queries.fetch(a, s, lds, stats[0], a.q, a.dout, a.neg_lse, a.minus_delta, wave, lane);
+  queries.init(a, kvh, by.first(row0), by.last(row0 + kRows - 1), nq, blockIdx.y, lane);
+  if (queries.from < queries.tiles)
+    queries.fetch(a, s, lds + (queries.from & 1) * 2 * kBytes, stats[queries.from & 1], a.q, a.dout, a.neg_lse,
+                  a.minus_delta, wave, lane);
   Operand<D> op;
   op.init(lane);
   const bool there = j < nk;
@@ -546,12 +581,15 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
           for (int d = 0; d < DT; ++d)
             sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(dt, 2 * n + x, d), p8[n][x], sum[d], 0, 0, 0);
     };
-    for (int t = 0; t < queries.tiles; ++t) {
+    for (int t = queries.from; t < queries.tiles; ++t) {
       tile_barrier();
       step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
            a.minus_delta);
     }
-    store_rows<D>(sum, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
+    if (a.splits > 1)
+      store_part<D>(sum, 0x1p-14f, part_row(a, 1, row, kvh, D), half, there);
+    else
+      store_rows<D>(sum, 0x1p-14f, a.dv + row * a.ld_dv + kvh * D, half, there);
     return;
   }
 
@@ -607,12 +645,57 @@ __global__ __launch_bounds__(128 * kPairs, 2) void prompt_dkv_kernel(GradArgs a)
           sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op.columns(qt, 2 * n + x, d), ds, sum[d], 0, 0, 0);
       }
   };
-  for (int t = 0; t < queries.tiles; ++t) {
+  for (int t = queries.from; t < queries.tiles; ++t) {
     tile_barrier();
     step(t, lds + (t & 1) * 2 * kBytes, stats[t & 1], lds + (~t & 1) * 2 * kBytes, stats[~t & 1], a.q, a.dout, a.neg_lse,
          a.minus_delta);
   }
-  store_rows<D>(sum, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
+  if (a.splits > 1)
+    store_part<D>(sum, a.scale * 0x1p-14f / power, part_row(a, 0, row, kvh, D), half, there);
+  else
+    store_rows<D>(sum, a.scale * 0x1p-14f / power, a.dk + row * a.ld_dk + kvh * D, half, there);
+}
+
+// The parts of keys whose queries were divided, in their order: each thread joins
+// eight channels of a key's dk and dv.
+__global__ __launch_bounds__(256) void prompt_grad_join_kernel(GradArgs a, int32_t d_shift) {
+  const int32_t kv_heads = a.heads / a.group;
+  const int64_t width = static_cast<int64_t>(kv_heads) << d_shift, all = a.s.Tk * width;
+  const int64_t at = 8 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
+  if (at >= all) return;
+  const int64_t row = at / width, c = at - row * width;
+  // Rows of no sequence have no parts, and are left as they are.
+  if (row < a.s.cu_k[0] || row >= a.s.cu_k[a.s.B]) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float x[8] = {};
+    for (int y = 0; y < a.splits; ++y) {
+      const float* p = a.parts + (2 * y + which) * all + at;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += p[i];
+    }
+    const v4i w = {static_cast<int>(pack_half(x[0], x[1])), static_cast<int>(pack_half(x[2], x[3])),
+                   static_cast<int>(pack_half(x[4], x[5])), static_cast<int>(pack_half(x[6], x[7]))};
+    *reinterpret_cast<v4i*>((which == 0 ? a.dk + row * a.ld_dk : a.dv + row * a.ld_dv) + c) = w;
+  }
+}
+
+// How many workgroups share a key tile's queries: as many as the GPU runs at once,
+// each with kLeast tiles of 64 queries or more of an average sequence.
+constexpr int kLeast = 4;
+int grad_splits(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t causal,
+                int32_t window) {
+  if (Tk == 0 || B == 0) return 1;
+  const int64_t groups = (Tk / kRows + B) * kv_heads, room = 256 * (head_dim == 64 ? 2 : 1);
+  int64_t each = Tq / B;  // queries of a key tile
+  if (window > 0 && int64_t{window} + kRows < each)
+    each = window + kRows;
+  else if (causal)
+    each = (each + 1) / 2;
+  const int64_t most = each * (heads / kv_heads) / (64 * kLeast);
+  int64_t n = room / groups;
+  if (n > most) n = most;
+  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
 template <int D>
@@ -624,17 +707,26 @@ qlin_status launch(const GradArgs& a, hipStream_t st) {
   }
   if (a.s.Tk > 0) {
     const int64_t wgs = (a.s.Tk / kRows + a.s.B) * (a.heads / a.group);
+    const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(a.splits));
     if constexpr (D == 64)
-      prompt_dkv64_kernel<<<static_cast<unsigned>(wgs), 64 * kWaves, 0, st>>>(a);
+      prompt_dkv64_kernel<<<grid, 64 * kWaves, 0, st>>>(a);
     else
-      prompt_dkv_kernel<D><<<static_cast<unsigned>(wgs), 128 * kPairs, 0, st>>>(a);
+      prompt_dkv_kernel<D><<<grid, 128 * kPairs, 0, st>>>(a);
     QLIN_LAUNCH_CHECK("prompt_dkv_kernel");
+    if (a.splits > 1) {
+      const int64_t threads = a.s.Tk * (a.heads / a.group) * (D / 8);
+      prompt_grad_join_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a, D == 64 ? 6 : D == 128 ? 7 : 8);
+      QLIN_LAUNCH_CHECK("prompt_grad_join_kernel");
+    }
   }
   return QLIN_OK;
 }
 
-size_t grad_work(int32_t heads, int64_t Tq) {  // two arrays, each a multiple of 16 bytes
-  return 2 * ((static_cast<size_t>(heads) * Tq * 4 + 15) / 16 * 16);
+// Two arrays of statistics, each a multiple of 16 bytes, and the parts.
+size_t stats_bytes(int32_t heads, int64_t Tq) { return (static_cast<size_t>(heads) * Tq * 4 + 15) / 16 * 16; }
+size_t grad_work(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t Tq, int64_t Tk, int splits) {
+  const size_t part = static_cast<size_t>(Tk) * kv_heads * head_dim * 8;
+  return 2 * stats_bytes(heads, Tq) + (splits > 1 ? splits * part : 0);
 }
 
 }  // namespace
@@ -663,7 +755,6 @@ extern "C" qlin_status qlin_attn_prompt_backward(
     QLIN_PTR(out);
     QLIN_PTR(lse);
     QLIN_PTR(dq);
-    QLIN_PTR(work);
   }
   if (Tk > 0) {
     QLIN_PTR(k);
@@ -671,6 +762,8 @@ extern "C" qlin_status qlin_attn_prompt_backward(
     QLIN_PTR(dk);
     QLIN_PTR(dv);
   }
+  const int splits = grad_splits(heads, kv_heads, head_dim, B, Tq, Tk, causal, window);
+  if (Tq > 0) QLIN_PTR(work);
   QLIN_PTR(cu_q);
   QLIN_PTR(cu_k);
   for (const uint16_t* g : {dq, dk, dv})
@@ -686,11 +779,15 @@ extern "C" qlin_status qlin_attn_prompt_backward(
   a.c = scale * kLog2e, a.scale = scale, a.causal = causal, a.window = prompt_window(window);
   a.dq = dq, a.dk = dk, a.dv = dv, a.ld_dq = ld_dq, a.ld_dk = ld_dk, a.ld_dv = ld_dv;
   a.neg_lse = static_cast<float*>(work);
-  a.minus_delta = a.neg_lse + grad_work(heads, Tq) / 8;
+  a.minus_delta = a.neg_lse + stats_bytes(heads, Tq) / 4;
+  a.splits = splits;
+  a.parts = a.minus_delta + stats_bytes(heads, Tq) / 4;
   hipStream_t st = as_stream(stream);
   return head_dim == 64 ? launch<64>(a, st) : head_dim == 128 ? launch<128>(a, st) : launch<256>(a, st);
 }
 
-extern "C" size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int64_t Tq) {
-  return heads < 1 || heads > 65535 || Tq < 0 || Tq >= kMaxDim ? 0 : grad_work(heads, Tq);
+extern "C" size_t qlin_attn_prompt_backward_work_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B,
+                                                       int64_t Tq, int64_t Tk, int32_t causal, int32_t window) {
+  if (!prompt_shape_ok(heads, kv_heads, head_dim, B, Tq, Tk, causal, window) || B == 0 || (Tq == 0 && Tk == 0)) return 0;
+  return grad_work(heads, kv_heads, head_dim, Tq, Tk, grad_splits(heads, kv_heads, head_dim, B, Tq, Tk, causal, window));
 }

@@ -962,8 +962,15 @@ def qlin_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0
     return out, lse
 
 
-def qlin_attn_prompt_backward_work_bytes(heads, Tq) -> int:
-    return int(_lib.load().qlin_attn_prompt_backward_work_bytes(heads, Tq))
+def qlin_attn_prompt_backward_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, causal=True, window=0) -> int:
+    return int(_lib.load().qlin_attn_prompt_backward_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, int(causal),
+                                                                window))
+
+
+@functools.lru_cache(maxsize=4096)
+def _grad_need(*sizes):
+    """As _prompt_need, for the gradients."""
+    return _lib.load().qlin_attn_prompt_backward_work_bytes(*sizes)
 
 
 def _grad(t, name, like, D, index):
@@ -978,8 +985,8 @@ def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=No
     """Gradients (dq, dk, dv) of qlin_attn_prompt's out, from dout, shaped like it
     (tokens any multiple of 8 elements apart), and that call's inputs and results.
     dq, dk and dv may be slices of one tensor.  work: a uint8 workspace of
-    qlin_attn_prompt_backward_work_bytes(heads, Tq) bytes, or None to allocate
-    one.  Rows of no sequence are left as they were."""
+    qlin_attn_prompt_backward_work_bytes(..) bytes, or None to allocate one.
+    Rows of no sequence are left as they were."""
     lib, index = _lib.load(), _gpu_of(q, "q")
     Tq, heads, ld_q, Tk, kv_heads, ld_k, ld_v, D = _prompt_rows(q, k, v, index)
     B, cu_q_p, cu_k_p = _borders(cu_q, cu_k, index)
@@ -994,10 +1001,11 @@ def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=No
         return dq, dk, dv
     if scale is None:
         scale = D ** -0.5
-    work = _space(work, lib.qlin_attn_prompt_backward_work_bytes(heads, Tq), index, q)
+    causal = bool(causal)
+    work = _space(work, _grad_need(heads, kv_heads, D, B, Tq, Tk, causal, window), index, q)
     st = lib.qlin_attn_prompt_backward(dout.data_ptr(), ld_do, q.data_ptr(), ld_q, heads, k.data_ptr(), ld_k,
                                        v.data_ptr(), ld_v, kv_heads, D, out_p, lse_p, cu_q_p, cu_k_p, B, Tq, Tk, scale,
-                                       int(causal), window, dq.data_ptr(), ld_dq, dk.data_ptr(), ld_dk, dv.data_ptr(),
+                                       causal, window, dq.data_ptr(), ld_dq, dk.data_ptr(), ld_dk, dv.data_ptr(),
                                        ld_dv, _ptr(work), _raw_stream_of(index))
     if st:
         _lib.check("qlin_attn_prompt_backward", st)

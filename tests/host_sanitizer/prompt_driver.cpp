@@ -59,7 +59,7 @@ struct Prompt {
     refused(what, x, backward());
     g_calls += 1;
     (void)qlin_attn_prompt_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, causal, window);
-    (void)qlin_attn_prompt_backward_work_bytes(heads, Tq);
+    (void)qlin_attn_prompt_backward_work_bytes(heads, kv_heads, head_dim, B, Tq, Tk, causal, window);
   }
 };
 

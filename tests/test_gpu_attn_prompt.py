@@ -4,6 +4,7 @@ finite in places that a row does not see, gradients of every size, and that the
 same call gives the same bits."""
 import numpy as np
 import pytest
+import torch
 
 from tests.gpu_helpers import dev, host, log
 from tests.prompt_helpers import Packed, strided, within
@@ -57,6 +58,32 @@ def test_backward(n):
     want, tol = c.backward()
     for name, g, w, t in zip(("dq", "dk", "dv"), got, want, tol):
         within(host(g), w, t, name)
+
+
+@pytest.mark.parametrize("heads,kv,D,nq,nk,causal,window", [
+    (8, 1, 64, [700], [700], True, 0), (8, 1, 128, [600, 0, 90], [900, 50, 0], True, 0), (4, 1, 256, [700], [700], False, 0),
+    (8, 2, 128, [1100], [1100], True, 300), (6, 1, 128, [900], [300], True, 0), (5, 1, 256, [640, 3], [700, 200], True, 70)])
+def test_gradients_of_few_keys(heads, kv, D, nq, nk, causal, window):
+    # The queries of a key are divided among workgroups; rows of no sequence stay.
+    from outlier_aware_bit_amd import qlin as q
+    log(f"prompt attention's gradients, divided {heads} {kv} {D} {nq} {nk} {causal} {window}")
+    c = Packed(31, nq, nk, heads, kv, D, causal, window, gap=3)
+    x, (out, lse) = _run(q, c)
+    Tq, Tk = c.q.shape[0], c.k.shape[0]
+    need = q.qlin_attn_prompt_backward_work_bytes(heads, kv, D, len(nq), Tq, Tk, causal, window)
+    assert need >= 2 * Tk * kv * D * 8
+    runs = []
+    for _ in range(2):
+        dkv = torch.full((Tk, 2 * kv, D), 7.0, dtype=torch.float16, device="cuda")
+        work = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN, if it were read
+        runs.append(q.qlin_attn_prompt_backward(strided(c.dout), *x, out, lse, dev(c.cu_q), dev(c.cu_k), scale=c.scale,
+                                                causal=causal, window=window, dk=dkv[:, :kv], dv=dkv[:, kv:], work=work))
+    want, tol = c.backward()
+    for name, g, again, w, t, cu in zip(("dq", "dk", "dv"), *runs, want, tol, (c.cu_q, c.cu_k, c.cu_k)):
+        assert torch.equal(g[cu[0]:cu[-1]], again[cu[0]:cu[-1]])
+        within(host(g)[cu[0]:cu[-1]], w[cu[0]:cu[-1]], t[cu[0]:cu[-1]], name)
+        if name != "dq":
+            assert bool((g[:cu[0]] == 7.0).all()) and bool((g[cu[-1]:] == 7.0).all())
 
 
 @pytest.mark.parametrize("D,nq,nk", [(256, [50], [6000]), (128, [1], [9000]), (64, [130, 7], [5000, 3001])])

@@ -27,7 +27,8 @@ class _Step:
         self.freq, _ = q.qlin_rope_freqs(D)
         self.work = torch.empty(max(16, q.qlin_attn_prompt_work_bytes(heads, kv_heads, D, B, T, T)), dtype=torch.uint8,
                                 device="cuda")
-        self.grad_work = torch.empty(q.qlin_attn_prompt_backward_work_bytes(heads, T), dtype=torch.uint8, device="cuda")
+        self.grad_work = torch.empty(q.qlin_attn_prompt_backward_work_bytes(heads, kv_heads, D, B, T, T), dtype=torch.uint8,
+                                     device="cuda")
         self.out = torch.zeros((T, heads, D), dtype=torch.float16, device="cuda")
         self.lse = torch.zeros((heads, T), device="cuda")
         self.grads = torch.zeros_like(self.qkv)

@@ -149,5 +149,13 @@ def test_workspace_sizes():
                 (4, 2, 128, 0, 10, 10, 1, 0), (4, 2, 128, 1, -1, 10, 1, 0), (4, 2, 128, 1, 10, 1 << 31, 1, 0),
                 (4, 2, 128, 1, 10, 10, 0, 5), (4, 2, 128, 1, 10, 10, 1, -5), (0, 0, 128, 1, 10, 10, 1, 0)):
         assert lib.qlin_attn_prompt_work_bytes(*bad) == 0
-    assert lib.qlin_attn_prompt_backward_work_bytes(4, 33) >= 2 * 4 * 33 * 4
-    assert lib.qlin_attn_prompt_backward_work_bytes(0, 33) == lib.qlin_attn_prompt_backward_work_bytes(4, -1) == 0
+        assert lib.qlin_attn_prompt_backward_work_bytes(*bad) == 0
+    # The gradients' statistics, and parts of dk and dv where the queries of a key are divided.
+    assert 2 * 4 * 33 * 4 <= lib.qlin_attn_prompt_backward_work_bytes(4, 2, 128, 1, 33, 33, 1, 0) < 2 * 4 * 48 * 4
+    assert lib.qlin_attn_prompt_backward_work_bytes(32, 8, 128, 4, 8192, 8192, 1, 0) == 2 * 32 * 8192 * 4
+    parts = lib.qlin_attn_prompt_backward_work_bytes(8, 1, 64, 1, 1000, 1000, 1, 0) - 2 * 8 * 1000 * 4
+    assert parts >= 2 * 1000 * 64 * 8 and parts % (1000 * 64 * 8) == 0
+    for window in (0, 2 ** 31 - 1):
+        assert lib.qlin_attn_prompt_backward_work_bytes(8, 1, 64, 1, 1000, 1000, 1, window) >= parts // 2
+    assert lib.qlin_attn_prompt_backward_work_bytes(1, 1, 64, 1, 1000, 1000, 1, 8) == 2 * 1000 * 4
+    assert lib.qlin_attn_prompt_work_bytes(16, 4, 256, 1, 500, 15500, 1, 2 ** 31 - 1) >= 2 * 16 * 500 * (256 * 4 + 8)
