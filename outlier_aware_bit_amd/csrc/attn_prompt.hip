@@ -338,9 +338,11 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
 // How many workgroups share a row's keys: as many as the GPU runs at once, each with
 // 512 keys or more of an average sequence.  500 queries after 15,000 keys, 32 heads
 // of 128 and of 64: 159 and 96 us, and 163 and 99 with two workgroups to a CU only;
-// 16 heads of 256: 158, and 783 undivided.  From 256 keys on, 2 x 40 queries after
-// 4,000 take 32 us where they take 34, and 512 after 512 take 34 instead of 33; from
-// 1,024 on, 51 and 30.
+// 16 heads of 256: 158, and 783 undivided.  Twice as many: 180 where this takes 144
+// (the last case), 78 where it takes 50 (3 x 1,500 tokens, 20 heads of 128).  From
+// 256 keys on, one prompt of 1,000 tokens with 8 heads takes 24 us instead of 27, and
+// 512 queries after 512 with 32 heads 34 instead of 30; from 1,024 on, 2 x 40 queries
+// after 4,000 take 51 instead of 34.
 int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
   const int64_t groups = (Tq / rows(head_dim) + B) * heads, room = 256 * beside(head_dim);
   int64_t each = Tk / B;

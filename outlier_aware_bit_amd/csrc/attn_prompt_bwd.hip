@@ -12,7 +12,8 @@
 //      delta and lse for the second kernel.
 //   2. dk, dv: a workgroup has 128 keys of one kv head, a lane one key, and goes
 //      over the queries of all its heads:  S = Q K^T,  dP = dO V^T,
-//      dV^T += dO^T P,  dK^T += Q^T dS.
+//      dV^T += dO^T P,  dK^T += Q^T dS.  (Few keys: several workgroups share the
+//      queries, and a third kernel adds their parts in order.)
 // As in the forward pass, P and dS leave one product in the registers where the
 // next takes them.
 //
@@ -680,13 +681,20 @@ __global__ __launch_bounds__(256) void prompt_grad_join_kernel(GradArgs a, int32
   }
 }
 
-// How many workgroups share a key tile's queries: as many as the GPU runs at once,
-// each with kLeast tiles of 64 queries or more of an average sequence.
+// How many workgroups share a key tile's queries: twice as many as the GPU runs at
+// once, the second beginning as the first end, each with kLeast tiles of 64 queries
+// or more of an average sequence.  One sequence of 1,000 tokens, 8 heads on 1: 56,
+// 72 and 131 us with 64, 128 and 256 channels, and 213, 265 and 463 undivided;
+// 2,000 tokens, 32 heads on 8: 211 and 309.  Twice against once: 4 x 1,024, 16 heads
+// of 256 on 4, 232 and 305; 3 x 1,500, 20 heads of 128 on 5, 191 and 254; elsewhere
+// the same; three or four times cost as often as they gain (8 x 1,000, 8 heads of
+// 64: 105 and 83).  Two tiles instead of four: 61 on the first case, 76 on the
+// second, 33 instead of 38 on 8 x 128 tokens; eight: 65, 83 and 47.
 constexpr int kLeast = 4;
 int grad_splits(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t causal,
                 int32_t window) {
   if (Tk == 0 || B == 0) return 1;
-  const int64_t groups = (Tk / kRows + B) * kv_heads, room = 256 * (head_dim == 64 ? 2 : 1);
+  const int64_t groups = (Tk / kRows + B) * kv_heads, room = 512 * (head_dim == 64 ? 2 : 1);
   int64_t each = Tq / B;  // queries of a key tile
   if (window > 0 && int64_t{window} + kRows < each)
     each = window + kRows;
