@@ -18,11 +18,11 @@
 // next takes them.
 //
 // Bound by the waits between products, vector work and LDS of the few waves that
-// the registers of two operands and two sums allow: matrix units are busy 40 - 45 %
+// the registers of two operands and two sums allow: matrix units are busy 37 - 45 %
 // of the cycles.  Four sequences of 2,048 tokens, 32 heads of 128 on 8, causal: dq
-// 228 us (3 products, 206 GFLOP: 903 TFLOP/s), dk and dv 311 (4 products, 275 GFLOP:
-// 885).  Twelve texts of 60 - 3,001 tokens, 40 heads of 64 on 8, a window of 1,000:
-// 281 and 357 us, vector units busy 57 and 47 %.
+// 231 us (3 products, 206 GFLOP: 892 TFLOP/s), dk and dv 318 (4 products, 275 GFLOP:
+// 865).  Twelve texts of 60 - 3,001 tokens, 40 heads of 64 on 8, a window of 1,000:
+// 283 and 378 us, vector units busy 57 and 43 %.
 #include <math.h>
 
 #include "prompt.hpp"

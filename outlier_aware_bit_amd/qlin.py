@@ -995,8 +995,9 @@ def qlin_attn_prompt_backward(dout, q, k, v, out, lse, cu_q, cu_k=None, scale=No
     ld_do = _heads3(dout, "dout", D, index)[2]
     out_p = _same(out, "out", torch.float16, q.shape, index)
     lse_p = _same(lse, "lse", torch.float32, (heads, Tq), index)
-    (dq, ld_dq), (dk, ld_dk), (dv, ld_dv) = (_grad(t, n, x, D, index) for t, n, x in
-                                             ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    dq, ld_dq = _grad(dq, "dq", q, D, index)
+    dk, ld_dk = _grad(dk, "dk", k, D, index)
+    dv, ld_dv = _grad(dv, "dv", v, D, index)
     if B == 0 or (Tq == 0 and Tk == 0):
         return dq, dk, dv
     if scale is None:
