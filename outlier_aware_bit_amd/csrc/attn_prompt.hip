@@ -316,16 +316,36 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
   // Rows of no sequence have no parts, and are left as they are.
   const int32_t begin = a.s.cu_q[0], end = a.s.cu_q[a.s.B];
   if (row < begin || row >= end) return;
-  float m = kNoRef;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * rows + at].x);
-  float l = 0.0f, o[8] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 p = a.part_ml[s * rows + at];
-    const float f = __builtin_amdgcn_exp2f(p.x - m);
-    l = __builtin_fmaf(p.y, f, l);
-    const float* x = a.part_o + ((s * rows + at) << d_shift) + c;
+  // Four parts' loads at a time, joined as they come: a wait for each would be most of
+  // the kernel's time.
+  constexpr int kAtOnce = 4;
+  float m = kNoRef, l = 0.0f, o[8] = {};
+  for (int s0 = 0; s0 < a.splits; s0 += kAtOnce) {
+    float2 p[kAtOnce];
+    v4f x[kAtOnce][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int64_t row_of = (s0 + j < a.splits ? s0 + j : s0) * rows + at;
+      p[j] = a.part_ml[row_of];
+      const v4f* from = reinterpret_cast<const v4f*>(a.part_o + (row_of << d_shift) + c);
+      x[j][0] = from[0], x[j][1] = from[1];
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) top = fmaxf(top, p[j].x);
+    const float keep = __builtin_amdgcn_exp2f(m - top);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= keep;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (s0 + j >= a.splits) break;
+      const float f = __builtin_amdgcn_exp2f(p[j].x - m);
+      l = __builtin_fmaf(p[j].y, f, l);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(x[j][i >> 2][i & 3], f, o[i]);
+    }
   }
   const float f = l == 0.0f ? 0.0f : 1.0f / l;
   const v4i w = {static_cast<int>(pack_half(o[0] * f, o[1] * f)), static_cast<int>(pack_half(o[2] * f, o[3] * f)),
@@ -336,19 +356,19 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, int32_t 
 }
 
 // How many workgroups share a row's keys: as many as the GPU runs at once, each with
-// 512 keys or more of an average sequence.  500 queries after 15,000 keys, 32 heads
+// 384 keys or more of an average sequence.  500 queries after 15,000 keys, 32 heads
 // of 128 and of 64: 159 and 96 us, and 163 and 99 with two workgroups to a CU only;
 // 16 heads of 256: 158, and 783 undivided.  Twice as many: 180 where this takes 144
 // (the last case), 78 where it takes 50 (3 x 1,500 tokens, 20 heads of 128).  From
-// 256 keys on, one prompt of 1,000 tokens with 8 heads takes 24 us instead of 27, and
-// 512 queries after 512 with 32 heads 34 instead of 30; from 1,024 on, 2 x 40 queries
-// after 4,000 take 51 instead of 34.
+// 256 keys on, 512 queries after 512, 32 heads of 128, take 33 us instead of 30, and
+// one prompt of 1,000 tokens, 8 heads of 256, 44 instead of 49; from 512 on, 59 the
+// latter; from 1,024 on, 2 x 40 queries after 4,000 take 51 instead of 31.
 int prompt_splits(int32_t heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t window) {
   const int64_t groups = (Tq / rows(head_dim) + B) * heads, room = 256 * beside(head_dim);
   int64_t each = Tk / B;
   if (window > 0 && int64_t{window} + rows(head_dim) < each) each = window + rows(head_dim);
   int64_t n = room / groups;
-  if (n > each / 512) n = each / 512;
+  if (n > each / 384) n = each / 384;
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 size_t prompt_work(int64_t rows, int32_t head_dim, int splits) {

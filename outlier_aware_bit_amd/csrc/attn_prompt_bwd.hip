@@ -670,6 +670,7 @@ __global__ __launch_bounds__(256) void prompt_grad_join_kernel(GradArgs a, int32
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float x[8] = {};
+#pragma unroll 4
     for (int y = 0; y < a.splits; ++y) {
       const float* p = a.parts + (2 * y + which) * all + at;
 #pragma unroll
@@ -683,13 +684,14 @@ __global__ __launch_bounds__(256) void prompt_grad_join_kernel(GradArgs a, int32
 
 // How many workgroups share a key tile's queries: twice as many as the GPU runs at
 // once, the second beginning as the first end, each with kLeast tiles of 64 queries
-// or more of an average sequence.  One sequence of 1,000 tokens, 8 heads on 1: 56,
-// 72 and 131 us with 64, 128 and 256 channels, and 213, 265 and 463 undivided;
+// or more of an average sequence.  One sequence of 1,000 tokens, 8 heads on 1: 51,
+// 66 and 123 us with 64, 128 and 256 channels, and 213, 265 and 463 undivided;
 // 2,000 tokens, 32 heads on 8: 211 and 309.  Twice against once: 4 x 1,024, 16 heads
 // of 256 on 4, 232 and 305; 3 x 1,500, 20 heads of 128 on 5, 191 and 254; elsewhere
 // the same; three or four times cost as often as they gain (8 x 1,000, 8 heads of
-// 64: 105 and 83).  Two tiles instead of four: 61 on the first case, 76 on the
-// second, 33 instead of 38 on 8 x 128 tokens; eight: 65, 83 and 47.
+// 64: 105 and 83).  Two tiles instead of four: 49 and 63 on the first cases, 31
+// instead of 38 on 8 x 128 tokens, 8 heads on 1, but 152 instead of 128 on 1,000
+// tokens, 16 heads of 256 on 4, and 61 instead of 53 on 4 x 300, 32 of 128 on 4.
 constexpr int kLeast = 4;
 int grad_splits(int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t B, int64_t Tq, int64_t Tk, int32_t causal,
                 int32_t window) {
