@@ -188,9 +188,9 @@ again:
           st[r] = j < span ? st[r] : -INFINITY;
         }
       }
-      float top = st[0];
+      float top = -INFINITY;
 #pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, st[r]);
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, st[r]);
       top = larger_half(top) * a.c;
       if (__any(top > m + kSlack)) {
         // Each query by itself: its bits do not depend on its neighbours'.
