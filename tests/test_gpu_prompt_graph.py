@@ -119,6 +119,56 @@ def test_two_streams_at_once():
             assert_equal(host(b).view(np.uint8), host(a).view(np.uint8), name)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_divided_calls_on_two_streams_and_replayed(D):
+    # Few heads of one long sequence: rows' keys and keys' queries are divided, workspaces hold the parts.
+    import torch
+    from outlier_aware_bit_amd import qlin as q
+    log(f"divided prompt attention on two streams and in a graph, D={D}")
+    T, heads = 900, 4
+    sizes = (heads, 1, D, 1, T, T, True, 0)
+    assert q.qlin_attn_prompt_work_bytes(*sizes) > 0
+    assert q.qlin_attn_prompt_backward_work_bytes(*sizes) >= 2 * T * D * 8
+    gen = torch.Generator().manual_seed(D)
+    cu = dev(np.array([0, T], np.int32))
+
+    def draw():
+        return [torch.randn((T, n, D), generator=gen).half().cuda() for n in (heads, 1, 1, heads)]
+
+    def step(qx, k, v, dout):
+        out, lse = q.qlin_attn_prompt(qx, k, v, cu, want_lse=True)
+        return (out, lse) + q.qlin_attn_prompt_backward(dout, qx, k, v, out, lse, cu)
+
+    def same(got, want, what):
+        for n, (a, b) in enumerate(zip(got, want)):
+            assert_equal(host(a).view(np.uint8), host(b).view(np.uint8), f"{what}, output {n}")
+
+    inputs = [draw() for _ in range(2)]
+    alone = [step(*x) for x in inputs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(3):
+        for n, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[n] = step(*inputs[n])
+    torch.cuda.synchronize()
+    for n in range(2):
+        same(got[n], alone[n], f"stream {n}")
+    held = [x.clone() for x in inputs[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = step(*held)
+    for i in range(4):
+        x = draw()
+        for a, b in zip(held, x):
+            a.copy_(b)
+        want = step(*x)
+        torch.randn(1 << 16, device="cuda").sum().item()  # unrelated work, synchronized
+        graph.replay()
+        torch.cuda.synchronize()
+        same(replayed, want, f"replay {i}")
+
+
 @pytest.fixture
 def calls():
     import torch
